@@ -16,6 +16,10 @@
  *   (fp8_gemm_dgrad_act     dgrad with the activation backward in its epilogue)
  *   (fp8_quant_mx,          MXFP8: 32-value blocks with power-of-two scales,
  *    fp8_gemm_mx             on the block-scaled tensor cores)
+ *   (layer_norm_fwd,        around the MLP, out = x + dropout(MLP(layer_norm(x))):
+ *    layer_norm_bwd,         the norm with the up-projection's quantize in its
+ *    dropout_fwd,            epilogue and the dropout + residual before it, and
+ *    dropout_bwd             the gradients)
  *
  * Conventions shared by every call:
  *  - All tensor pointers are DEVICE pointers to caller-owned memory; the
@@ -23,7 +27,8 @@
  *    enqueued on `stream` (0 = the legacy default stream) and the call returns
  *    as soon as it is enqueued.
  *  - Matrices are row-major and densely packed (leading dimension = number of
- *    columns).  Tensor pointers must be 16-byte aligned.
+ *    columns).  Tensor pointers must be 16-byte aligned.  (The layer norm and
+ *    dropout calls take row strides and need element alignment only.)
  *  - FP8 tensors are raw bytes (E4M3 "fn" variant: max 448, no infinity;
  *    E5M2: IEEE-like, max 57344).  BF16 tensors are raw 16-bit patterns.
  *  - Scales are multipliers: q = FP8(x * s); dequantisation divides by s.
@@ -621,6 +626,147 @@ int amax_history_update_ex(float* history, int L, int* head, const float* amax_n
                            float margin, int fmt, const float* scale_prev, float* scale_out,
                            int* status, float* amax_clear, unsigned long long* sat_clear,
                            cudaStream_t stream);
+
+/*
+ * Layer norm and dropout around the MLP
+ *
+ * One sub-layer is  out = x + dropout(MLP(layer_norm(x))).  Element types are
+ * fp8q_dtype; every [M,N] tensor of a call has the same type, rows of N
+ * adjacent elements and its own row stride (ld >= N, in elements); pointers
+ * are aligned to the element.  0 <= M <= FP8Q_NORM_MAX, 1 <= N <=
+ * FP8Q_NORM_MAX.  An [M,N] output may be one of the [M,N] inputs (the same
+ * pointer and row stride: each element is read before it is written); apart
+ * from that the tensors must not overlap.  Rows whose pointers and row strides
+ * (in bytes) are multiples of 16 are moved in 16-byte pieces, others element
+ * by element.
+ *
+ * Dropout masks are never stored.  rng points to 16 bytes of device memory:
+ * a 64-bit seed and a 64-bit offset.  Element (i, j) is dropped when word
+ * j % 4 of Philox4x32-10 (Salmon, Moraes, Dror, Shaw, "Parallel random
+ * numbers: as easy as 1, 2, 3", SC 2011) at the counter (j / 4, i, offset low
+ * half, offset high half) under the key (seed low half, seed high half) is
+ * below round(p * 2^32) (half to even).  So the mask depends on seed, offset,
+ * row and column alone; a backward call given the forward's rng forms the
+ * forward's mask; a program gives every layer and step an offset of its own,
+ * and a captured graph takes new ones by writing to rng between replays.
+ * 0 <= p <= 1; a p that rounds to no word drops nothing and needs no rng.
+ * inv below is float32(1 / (1 - p)), 0 for p = 1.  A dropped element counts
+ * as 0 whatever it holds.
+ */
+typedef enum { FP8Q_BF16 = 0, FP8Q_FP16 = 1, FP8Q_FP32 = 2 } fp8q_dtype;
+
+#define FP8Q_NORM_MAX 2147483647LL /* largest M and N of the layer norm and dropout calls */
+
+/*
+ * layer_norm_fwd -- [dropout + residual +] layer norm [+ FP8 cast]
+ *
+ *     d    = keep ? float32(x * inv) : 0             (x itself without dropout)
+ *     r    = T(float32(residual + d))                -> r_out
+ *     mean = sum_j r / N                             -> mean[i]
+ *     rstd = 1 / sqrt(sum_j (r - mean)^2 / N + eps)  -> rstd[i]
+ *     y    = T((r - mean) * rstd * weight + bias)    -> y
+ *     v    = float32(y * *scale);  q = FP8(v)        -> q_out  (as fp8_quant_fused)
+ *     amax_out = max |y|;  sat_count = #{ |v| > format max }
+ *
+ * The norm is that of the stored r (rounded to T; r = x without residual and
+ * dropout).  Sums are float32.  An infinity or NaN in a row gives NaNs in that
+ * row alone (and a NaN amax, which the history update reports).
+ *   dtype, param_dtype  x, residual, r_out, y;  weight and bias: FP8Q_FP32 or
+ *                       dtype, [N] each, NULL for 1 and 0.
+ *   x                   required unless M == 0.
+ *   residual            NULL: none.
+ *   r_out               NULL: r is not kept (layer_norm_bwd needs it).
+ *   y                   may be NULL when q_out is given (nothing but the codes).
+ *   mean, rstd          device [M] float, or NULL.
+ *   eps                 finite, >= 0.
+ *   q_out               device [M,N] FP8, densely packed, or NULL; fmt, scale:
+ *                       its fp8q_format and device scale (required with
+ *                       q_out, amax_out or sat_count).
+ *   amax_out, sat_count device float / uint64 or NULL; zeroed by this call
+ *                       unless flags has FP8Q_ACCUMULATE.
+ * Zero the struct and set what the call needs.
+ */
+typedef struct {
+    int64_t M, N;
+    int dtype, param_dtype;
+    const void* x;        int64_t ldx;
+    const void* residual; int64_t ld_residual;
+    void* r_out;          int64_t ld_r;
+    const void* weight;
+    const void* bias;
+    void* y;              int64_t ldy;
+    float* mean;
+    float* rstd;
+    double p;
+    const uint64_t* rng;
+    const float* scale;
+    void* q_out;
+    float* amax_out;
+    unsigned long long* sat_count;
+    float eps;
+    int fmt;
+    unsigned flags;
+} fp8q_layer_norm_args;
+
+int layer_norm_fwd(const fp8q_layer_norm_args* args, cudaStream_t stream);
+
+/*
+ * layer_norm_bwd -- gradient of layer_norm_fwd
+ *
+ * From dy (the gradient of y), the stored r, mean and rstd; xhat = (r - mean) *
+ * rstd, g = dy * weight, all in float32:
+ *     dr      = rstd * (g - sum_j g / N - xhat * sum_j (g * xhat) / N) + dresidual
+ *     dx      = T(dr)                               gradient of r and of residual
+ *     dbranch = keep ? T(float32(dr * inv)) : 0     gradient of x
+ *     dweight = sum_i dy * xhat,  dbias = sum_i dy  float32
+ * dweight and dbias are summed in a fixed order (which depends on M, N, the
+ * tensors' alignment and the device): the same call gives the same bits.
+ *   dresidual      gradient that reaches r on its other way, or NULL.
+ *   dbranch        NULL: not wanted.  With p = 0 it is T(dr).
+ *   weight         NULL: 1.
+ *   dweight, dbias device [N] float, or NULL; FP8Q_ACCUMULATE in flags adds to
+ *                  them.  M == 0 without it zeroes them.
+ *   workspace      device, 16-byte aligned, layer_norm_bwd_workspace_bytes(M, N)
+ *                  bytes; its contents need no preparation.  Required with
+ *                  dweight or dbias (unless M == 0).
+ */
+typedef struct {
+    int64_t M, N;
+    int dtype, param_dtype;
+    const void* dy;        int64_t ld_dy;
+    const void* r;         int64_t ld_r;
+    const float* mean;
+    const float* rstd;
+    const void* weight;
+    const void* dresidual; int64_t ld_dresidual;
+    void* dx;              int64_t ld_dx;
+    void* dbranch;         int64_t ld_dbranch;
+    double p;
+    const uint64_t* rng;
+    float* dweight;
+    float* dbias;
+    void* workspace;
+    size_t workspace_bytes;
+    unsigned flags;
+} fp8q_layer_norm_bwd_args;
+
+int layer_norm_bwd(const fp8q_layer_norm_bwd_args* args, cudaStream_t stream);
+
+/* Bytes of layer_norm_bwd's workspace: at most 1024 partial rows of 2 N floats
+ * (at most 8192 N).  0 for sizes that the call refuses and for M == 0. */
+size_t layer_norm_bwd_workspace_bytes(int64_t M, int64_t N);
+
+/*
+ * dropout_fwd -- y = T(float32(residual + (keep ? float32(x * inv) : 0)))
+ * (residual NULL: T(keep ? float32(x * inv) : 0)).
+ */
+int dropout_fwd(const void* x, int64_t ldx, const void* residual, int64_t ld_residual, void* y, int64_t ldy,
+                int64_t M, int64_t N, int dtype, double p, const uint64_t* rng, cudaStream_t stream);
+
+/* dropout_bwd -- dx = keep ? T(float32(dy * inv)) : 0, the gradient of
+ * dropout_fwd's x (the residual's is dy itself). */
+int dropout_bwd(const void* dy, int64_t ld_dy, void* dx, int64_t ld_dx, int64_t M, int64_t N, int dtype, double p,
+                const uint64_t* rng, cudaStream_t stream);
 
 /* Human-readable name of an fp8q_status value (static string). */
 const char* fp8q_status_string(int status);

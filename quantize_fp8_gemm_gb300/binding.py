@@ -23,6 +23,7 @@ ACT_IDENTITY, ACT_RELU, ACT_RELU2 = 0, 1, 2
 DEV_TIMEOUT, DEV_BAD_AMAX = 1, 2
 ACCUMULATE = 1  # fp8_quant_fused_ex flag
 BATCH_MAX = 4  # FP8Q_BATCH_MAX
+BF16, FP16, FP32 = 0, 1, 2  # fp8q_dtype
 GROUP = 128
 NOALLOC_MAX_M = 262144  # FP8Q_NOALLOC_MAX_M
 
@@ -88,9 +89,16 @@ def lib() -> ctypes.CDLL:
         L.fp8_gemm_mx.argtypes = [P, P, P, P, P, i64, i64, i64, i32, i32, P, P]
         L.fp8_mx_scale_bytes.argtypes = [i64, i64]
         L.fp8_mx_scale_bytes.restype = i64
+        L.layer_norm_fwd.argtypes = [P, P]
+        L.layer_norm_bwd.argtypes = [P, P]
+        L.layer_norm_bwd_workspace_bytes.argtypes = [i64, i64]
+        L.layer_norm_bwd_workspace_bytes.restype = ctypes.c_size_t
+        L.dropout_fwd.argtypes = [P, i64, P, i64, P, i64, i64, i64, i32, ctypes.c_double, P, P]
+        L.dropout_bwd.argtypes = [P, i64, P, i64, i64, i64, i32, ctypes.c_double, P, P]
         for fn in ("fp8_quant_fused", "fp8_quant_fused_ex", "fp8_quant_fused_batch", "fp8_downproj_fwd",
                    "fp8_downproj_fwd_noalloc", "fp8_downproj_fwd_ex", "fp8_gemm_fwd", "fp8_gemm_fwd_update", "fp8_gemm_dgrad", "fp8_gemm_wgrad", "fp8_gemm_dgrad_act", "fp8_gemm_dgrad_act_q", "fp8_upproj_fwd", "amax_history_update",
-                   "amax_history_update_ex", "fp8_quant_mx", "fp8_gemm_mx"):
+                   "amax_history_update_ex", "fp8_quant_mx", "fp8_gemm_mx", "layer_norm_fwd", "layer_norm_bwd",
+                   "dropout_fwd", "dropout_bwd"):
             getattr(L, fn).restype = i32
         _lib = L
     return _lib
@@ -456,6 +464,159 @@ def amax_history_update_ex(history: torch.Tensor, head: torch.Tensor, amax_new: 
         _ptr(status, 4, "status"), _ptr(amax_clear, 4, "amax_clear"), _ptr(sat_clear, 8, "sat_clear"),
         _stream(stream))
     _check("amax_history_update_ex", st)
+
+
+# -- layer norm and dropout around the MLP --
+_DTYPES = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}
+
+
+class LayerNormArgs(ctypes.Structure):
+    """fp8q_layer_norm_args."""
+    _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int64), ("dtype", ctypes.c_int), ("param_dtype", ctypes.c_int),
+                ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("residual", ctypes.c_void_p),
+                ("ld_residual", ctypes.c_int64), ("r_out", ctypes.c_void_p), ("ld_r", ctypes.c_int64),
+                ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64),
+                ("mean", ctypes.c_void_p), ("rstd", ctypes.c_void_p), ("p", ctypes.c_double), ("rng", ctypes.c_void_p),
+                ("scale", ctypes.c_void_p), ("q_out", ctypes.c_void_p), ("amax_out", ctypes.c_void_p),
+                ("sat_count", ctypes.c_void_p), ("eps", ctypes.c_float), ("fmt", ctypes.c_int),
+                ("flags", ctypes.c_uint)]
+
+
+class LayerNormBwdArgs(ctypes.Structure):
+    """fp8q_layer_norm_bwd_args."""
+    _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int64), ("dtype", ctypes.c_int), ("param_dtype", ctypes.c_int),
+                ("dy", ctypes.c_void_p), ("ld_dy", ctypes.c_int64), ("r", ctypes.c_void_p), ("ld_r", ctypes.c_int64),
+                ("mean", ctypes.c_void_p), ("rstd", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("dresidual", ctypes.c_void_p), ("ld_dresidual", ctypes.c_int64), ("dx", ctypes.c_void_p),
+                ("ld_dx", ctypes.c_int64), ("dbranch", ctypes.c_void_p), ("ld_dbranch", ctypes.c_int64),
+                ("p", ctypes.c_double), ("rng", ctypes.c_void_p), ("dweight", ctypes.c_void_p),
+                ("dbias", ctypes.c_void_p), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+                ("flags", ctypes.c_uint)]
+
+
+def _dtype_code(t, name: str) -> int:
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise TypeError(f"{name} must be a 2-dimensional CUDA tensor")
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be bfloat16, float16 or float32, not {t.dtype}")
+    return code
+
+
+def _rows(t, like, name: str):
+    """(device pointer, row stride) of an optional [M,N] CUDA tensor of like's shape and type whose
+    rows are N adjacent elements."""
+    if t is None:
+        return None, 0
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != like.dtype:
+        raise TypeError(f"{name} must be {like.dtype}, not {t.dtype}")
+    if t.shape != like.shape:
+        raise ValueError(f"{name} is {list(t.shape)}, the call needs {list(like.shape)}")
+    M, N = like.shape
+    ld, inner = t.stride()
+    if M <= 1:
+        ld = N
+    if (inner != 1 and N > 1) or ld < N:
+        raise ValueError(f"{name} needs rows of adjacent elements that do not overlap (strides {tuple(t.stride())})")
+    return t.data_ptr(), ld
+
+
+def _vec(t, n: int, dtype, name: str):
+    """Device pointer of an optional packed CUDA vector of n elements of one type."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must hold {n} packed elements")
+    return t.data_ptr()
+
+
+def _rng(t):
+    """Device pointer of the generator state: int64 (seed, offset)."""
+    return _vec(t, 2, torch.int64, "rng")
+
+
+def _param_code(x, weight, bias, code: int):
+    """(param_dtype, its torch type) of the weight and bias: float32, or x's type."""
+    t = weight if weight is not None else bias
+    if t is None or not isinstance(t, torch.Tensor) or t.dtype == torch.float32:
+        return FP32, torch.float32
+    return code, x.dtype
+
+
+def layer_norm_fwd(x: torch.Tensor, weight, bias, y, *, eps: float = 1e-5, mean=None, rstd=None, residual=None,
+                   r_out=None, p: float = 0.0, rng=None, fmt: int = E4M3, scale=None, q_out=None, amax_out=None,
+                   sat_count=None, flags: int = 0, stream=None) -> None:
+    """y = layer_norm(r) * weight + bias of the rows of r = residual + dropout(x) (r = x without either),
+    and optionally r_out, the float32 statistics [M], and the FP8 codes q_out [M,N] of y under `scale`
+    with amax_out and sat_count.  x, residual, r_out, y: [M,N] bfloat16, float16 or float32 with any row
+    stride; weight, bias: [N] float32 or x's type, or None; rng: int64 (seed, offset) on the device."""
+    code = _dtype_code(x, "x")
+    M, N = x.shape
+    px, ldx = _rows(x, x, "x")
+    pres, ldres = _rows(residual, x, "residual")
+    pr, ldr = _rows(r_out, x, "r_out")
+    py, ldy = _rows(y, x, "y")
+    pcode, ptype = _param_code(x, weight, bias, code)
+    if q_out is not None and (q_out.element_size() != 1 or q_out.numel() != M * N):
+        raise ValueError(f"q_out must hold {M * N} one-byte codes")
+    a = LayerNormArgs(
+        M, N, code, pcode, px, ldx, pres, ldres, pr, ldr, _vec(weight, N, ptype, "weight"), _vec(bias, N, ptype, "bias"),
+        py, ldy, _vec(mean, M, torch.float32, "mean"), _vec(rstd, M, torch.float32, "rstd"), p, _rng(rng),
+        _ptr(scale, 4, "scale"), _ptr(q_out, M * N, "q_out"), _ptr(amax_out, 4, "amax_out"),
+        _ptr(sat_count, 8, "sat_count"), eps, fmt, flags)
+    _check("layer_norm_fwd", lib().layer_norm_fwd(ctypes.byref(a), _stream(stream)))
+
+
+def layer_norm_bwd_workspace_bytes(M: int, N: int) -> int:
+    return int(lib().layer_norm_bwd_workspace_bytes(int(M), int(N)))
+
+
+def layer_norm_bwd(dy: torch.Tensor, r: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor, weight,
+                   dx: torch.Tensor, *, dresidual=None, dweight=None, dbias=None, workspace=None, p: float = 0.0,
+                   rng=None, dbranch=None, flags: int = 0, stream=None) -> None:
+    """Gradient of layer_norm_fwd from dy, the stored r and the statistics: dx (of r and the residual,
+    with dresidual added), dbranch (of the x that went through dropout) and the float32 column sums
+    dweight and dbias, which need a workspace of layer_norm_bwd_workspace_bytes(M, N) bytes."""
+    code = _dtype_code(dy, "dy")
+    M, N = dy.shape
+    pdy, lddy = _rows(dy, dy, "dy")
+    pr, ldr = _rows(r, dy, "r")
+    pdres, lddres = _rows(dresidual, dy, "dresidual")
+    pdx, lddx = _rows(dx, dy, "dx")
+    pdb, lddb = _rows(dbranch, dy, "dbranch")
+    pcode, ptype = _param_code(dy, weight, None, code)
+    a = LayerNormBwdArgs(
+        M, N, code, pcode, pdy, lddy, pr, ldr, _vec(mean, M, torch.float32, "mean"),
+        _vec(rstd, M, torch.float32, "rstd"), _vec(weight, N, ptype, "weight"), pdres, lddres, pdx, lddx, pdb, lddb,
+        p, _rng(rng), _vec(dweight, N, torch.float32, "dweight"), _vec(dbias, N, torch.float32, "dbias"),
+        _ptr(workspace, None, "workspace"), 0 if workspace is None else workspace.numel() * workspace.element_size(),
+        flags)
+    _check("layer_norm_bwd", lib().layer_norm_bwd(ctypes.byref(a), _stream(stream)))
+
+
+def dropout_fwd(x: torch.Tensor, y: torch.Tensor, p: float, rng, *, residual=None, stream=None) -> None:
+    """y = residual + dropout(x) (y = dropout(x) without a residual), [M,N]; rng: int64 (seed, offset)."""
+    code = _dtype_code(x, "x")
+    M, N = x.shape
+    px, ldx = _rows(x, x, "x")
+    py, ldy = _rows(y, x, "y")
+    pres, ldres = _rows(residual, x, "residual")
+    _check("dropout_fwd", lib().dropout_fwd(px, ldx, pres, ldres, py, ldy, M, N, code, p, _rng(rng), _stream(stream)))
+
+
+def dropout_bwd(dy: torch.Tensor, dx: torch.Tensor, p: float, rng, *, stream=None) -> None:
+    """dx = the gradient of dropout_fwd's x under the same p and rng (the residual's gradient is dy)."""
+    code = _dtype_code(dy, "dy")
+    M, N = dy.shape
+    pdy, lddy = _rows(dy, dy, "dy")
+    pdx, lddx = _rows(dx, dy, "dx")
+    _check("dropout_bwd", lib().dropout_bwd(pdy, lddy, pdx, lddx, M, N, code, p, _rng(rng), _stream(stream)))
 
 
 # -- the unfused three-pass comparator (include/fp8q_naive.h, libfp8q_naive.so) --

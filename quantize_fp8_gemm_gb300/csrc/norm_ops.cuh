@@ -1,0 +1,156 @@
+// norm_ops.cuh -- element types, the counter-based generator and the quantize
+// epilogue shared by the layer norm (norm_fwd.cu, norm_bwd.cu) and dropout
+// (dropout.cu) kernels.
+#pragma once
+
+#include "common.cuh"
+#include "quant_ops.cuh"
+
+namespace fp8q {
+
+// ------------------------------------------------------------ element types --
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+// Round to nearest even; a half-precision overflow gives infinity.
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// The float32 value of v rounded to T.
+template <typename T>
+__device__ __forceinline__ float round_to(float v) { return to_f32(from_f32<T>(v)); }
+
+// A parameter vector of either type: float32, or the activations' type T.
+template <typename T>
+struct Params {
+    const void* p;  // NULL: every value is `none`
+    bool f32;
+    float none;
+    __device__ __forceinline__ float at(int64_t j) const {
+        if (p == nullptr) return none;
+        return f32 ? static_cast<const float*>(p)[j] : to_f32(static_cast<const T*>(p)[j]);
+    }
+};
+
+// ----------------------------------------------------------------- dropout --
+// Philox4x32-10 (J. Salmon, M. Moraes, R. Dror, D. Shaw, "Parallel random
+// numbers: as easy as 1, 2, 3", SC 2011): ten rounds of two 32 x 32 -> 64 bit
+// products over a 128-bit counter under a 64-bit key that grows by a constant
+// each round.  The key is the seed; the counter is (column / 4, row, offset
+// low, offset high), so a block gives the four words of columns 4j .. 4j + 3
+// of one row, and the mask depends on seed, offset, row and column alone:
+// not on the element type, the strides, the launch shape or the kernel.
+struct Philox {
+    uint32_t k0, k1, o0, o1;
+    __device__ __forceinline__ explicit Philox(const uint64_t* rng) {
+        const uint64_t seed = rng[0], off = rng[1];
+        k0 = static_cast<uint32_t>(seed);
+        k1 = static_cast<uint32_t>(seed >> 32);
+        o0 = static_cast<uint32_t>(off);
+        o1 = static_cast<uint32_t>(off >> 32);
+    }
+    __device__ __forceinline__ uint4 block(uint32_t quad, uint32_t row) const {
+        uint32_t c0 = quad, c1 = row, c2 = o0, c3 = o1, a = k0, b = k1;
+#pragma unroll
+        for (int i = 0; i < 10; ++i) {
+            const uint64_t p0 = static_cast<uint64_t>(0xD2511F53u) * c0;
+            const uint64_t p1 = static_cast<uint64_t>(0xCD9E8D57u) * c2;
+            c0 = static_cast<uint32_t>(p1 >> 32) ^ c1 ^ a;
+            c2 = static_cast<uint32_t>(p0 >> 32) ^ c3 ^ b;
+            c1 = static_cast<uint32_t>(p1);
+            c3 = static_cast<uint32_t>(p0);
+            a += 0x9E3779B9u;
+            b += 0xBB67AE85u;
+        }
+        return make_uint4(c0, c1, c2, c3);
+    }
+};
+
+// Drop probability as the kernels use it.  An element is dropped when its word
+// is <= last (= round(p 2^32) - 1), i.e. below round(p 2^32); p that rounds to
+// no word at all runs without a generator (on = false).
+struct Dropout {
+    const uint64_t* rng;
+    uint32_t last;
+    float inv;  // float32(1 / (1 - p)); 0 for p = 1, where every element is dropped
+    bool on;
+};
+
+// Host: false if p is not in [0, 1].
+inline bool make_dropout(double p, const void* rng, Dropout* d) {
+    if (!(p >= 0.0 && p <= 1.0)) return false;
+    const double words = p * 4294967296.0;
+    uint64_t n = static_cast<uint64_t>(words);  // round half to even, as the documented formula rounds
+    const double rest = words - static_cast<double>(n);
+    if (rest > 0.5 || (rest == 0.5 && (n & 1u))) ++n;
+    d->rng = static_cast<const uint64_t*>(rng);
+    d->on = n > 0;
+    d->last = n > 0 ? static_cast<uint32_t>(n - 1) : 0u;
+    d->inv = p < 1.0 ? static_cast<float>(1.0 / (1.0 - p)) : 0.0f;
+    return true;
+}
+
+__device__ __forceinline__ uint32_t word_of(uint4 w, int i) {
+    return i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w;
+}
+
+// keep ? x * inv : 0.  A dropped element is 0 whatever x holds.
+__device__ __forceinline__ float dropped(float x, uint32_t word, const Dropout& d) {
+    return word > d.last ? __fmul_rn(x, d.inv) : 0.0f;
+}
+
+// -------------------------------------------------------- quantize epilogue --
+// The framework's cast of the rounded output: v = y * s, q = FP8(v), max |y|
+// (as float32 bits: those of non-negative floats order like the values, and a
+// NaN orders above infinity, as in the quantize kernels), #{|v| > max}.
+struct QuantOut {
+    const float* scale;
+    uint8_t* q;
+    float* amax;
+    unsigned long long* sat;
+    int fmt;
+    bool on;
+};
+
+__device__ __forceinline__ uint16_t cast_pair(float v0, float v1, int fmt) {
+    return fmt == FP8Q_E5M2 ? cvt_fp8x2<FP8Q_E5M2>(v0, v1) : cvt_fp8x2<FP8Q_E4M3>(v0, v1);
+}
+
+// Zeroes the accumulators of a call that does not accumulate.  One launch for
+// both words, and one the next kernel's launch overlaps.
+__global__ void clear_quant_kernel(float* amax, unsigned long long* sat);
+
+inline bool is_dtype(int t) { return t == FP8Q_BF16 || t == FP8Q_FP16 || t == FP8Q_FP32; }
+inline size_t dtype_size(int t) { return t == FP8Q_FP32 ? 4 : 2; }
+inline bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// Sum over the CTA's threads of two values, in every thread; the order of the
+// additions depends on blockDim.x alone.  `s` holds 2 * 32 + 2 floats.
+__device__ __forceinline__ float2 block_sum2(float a, float b, float* s) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = (blockDim.x + 31) >> 5;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+        b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+    }
+    __syncthreads();  // the previous sum's readers are done with s
+    if (lane == 0) { s[warp] = a; s[32 + warp] = b; }
+    __syncthreads();
+    a = lane < nw ? s[lane] : 0.0f;
+    b = lane < nw ? s[32 + lane] : 0.0f;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+        b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+    }
+    return make_float2(a, b);
+}
+
+}  // namespace fp8q
