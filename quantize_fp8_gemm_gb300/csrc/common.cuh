@@ -128,6 +128,10 @@ __device__ __forceinline__ void st_stream_v4(void* p, uint4 v) {
 __device__ __forceinline__ void cp_async16(uint32_t smem_addr, const void* gmem) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(smem_addr), "l"(gmem) : "memory");
 }
+// The same, or 16 zero bytes without reading gmem.
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t smem_addr, const void* gmem, bool read) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(smem_addr), "l"(gmem), "r"(read ? 16u : 0u) : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // Wait until at most N of this thread's committed groups are still in flight.
 template <int N>

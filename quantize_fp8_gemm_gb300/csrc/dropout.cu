@@ -48,11 +48,88 @@ __global__ void __launch_bounds__(256) dropout_quad_kernel(const DropParams<T> p
     pdl_launch_dependents();
 }
 
+// Division of n < 2^31 by a fixed d >= 1 as a product: n / d = (n * m) >> (31 + s)
+// with s = ceil(log2 d), m = ceil(2^(31 + s) / d) (below 2^32); the excess
+// n * (m d - 2^(31 + s)) / (d 2^(31 + s)) is below n / 2^31 / d < 1 / d, so
+// the quotient is exact.
+struct FastDiv {
+    uint32_t m;
+    int s;
+    __host__ explicit FastDiv(uint32_t d) : s(31) {
+        while ((1u << (s - 31)) < d) ++s;
+        m = static_cast<uint32_t>(((uint64_t(1) << s) + d - 1) / d);
+    }
+    __device__ __forceinline__ uint32_t div(uint32_t n) const {
+        return static_cast<uint32_t>((static_cast<uint64_t>(n) * m) >> s);
+    }
+};
+
+// Rows on the 16-byte grid: a thread takes U 16-byte pieces, loads first.
+template <typename T, int U, bool RES>
+__global__ void __launch_bounds__(256) dropout_piece_kernel(const DropParams<T> p, uint32_t total, uint32_t per_row,
+                                                            const FastDiv div) {
+    constexpr int V = 16 / sizeof(T);
+    pdl_wait();
+    const uint32_t first = blockIdx.x * (256u * U) + threadIdx.x;
+    Piece<T, V> x[U], r[U];
+    uint32_t row[U], k[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const uint32_t i = first + u * 256u;
+        row[u] = div.div(i);
+        k[u] = i - row[u] * per_row;
+        if (i < total) x[u].load(p.x + static_cast<int64_t>(row[u]) * p.ldx + static_cast<int64_t>(k[u]) * V);
+    }
+    if constexpr (RES) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (first + u * 256u < total)
+                r[u].load(p.res + static_cast<int64_t>(row[u]) * p.ld_res + static_cast<int64_t>(k[u]) * V);
+    }
+    Philox g;
+    if (p.drop.on) g = Philox(p.drop.rng);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (first + u * 256u >= total) continue;
+        float v[V];
+        x[u].unpack(v);
+        if (p.drop.on) {
+            uint32_t w[V];
+            words_at<V>(g, k[u] * V, row[u], w);
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[i] = dropped(v[i], w[i], p.drop);
+        }
+        if constexpr (RES) {
+            float f[V];
+            r[u].unpack(f);
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[i] = __fadd_rn(f[i], v[i]);
+        }
+        x[u].pack(v);
+        x[u].store(p.y + static_cast<int64_t>(row[u]) * p.ldy + static_cast<int64_t>(k[u]) * V);
+    }
+    pdl_launch_dependents();
+}
+
 template <typename T>
 int launch_drop(const void* x, int64_t ldx, const void* res, int64_t ld_res, void* y, int64_t ldy, int64_t M, int64_t N,
                 const Dropout& drop, cudaStream_t stream) {
     const DropParams<T> p = {M, N, static_cast<const T*>(x), ldx, static_cast<const T*>(res), ld_res,
                              static_cast<T*>(y), ldy, drop};
+    constexpr int V = 16 / sizeof(T), U = 2;
+    if (N % V == 0 && rows16(x, ldx, sizeof(T)) && rows16(res, ld_res, sizeof(T)) && rows16(y, ldy, sizeof(T)) &&
+        N / V < (int64_t(1) << 31) / M) {
+        const uint32_t per_row = static_cast<uint32_t>(N / V), total = per_row * static_cast<uint32_t>(M);
+        const dim3 grid((total + 256 * U - 1) / (256 * U));
+        const FastDiv div(per_row);
+        if ((res ? launch_pdl(dropout_piece_kernel<T, U, true>, grid, dim3(256), 0, stream, p, total, per_row, div)
+                 : launch_pdl(dropout_piece_kernel<T, U, false>, grid, dim3(256), 0, stream, p, total, per_row, div)) !=
+            cudaSuccess) {
+            (void)cudaGetLastError();
+            return FP8Q_ERR_CUDA;
+        }
+        return FP8Q_OK;
+    }
     const int64_t want = ((N + 3) / 4 * M + 255) / 256;
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>(want, int64_t(sm_count()) * 64));
     if (launch_pdl(dropout_quad_kernel<T>, dim3(grid), dim3(256), 0, stream, p) != cudaSuccess) {

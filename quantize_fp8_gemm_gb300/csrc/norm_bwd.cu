@@ -12,6 +12,7 @@
 #include "norm_ops.cuh"
 
 #include <algorithm>
+#include <atomic>
 
 namespace fp8q {
 
@@ -97,35 +98,326 @@ __global__ void __launch_bounds__(256) ln_bwd_cols_kernel(const BwdParams<T> p) 
     pdl_launch_dependents();
 }
 
-// dweight / dbias = the partial rows' sums, in the order of the parts.  A warp
-// of a block takes 32 columns of every eighth part; the eight sums are added in order.
-__global__ void __launch_bounds__(256) ln_bwd_reduce_kernel(const float* part, int parts, int64_t N, float* dweight,
-                                                            float* dbias, bool accumulate) {
-    __shared__ float s[8][32];
+// dweight / dbias = the partial rows' sums in a fixed order.  A block takes 32
+// columns; warp k of its 32 adds parts k, k + 32, ..., then the warps' sums are
+// added in order.
+__global__ void __launch_bounds__(1024) ln_bwd_reduce_kernel(const float* part, int parts, int64_t N, float* dweight,
+                                                             float* dbias, bool accumulate) {
+    __shared__ float s[32][33];
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t j = static_cast<int64_t>(blockIdx.x) * 32 + lane;  // column of [2][N]
     float sum = 0.0f;
-    if (j < 2 * N)
-        for (int k = warp; k < parts; k += 8) sum += part[static_cast<int64_t>(k) * 2 * N + j];
+    if (j < 2 * N) {
+#pragma unroll 4
+        for (int k = warp; k < parts; k += 32) sum += part[static_cast<int64_t>(k) * 2 * N + j];
+    }
     s[warp][lane] = sum;
     __syncthreads();
-    if (warp == 0 && j < 2 * N) {
-        sum = s[0][lane];
+    sum = s[lane][warp];  // column `warp` of the block
 #pragma unroll
-        for (int k = 1; k < 8; ++k) sum += s[k][lane];
-        float* out = j < N ? dweight : dbias;
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + warp;
+    if (lane == 0 && col < 2 * N) {
+        float* out = col < N ? dweight : dbias;
         if (out) {
-            out += j < N ? j : j - N;
+            out += col < N ? col : col - N;
             *out = accumulate ? *out + sum : sum;
         }
     }
     pdl_launch_dependents();
 }
 
-int loop_parts(int64_t M) { return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(64, M / 16))); }
+// One pass: every input is read once.  A thread keeps its C pieces' columns for
+// all the rows that its CTA takes (row blockIdx.x, + the grid, ...), so the
+// column sums stay in registers until the end.  16-byte pieces come through a
+// ring of kStages rows in shared memory, filled by cp.async: a thread copies
+// and reads its own pieces only, so it waits for its own copies and no barrier
+// guards the ring.  Single elements are loaded where they are used.
+enum RowsMode {
+    NARROW,  // `team` lanes (a power of two) take a row, 32 / team rows a warp, 4 warps
+    WIDE,    // a CTA of up to 512 threads takes a row
+    BROAD    // the same with up to 1024 threads, whose 64 registers hold no weights
+};
 
-int parts_of(int64_t M, int64_t) { return loop_parts(M); }
+// Rows of the ring: what a CTA's shared memory holds of its widest row.  A
+// stage is 48 C bytes a thread: 96 KB for 512 threads of C = 4, or 1024 of C = 2.
+constexpr int ring_stages(int V, int C, RowsMode mode) {
+    return V == 1 ? 0 : mode == BROAD ? (C == 4 ? 1 : 2) : mode == WIDE && C == 4 ? 2 : 3;
+}
+
+template <typename T, int V, int C, RowsMode MODE, bool DROP>
+__global__ void __launch_bounds__(MODE == NARROW ? 128 : MODE == WIDE ? 512 : 1024)
+ln_bwd_rows_kernel(const BwdParams<T> p, int team) {
+    extern __shared__ uint4 s_ring[];  // [stage][dy, r, dresidual][c][thread]
+    __shared__ float s_part[MODE == NARROW ? 2 * 32 * C * V : 1];
+    __shared__ float2 s_sum[2][32];
+    constexpr int S = ring_stages(V, C, MODE);
+    constexpr bool kHeld = V > 1 && MODE != BROAD;  // weights in registers
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    const int t = MODE == NARROW ? lane & (team - 1) : threadIdx.x;
+    const int span = MODE == NARROW ? team : blockDim.x;
+    const int pieces = static_cast<int>(p.N / V);
+    const float inv_n = 1.0f / static_cast<float>(p.N);
+    pdl_wait();
+
+    float w[kHeld ? C : 1][V], dw[C][V], db[C][V];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) dw[c][i] = db[c][i] = 0.0f;
+        if constexpr (kHeld) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) w[c][i] = 0.0f;
+            if (t + c * span < pieces) load_params<T, V>(p.w, static_cast<int64_t>(t + c * span) * V, w[c]);
+        }
+    }
+    Philox g;
+    if constexpr (DROP) g = Philox(p.drop.rng);
+
+    const int rows_warp = MODE == NARROW ? 32 / team : 1;
+    const int rows_cta = MODE == NARROW ? rows_warp * nw : 1;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * rows_cta;
+    const int64_t base0 = static_cast<int64_t>(blockIdx.x) * rows_cta;
+    const int64_t sub = MODE == NARROW ? warp * rows_warp + lane / team : 0;
+
+    // pieces past the row, and rows past the last, are zeros
+    auto slot = [&](int stage, int tensor, int c) {
+        return s_ring + ((stage * 3 + tensor) * C + c) * static_cast<int>(blockDim.x) + threadIdx.x;
+    };
+    auto fill = [&](int stage, int64_t row) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const bool in = row < p.M && t + c * span < pieces;
+            const int64_t j = static_cast<int64_t>(t + c * span) * V;
+            cp_async16_or_zero(smem_u32(slot(stage, 0, c)), in ? p.dy + row * p.ld_dy + j : p.dy, in);
+            cp_async16_or_zero(smem_u32(slot(stage, 1, c)), in ? p.r + row * p.ld_r + j : p.r, in);
+            if (p.dres) cp_async16_or_zero(smem_u32(slot(stage, 2, c)), in ? p.dres + row * p.ld_dres + j : p.dres, in);
+        }
+        cp_async_commit();
+    };
+    if constexpr (S > 0) {
+#pragma unroll
+        for (int k = 0; k < S - 1; ++k) fill(k, base0 + sub + k * stride);
+    }
+    float mean = base0 + sub < p.M ? p.mean[base0 + sub] : 0.0f;
+    float rstd = base0 + sub < p.M ? p.rstd[base0 + sub] : 0.0f;
+    int buf = 0, stage = 0;
+    for (int64_t base = base0; base < p.M; base += stride) {
+        const int64_t row = base + sub, ahead = row + stride;
+        const float mean_next = ahead < p.M ? p.mean[ahead] : 0.0f, rstd_next = ahead < p.M ? p.rstd[ahead] : 0.0f;
+        Piece<T, V> dyp[V == 1 ? C : 1], rp[V == 1 ? C : 1];
+        if constexpr (S > 0) {
+            fill(stage == 0 ? S - 1 : stage - 1, row + (S - 1) * stride);
+            cp_async_wait<S - 1>();
+        } else {
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const int k = t + c * span;
+                dyp[c].zero();
+                rp[c].zero();
+                if (row < p.M && k < pieces) {
+                    dyp[c].load(p.dy + row * p.ld_dy + k);
+                    rp[c].load(p.r + row * p.ld_r + k);
+                }
+            }
+        }
+        auto inputs = [&](int c, float (&dy)[V], float (&xhat)[V]) {
+            Piece<T, V> a, b;
+            if constexpr (S > 0) {
+                a.raw = *slot(stage, 0, c);
+                b.raw = *slot(stage, 1, c);
+            } else {
+                a = dyp[c];
+                b = rp[c];
+            }
+            a.unpack(dy);
+            b.unpack(xhat);
+#pragma unroll
+            for (int i = 0; i < V; ++i) xhat[i] = (xhat[i] - mean) * rstd;
+        };
+        auto weights = [&](int c, float (&v)[V]) {
+            if constexpr (kHeld) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) v[i] = w[c][i];
+            } else {
+                load_params<T, V>(p.w, static_cast<int64_t>(t + c * span) * V, v);
+            }
+        };
+        float c1 = 0.0f, c2 = 0.0f;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            if (t + c * span >= pieces) continue;
+            float dy[V], xhat[V], wc[V];
+            inputs(c, dy, xhat);
+            weights(c, wc);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float gi = dy[i] * wc[i];
+                c1 += gi;
+                c2 = __fmaf_rn(gi, xhat[i], c2);
+                dw[c][i] = __fmaf_rn(dy[i], xhat[i], dw[c][i]);
+                db[c][i] += dy[i];
+            }
+        }
+        const int width = MODE == NARROW ? team : 32;
+        for (int o = width / 2; o; o >>= 1) {
+            c1 += __shfl_xor_sync(0xFFFFFFFFu, c1, o);
+            c2 += __shfl_xor_sync(0xFFFFFFFFu, c2, o);
+        }
+        if constexpr (MODE != NARROW) {
+            // two buffers: a warp that runs ahead writes the other one, and cannot reach this one
+            // again before every warp has passed the next row's barrier
+            if (lane == 0) s_sum[buf][warp] = make_float2(c1, c2);
+            __syncthreads();
+            c1 = c2 = 0.0f;
+            for (int k = 0; k < nw; ++k) {
+                const float2 f = s_sum[buf][k];
+                c1 += f.x;
+                c2 += f.y;
+            }
+            buf ^= 1;
+        }
+        c1 *= inv_n;
+        c2 *= inv_n;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int k = t + c * span;
+            if (row >= p.M || k >= pieces) continue;
+            const int64_t j = static_cast<int64_t>(k) * V;
+            float d[V], xhat[V], wc[V];
+            inputs(c, d, xhat);
+            weights(c, wc);
+#pragma unroll
+            for (int i = 0; i < V; ++i) d[i] = rstd * (d[i] * wc[i] - c1 - xhat[i] * c2);
+            if (p.dres) {
+                Piece<T, V> a;
+                if constexpr (S > 0) a.raw = *slot(stage, 2, c);
+                else a.load(p.dres + row * p.ld_dres + k);
+                a.unpack(xhat);
+#pragma unroll
+                for (int i = 0; i < V; ++i) d[i] += xhat[i];
+            }
+            Piece<T, V> out;
+            out.pack(d);
+            out.store(p.dx + row * p.ld_dx + j);
+            if (p.dbranch) {
+                if constexpr (DROP) {
+                    uint32_t words[V];
+                    words_at<V>(g, static_cast<uint32_t>(j), static_cast<uint32_t>(row), words);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) d[i] = dropped(d[i], words[i], p.drop);
+                    out.pack(d);
+                }
+                out.store(p.dbranch + row * p.ld_db + j);
+            }
+        }
+        mean = mean_next;
+        rstd = rstd_next;
+        if constexpr (S > 0) stage = stage == S - 1 ? 0 : stage + 1;
+    }
+    pdl_launch_dependents();
+    if constexpr (S > 0) cp_async_wait<0>();
+    if (p.part == nullptr) return;
+
+    float* part = p.part + static_cast<int64_t>(blockIdx.x) * 2 * p.N;
+    if constexpr (MODE == NARROW) {
+        // lanes of the warp that took other rows of the same columns, then the warps in order
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                for (int o = team; o < 32; o *= 2) {
+                    dw[c][i] += __shfl_xor_sync(0xFFFFFFFFu, dw[c][i], o);
+                    db[c][i] += __shfl_xor_sync(0xFFFFFFFFu, db[c][i], o);
+                }
+        const int n = static_cast<int>(p.N);
+        for (int k = 0; k < nw; ++k) {
+            if (warp == k && lane < team) {
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    if (t + c * span >= pieces) continue;
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        const int j = (t + c * span) * V + i;
+                        s_part[j] = k ? s_part[j] + dw[c][i] : dw[c][i];
+                        s_part[n + j] = k ? s_part[n + j] + db[c][i] : db[c][i];
+                    }
+                }
+            }
+            __syncthreads();
+        }
+        for (int j = threadIdx.x; j < 2 * n; j += blockDim.x) part[j] = s_part[j];
+    } else {
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            if (t + c * span >= pieces) continue;
+            const int64_t j = static_cast<int64_t>(t + c * span) * V;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                part[j + i] = dw[c][i];
+                part[p.N + j + i] = db[c][i];
+            }
+        }
+    }
+}
+
+// Most partial rows of a call: CTAs of the row kernels that run at a time.
+int parts_of(int64_t M, int64_t N) {
+    const int64_t rows = N <= 1024 ? 4 : 1;  // rows that a CTA takes at a time, or so
+    return static_cast<int>(std::min<int64_t>((M + rows - 1) / rows, std::min(1024, 4 * sm_count())));
+}
+
+template <typename T, int V, int C, RowsMode MODE, bool DROP>
+cudaError_t launch_rows_as(BwdParams<T>& p, int team, unsigned block, cudaStream_t stream) {
+    // one wave: as many CTAs as run at a time (the answer is kept per CTA size)
+    static std::atomic<int> per_sm[33];
+    const auto kern = ln_bwd_rows_kernel<T, V, C, MODE, DROP>;
+    const size_t smem = size_t(ring_stages(V, C, MODE)) * 3 * C * block * 16;
+    int n = per_sm[block / 32].load(std::memory_order_relaxed);
+    if (n == 0) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - 16 * 1024);
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, static_cast<int>(block), smem);
+        if (e != cudaSuccess) return e;
+        n = std::max(n, 1);
+        per_sm[block / 32].store(n, std::memory_order_relaxed);
+    }
+    p.parts = std::min(p.parts, n * sm_count());
+    return launch_pdl(kern, dim3(p.parts), dim3(block), smem, stream, p, team);
+}
+
+template <typename T, int V, int C, RowsMode MODE>
+cudaError_t launch_rows(BwdParams<T>& p, int team, unsigned block, cudaStream_t stream) {
+    return p.drop.on && p.dbranch ? launch_rows_as<T, V, C, MODE, true>(p, team, block, stream)
+                                  : launch_rows_as<T, V, C, MODE, false>(p, team, block, stream);
+}
+
+// The one-pass kernels, where the row fits one; cudaErrorNotSupported where it
+// does not.  Lowers p.parts to the partial rows that are written.
+template <typename T, int V>
+cudaError_t launch_bwd_rows(BwdParams<T>& p, cudaStream_t stream) {
+    const int64_t pieces = p.N / V;
+    constexpr int kMost = 16 / V;  // pieces of a thread of a CTA's row: 16 columns
+    const auto threads = [&](int c) { return static_cast<unsigned>((pieces + 32 * c - 1) / (32 * c)) * 32; };
+    if (pieces > 512 * kMost) {
+        if constexpr (V > 1) {
+            if (pieces <= 1024 * kMost) return launch_rows<T, V, kMost, BROAD>(p, 0, threads(kMost), stream);
+        }
+        return cudaErrorNotSupported;
+    }
+    if (pieces > 128) {
+        if (pieces <= 256 * (kMost / 2)) return launch_rows<T, V, kMost / 2, WIDE>(p, 0, threads(kMost / 2), stream);
+        return launch_rows<T, V, kMost, WIDE>(p, 0, threads(kMost), stream);
+    }
+    int team = 1;
+    while (team < 32 && team < pieces) team *= 2;
+    switch ((pieces + team - 1) / team) {
+        case 1: return launch_rows<T, V, 1, NARROW>(p, team, 128, stream);
+        case 2: return launch_rows<T, V, 2, NARROW>(p, team, 128, stream);
+        case 3: return launch_rows<T, V, 3, NARROW>(p, team, 128, stream);
+        default: return launch_rows<T, V, 4, NARROW>(p, team, 128, stream);
+    }
+}
 
 template <typename T>
 int launch_bwd(const fp8q_layer_norm_bwd_args& a, const Dropout& drop, cudaStream_t stream) {
@@ -149,16 +441,24 @@ int launch_bwd(const fp8q_layer_norm_bwd_args& a, const Dropout& drop, cudaStrea
     p.part = static_cast<float*>(a.workspace);
     p.parts = parts_of(a.M, a.N);
     const bool cols = a.dweight || a.dbias;
-    cudaError_t e = cudaSuccess;
-    if (cols)
-        e = launch_pdl(ln_bwd_cols_kernel<T>, dim3(static_cast<unsigned>((a.N + 255) / 256), p.parts), dim3(256), 0,
-                       stream, p);
-    if (e == cudaSuccess)
-        e = launch_pdl(ln_bwd_loop_kernel<T>,
-                       dim3(static_cast<unsigned>(std::min<int64_t>(a.M, int64_t(sm_count()) * 8))), dim3(256), 0,
-                       stream, p);
+    if (!cols) p.part = nullptr;
+    constexpr int V = 16 / sizeof(T);
+    const bool pieces = a.N % V == 0 && rows16(a.dy, a.ld_dy, sizeof(T)) && rows16(a.r, a.ld_r, sizeof(T)) &&
+                        rows16(a.dresidual, a.ld_dresidual, sizeof(T)) && rows16(a.dx, a.ld_dx, sizeof(T)) &&
+                        rows16(a.dbranch, a.ld_dbranch, sizeof(T)) && aligned16(a.weight);
+    cudaError_t e = pieces ? launch_bwd_rows<T, V>(p, stream) : launch_bwd_rows<T, 1>(p, stream);
+    if (e == cudaErrorNotSupported) {
+        e = cudaSuccess;
+        if (cols)
+            e = launch_pdl(ln_bwd_cols_kernel<T>, dim3(static_cast<unsigned>((a.N + 255) / 256), p.parts), dim3(256), 0,
+                           stream, p);
+        if (e == cudaSuccess)
+            e = launch_pdl(ln_bwd_loop_kernel<T>,
+                           dim3(static_cast<unsigned>(std::min<int64_t>(a.M, int64_t(sm_count()) * 8))), dim3(256), 0,
+                           stream, p);
+    }
     if (cols && e == cudaSuccess)
-        e = launch_pdl(ln_bwd_reduce_kernel, dim3(static_cast<unsigned>((2 * a.N + 31) / 32)), dim3(256), 0, stream,
+        e = launch_pdl(ln_bwd_reduce_kernel, dim3(static_cast<unsigned>((2 * a.N + 31) / 32)), dim3(1024), 0, stream,
                        static_cast<const float*>(p.part), p.parts, a.N, a.dweight, a.dbias,
                        (a.flags & FP8Q_ACCUMULATE) != 0);
     if (e != cudaSuccess) {

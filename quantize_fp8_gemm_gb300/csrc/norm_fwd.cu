@@ -114,13 +114,166 @@ __global__ void __launch_bounds__(256) ln_fwd_loop_kernel(const FwdParams<T> p) 
         }
     }
     pdl_launch_dependents();
-    if (p.quant.on) {
-        amax = __reduce_max_sync(0xFFFFFFFFu, amax);
-        nsat = __reduce_add_sync(0xFFFFFFFFu, nsat);
-        if ((threadIdx.x & 31) == 0) {
-            if (p.quant.amax && amax) atomicMax(reinterpret_cast<unsigned*>(p.quant.amax), amax);
-            if (p.quant.sat && nsat) atomicAdd(p.quant.sat, static_cast<unsigned long long>(nsat));
+    if (p.quant.on) publish_quant(p.quant, amax, nsat);
+}
+
+// Rows of up to C pieces a thread, held in registers: one read of every input,
+// one write of every output.  WIDE = false: `team` (a power of two <= 32) lanes
+// of a warp take a row, statistics by shuffles.  WIDE = true: a CTA takes a row;
+// each warp forms the mean and the squared deviations of its part, and the
+// parts are joined in one exchange:  mean = sum n_w mean_w / N,
+// sum dev^2 = sum (dev^2_w + n_w (mean_w - mean)^2).
+template <typename T, int V, int C, bool DROP, bool WIDE>
+__global__ void __launch_bounds__(WIDE ? 1024 : 128)
+ln_fwd_rows_kernel(const FwdParams<T> p, int team) {
+    __shared__ float s_mean[32], s_dev[32], s_n[32];
+    const int lane = threadIdx.x & 31;
+    const int t = WIDE ? threadIdx.x : lane & (team - 1);  // this thread's place in its row's team
+    const int64_t row = WIDE ? blockIdx.x : (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) / team;
+    const int span = WIDE ? blockDim.x : team;
+    const int pieces = static_cast<int>(p.N / V);
+    const bool in = row < p.M;
+    const float inv_n = 1.0f / static_cast<float>(p.N);
+    pdl_wait();
+
+    float v[C][V];
+    float sum = 0.0f;
+    {
+        Piece<T, V> a[C], r[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int k = t + c * span;
+            a[c].zero();
+            if (in && k < pieces) a[c].load(p.x + row * p.ldx + static_cast<int64_t>(k) * V);
         }
+        if (p.res) {
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const int k = t + c * span;
+                r[c].zero();
+                if (in && k < pieces) r[c].load(p.res + row * p.ld_res + static_cast<int64_t>(k) * V);
+            }
+        }
+        Philox g;
+        if constexpr (DROP) g = Philox(p.drop.rng);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int k = t + c * span;
+            a[c].unpack(v[c]);
+            if (DROP || p.res) {
+                if constexpr (DROP) {
+                    uint32_t w[V];
+                    words_at<V>(g, static_cast<uint32_t>(k) * V, static_cast<uint32_t>(row), w);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) v[c][i] = dropped(v[c][i], w[i], p.drop);
+                }
+                if (p.res) {
+                    float f[V];
+                    r[c].unpack(f);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) v[c][i] = __fadd_rn(f[i], v[c][i]);
+                }
+                a[c].pack(v[c]);
+                if (p.r_out && in && k < pieces) a[c].store(p.r_out + row * p.ld_r + static_cast<int64_t>(k) * V);
+                a[c].unpack(v[c]);
+            }
+#pragma unroll
+            for (int i = 0; i < V; ++i) sum += v[c][i];  // pieces past the row are zeros
+        }
+    }
+
+    int own = 0;  // elements of this thread
+#pragma unroll
+    for (int c = 0; c < C; ++c) own += t + c * span < pieces ? V : 0;
+    int n = own;
+    const int width = WIDE ? 32 : team;
+    for (int o = width / 2; o; o >>= 1) {
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        if (WIDE) n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
+    }
+    float mean = WIDE ? sum / static_cast<float>(max(n, 1)) : sum * inv_n;
+    float dev = 0.0f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        if (t + c * span < pieces) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) dev = __fmaf_rn(v[c][i] - mean, v[c][i] - mean, dev);
+        }
+    }
+    for (int o = width / 2; o; o >>= 1) dev += __shfl_xor_sync(0xFFFFFFFFu, dev, o);
+    if constexpr (WIDE) {
+        const int warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+        if (lane == 0) {
+            s_mean[warp] = mean;
+            s_dev[warp] = dev;
+            s_n[warp] = static_cast<float>(n);
+        }
+        __syncthreads();
+        const float wn = lane < nw ? s_n[lane] : 0.0f, wm = lane < nw ? s_mean[lane] : 0.0f;
+        dev = lane < nw ? s_dev[lane] : 0.0f;
+        sum = wn * wm;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        mean = sum * inv_n;
+        dev = __fmaf_rn(wn * (wm - mean), wm - mean, dev);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) dev += __shfl_xor_sync(0xFFFFFFFFu, dev, o);
+    }
+    const float rstd = 1.0f / sqrtf(__fmaf_rn(dev, inv_n, p.eps));
+
+    uint32_t amax = 0, nsat = 0;
+    const float s = p.quant.on ? *p.quant.scale : 0.0f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int k = t + c * span;
+        if (!in || k >= pieces) continue;
+        const int64_t j = static_cast<int64_t>(k) * V;
+        float w[V], b[V];
+        load_params<T, V>(p.w, j, w);
+        load_params<T, V>(p.b, j, b);
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[c][i] = __fmaf_rn((v[c][i] - mean) * rstd, w[i], b[i]);
+        Piece<T, V> y;
+        y.pack(v[c]);
+        if (p.y) y.store(p.y + row * p.ldy + j);
+        if (p.quant.on) quant_piece<T, V>(p.quant, s, y, p.quant.q ? p.quant.q + row * p.N + j : nullptr, amax, nsat);
+    }
+    if (in && t == 0) {
+        if (p.mean) p.mean[row] = mean;
+        if (p.rstd) p.rstd[row] = rstd;
+    }
+    pdl_launch_dependents();
+    if (p.quant.on) publish_quant(p.quant, amax, nsat);
+}
+
+template <typename T, int V, int C, bool WIDE>
+cudaError_t launch_rows(const FwdParams<T>& p, int team, unsigned grid, unsigned block, cudaStream_t stream) {
+    return p.drop.on ? launch_pdl(ln_fwd_rows_kernel<T, V, C, true, WIDE>, dim3(grid), dim3(block), 0, stream, p, team)
+                     : launch_pdl(ln_fwd_rows_kernel<T, V, C, false, WIDE>, dim3(grid), dim3(block), 0, stream, p, team);
+}
+
+// The register kernels, where the row fits one; cudaErrorNotSupported where it does not.
+template <typename T, int V>
+cudaError_t launch_fwd_rows(const FwdParams<T>& p, cudaStream_t stream) {
+    constexpr int kWide = V == 1 ? 8 : 4;  // pieces of a thread of a CTA's row
+    const int64_t pieces = p.N / V;
+    if (pieces > 1024 * kWide) return cudaErrorNotSupported;
+    if (pieces > 32 * 8) {
+        const unsigned block = static_cast<unsigned>((pieces + 32 * kWide - 1) / (32 * kWide)) * 32;
+        return launch_rows<T, V, kWide, true>(p, 0, static_cast<unsigned>(p.M), block, stream);
+    }
+    int team = 1;
+    while (team < 32 && team < pieces) team *= 2;
+    const unsigned grid = static_cast<unsigned>((p.M * team + 127) / 128);
+    switch ((pieces + team - 1) / team) {
+        case 1: return launch_rows<T, V, 1, false>(p, team, grid, 128, stream);
+        case 2: return launch_rows<T, V, 2, false>(p, team, grid, 128, stream);
+        case 3: return launch_rows<T, V, 3, false>(p, team, grid, 128, stream);
+        case 4: return launch_rows<T, V, 4, false>(p, team, grid, 128, stream);
+        case 5: return launch_rows<T, V, 5, false>(p, team, grid, 128, stream);
+        case 6: return launch_rows<T, V, 6, false>(p, team, grid, 128, stream);
+        case 7: return launch_rows<T, V, 7, false>(p, team, grid, 128, stream);
+        default: return launch_rows<T, V, 8, false>(p, team, grid, 128, stream);
     }
 }
 
@@ -144,8 +297,16 @@ int launch_fwd(const fp8q_layer_norm_args& a, const Dropout& drop, const QuantOu
     p.rstd = a.rstd;
     p.drop = drop;
     p.quant = quant;
-    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(a.M, int64_t(sm_count()) * 8));
-    if (launch_pdl(ln_fwd_loop_kernel<T>, dim3(grid), dim3(256), 0, stream, p) != cudaSuccess) {
+    constexpr int V = 16 / sizeof(T);
+    const bool pieces = a.N % V == 0 && rows16(a.x, a.ldx, sizeof(T)) && rows16(a.residual, a.ld_residual, sizeof(T)) &&
+                        rows16(a.r_out, a.ld_r, sizeof(T)) && rows16(a.y, a.ldy, sizeof(T)) && aligned16(a.weight) &&
+                        aligned16(a.bias) && aligned_to(a.q_out, V);
+    cudaError_t e = pieces ? launch_fwd_rows<T, V>(p, stream) : launch_fwd_rows<T, 1>(p, stream);
+    if (e == cudaErrorNotSupported) {
+        const unsigned grid = static_cast<unsigned>(std::min<int64_t>(a.M, int64_t(sm_count()) * 8));
+        e = launch_pdl(ln_fwd_loop_kernel<T>, dim3(grid), dim3(256), 0, stream, p);
+    }
+    if (e != cudaSuccess) {
         (void)cudaGetLastError();
         return FP8Q_ERR_CUDA;
     }

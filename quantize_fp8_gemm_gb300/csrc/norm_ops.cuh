@@ -6,6 +6,8 @@
 #include "common.cuh"
 #include "quant_ops.cuh"
 
+#include <type_traits>
+
 namespace fp8q {
 
 // ------------------------------------------------------------ element types --
@@ -39,6 +41,80 @@ struct Params {
     }
 };
 
+// V adjacent elements of a row: 16 bytes in one access, or one element.
+template <typename T, int V>
+struct Piece {
+    static_assert(V * sizeof(T) == 16, "16-byte pieces or single elements");
+    uint4 raw;
+    __device__ __forceinline__ void load(const T* p) { raw = ld_stream_v4(p); }
+    __device__ __forceinline__ void store(T* p) const { st_v4(p, raw); }
+    __device__ __forceinline__ void zero() { raw = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void unpack(float (&v)[V]) const {
+        const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                v[i] = __uint_as_float(u[i]);
+            } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+                v[2 * i] = bf16lo_to_f32(u[i]);
+                v[2 * i + 1] = bf16hi_to_f32(u[i]);
+            } else {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+                v[2 * i] = f.x;
+                v[2 * i + 1] = f.y;
+            }
+        }
+    }
+    __device__ __forceinline__ void pack(const float (&v)[V]) {
+        uint32_t u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                u[i] = __float_as_uint(v[i]);
+            } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+                u[i] = cvt_bf16x2(v[2 * i], v[2 * i + 1]);
+            } else {
+                const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+                u[i] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+        }
+        raw = make_uint4(u[0], u[1], u[2], u[3]);
+    }
+};
+template <typename T>
+struct Piece<T, 1> {
+    T raw;
+    __device__ __forceinline__ void load(const T* p) { raw = *p; }
+    __device__ __forceinline__ void store(T* p) const { *p = raw; }
+    __device__ __forceinline__ void zero() { raw = from_f32<T>(0.0f); }
+    __device__ __forceinline__ void unpack(float (&v)[1]) const { v[0] = to_f32(raw); }
+    __device__ __forceinline__ void pack(const float (&v)[1]) { raw = from_f32<T>(v[0]); }
+};
+
+// V parameters from column j (16-byte accesses need the vector 16-byte aligned).
+template <typename T, int V>
+__device__ __forceinline__ void load_params(const Params<T>& w, int64_t j, float (&v)[V]) {
+    if (w.p == nullptr) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = w.none;
+    } else if constexpr (V == 1) {
+        v[0] = w.at(j);
+    } else if (w.f32) {
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+            const float4 f = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(w.p) + j + i));
+            v[i] = f.x;
+            v[i + 1] = f.y;
+            v[i + 2] = f.z;
+            v[i + 3] = f.w;
+        }
+    } else {
+        Piece<T, V> q;
+        q.raw = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(w.p) + j));
+        q.unpack(v);
+    }
+}
+
 // ----------------------------------------------------------------- dropout --
 // Philox4x32-10 (J. Salmon, M. Moraes, R. Dror, D. Shaw, "Parallel random
 // numbers: as easy as 1, 2, 3", SC 2011): ten rounds of two 32 x 32 -> 64 bit
@@ -49,6 +125,7 @@ struct Params {
 // not on the element type, the strides, the launch shape or the kernel.
 struct Philox {
     uint32_t k0, k1, o0, o1;
+    Philox() = default;
     __device__ __forceinline__ explicit Philox(const uint64_t* rng) {
         const uint64_t seed = rng[0], off = rng[1];
         k0 = static_cast<uint32_t>(seed);
@@ -106,6 +183,23 @@ __device__ __forceinline__ float dropped(float x, uint32_t word, const Dropout& 
     return word > d.last ? __fmul_rn(x, d.inv) : 0.0f;
 }
 
+// The generator words of the V columns from j of a row (V = 1: the word of column j).
+template <int V>
+__device__ __forceinline__ void words_at(const Philox& g, uint32_t j, uint32_t row, uint32_t (&w)[V]) {
+    if constexpr (V == 1) {
+        w[0] = word_of(g.block(j >> 2, row), j & 3);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+            const uint4 b = g.block((j + i) >> 2, row);
+            w[i] = b.x;
+            w[i + 1] = b.y;
+            w[i + 2] = b.z;
+            w[i + 3] = b.w;
+        }
+    }
+}
+
 // -------------------------------------------------------- quantize epilogue --
 // The framework's cast of the rounded output: v = y * s, q = FP8(v), max |y|
 // (as float32 bits: those of non-negative floats order like the values, and a
@@ -123,12 +217,56 @@ __device__ __forceinline__ uint16_t cast_pair(float v0, float v1, int fmt) {
     return fmt == FP8Q_E5M2 ? cvt_fp8x2<FP8Q_E5M2>(v0, v1) : cvt_fp8x2<FP8Q_E4M3>(v0, v1);
 }
 
+// Scale and cast V values of the rounded output from a row's column j; folds
+// their magnitudes and saturations into amax / nsat.
+template <typename T, int V>
+__device__ __forceinline__ void quant_piece(const QuantOut& o, float s, const Piece<T, V>& y, uint8_t* dst,
+                                            uint32_t& amax, uint32_t& nsat) {
+    float f[V], v[V];
+    y.unpack(f);
+    const float fmax = fp8_max_value(o.fmt);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        v[i] = __fmul_rn(f[i], s);
+        amax = max(amax, __float_as_uint(fabsf(f[i])));
+        nsat += fabsf(v[i]) > fmax;
+    }
+    if (dst == nullptr) return;
+    if constexpr (V == 1) {
+        *dst = static_cast<uint8_t>(cast_pair(v[0], 0.0f, o.fmt));
+    } else {
+        uint32_t q[V / 4];
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i)
+            q[i] = cast_pair(v[4 * i], v[4 * i + 1], o.fmt) |
+                   (static_cast<uint32_t>(cast_pair(v[4 * i + 2], v[4 * i + 3], o.fmt)) << 16);
+        if constexpr (V == 8) st_v2(dst, make_uint2(q[0], q[1]));
+        else *reinterpret_cast<uint32_t*>(dst) = q[0];
+    }
+}
+
+// A warp's maximum and count into the call's accumulators.  The maximum only
+// grows, so a warp whose own is no larger than a value read earlier has
+// nothing to add: of tens of thousands of warps a few reach the atomic.
+__device__ __forceinline__ void publish_quant(const QuantOut& o, uint32_t amax, uint32_t nsat) {
+    amax = __reduce_max_sync(0xFFFFFFFFu, amax);
+    nsat = __reduce_add_sync(0xFFFFFFFFu, nsat);
+    if ((threadIdx.x & 31) != 0) return;
+    unsigned* a = reinterpret_cast<unsigned*>(o.amax);
+    if (a && amax > *reinterpret_cast<volatile unsigned*>(a)) atomicMax(a, amax);
+    if (o.sat && nsat) atomicAdd(o.sat, static_cast<unsigned long long>(nsat));
+}
+
 // Zeroes the accumulators of a call that does not accumulate.  One launch for
 // both words, and one the next kernel's launch overlaps.
 __global__ void clear_quant_kernel(float* amax, unsigned long long* sat);
 
 inline bool is_dtype(int t) { return t == FP8Q_BF16 || t == FP8Q_FP16 || t == FP8Q_FP32; }
 inline size_t dtype_size(int t) { return t == FP8Q_FP32 ? 4 : 2; }
+// Whether a tensor's rows (NULL: no tensor) all start on 16-byte boundaries.
+inline bool rows16(const void* p, int64_t ld, size_t es) {
+    return p == nullptr || (aligned16(p) && (static_cast<uint64_t>(ld) * es) % 16 == 0);
+}
 inline bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 // Sum over the CTA's threads of two values, in every thread; the order of the
