@@ -91,6 +91,54 @@ struct Piece<T, 1> {
     __device__ __forceinline__ void pack(const float (&v)[1]) { raw = from_f32<T>(v[0]); }
 };
 
+// Two float32 values in one 64-bit register pair; each lane of an operation is
+// the IEEE operation rounded once, at half the instructions.
+using f32x2 = uint64_t;
+__device__ __forceinline__ f32x2 pair_of(float a, float b) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 split(f32x2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+// A 16-byte piece as pairs, and back.
+template <typename T, int V>
+__device__ __forceinline__ void unpack2(const Piece<T, V>& q, f32x2 (&v)[V / 2]) {
+    float f[V];
+    q.unpack(f);
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) v[i] = pair_of(f[2 * i], f[2 * i + 1]);
+}
+template <typename T, int V>
+__device__ __forceinline__ void pack2(Piece<T, V>& q, const f32x2 (&v)[V / 2]) {
+    float f[V];
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+        const float2 a = split(v[i]);
+        f[2 * i] = a.x;
+        f[2 * i + 1] = a.y;
+    }
+    q.pack(f);
+}
+
 // V parameters from column j (16-byte accesses need the vector 16-byte aligned).
 template <typename T, int V>
 __device__ __forceinline__ void load_params(const Params<T>& w, int64_t j, float (&v)[V]) {
@@ -243,6 +291,18 @@ __device__ __forceinline__ void quant_piece(const QuantOut& o, float s, const Pi
         if constexpr (V == 8) st_v2(dst, make_uint2(q[0], q[1]));
         else *reinterpret_cast<uint32_t*>(dst) = q[0];
     }
+}
+
+// The same for the 8 packed BF16 values of a piece, magnitudes folded into two
+// 16-bit lanes.  Saturations are counted only where the largest magnitude can
+// saturate (a NaN among them takes the counting route too).
+template <int FMT>
+__device__ __forceinline__ void quant_bf16x8(float s, uint4 y, uint8_t* dst, uint32_t& amax2, uint32_t& nsat) {
+    uint32_t m2 = __vmaxu2(__vmaxu2(y.x & 0x7FFF7FFFu, y.y & 0x7FFF7FFFu),
+                           __vmaxu2(y.z & 0x7FFF7FFFu, y.w & 0x7FFF7FFFu));
+    amax2 = __vmaxu2(amax2, m2);
+    if (!(__fmul_rn(__uint_as_float(max16x2(m2) << 16), s) <= fp8_max_value(FMT))) nsat += sat_count8<FMT>(y, s);
+    if (dst != nullptr) st_v2(dst, cast8_codes<FMT>(y, s));
 }
 
 // A warp's maximum and count into the call's accumulators.  The maximum only
