@@ -8,6 +8,7 @@
 #include "norm_ops.cuh"
 
 #include <algorithm>
+#include <atomic>
 
 namespace fp8q {
 
@@ -25,90 +26,100 @@ struct DropParams {
     Dropout drop;
 };
 
-// Any layout: a thread takes quads of columns, one generator block each.
-template <typename T>
-__global__ void __launch_bounds__(256) dropout_quad_kernel(const DropParams<T> p) {
+// A warp takes 32 adjacent pieces of a row (or, where a row has fewer, 32 / team
+// rows), the same columns of every row that it comes to: the generator's
+// products of the columns are formed once.  U rows are in flight a warp.
+// SHIFT: rows off the 16-byte grid (norm_ops.cuh); a lane loads the two granules
+// that hold its piece (the second from L1, where its neighbour brought it).
+template <typename T, bool RES, bool SHIFT>
+__global__ void __launch_bounds__(256) dropout_rows_kernel(const DropParams<T> p, int team, int chunks) {
+    constexpr int V = 16 / sizeof(T), U = 4;
+    const int lane = threadIdx.x & 31;
+    const int64_t N = p.N, pieces = SHIFT ? (N + V - 1) / V : N / V;
+    const int64_t warp = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+    const int64_t warps = static_cast<int64_t>(gridDim.x) * blockDim.x >> 5;
+    const int k = static_cast<int>(warp % chunks) * 32 + (lane & (team - 1));
+    const int rows_warp = 32 / team;
+    const int64_t step = warps / chunks * rows_warp;  // rows that all warps of a chunk take at a time
+    const int64_t first = warp / chunks * rows_warp + lane / team;
+    const int64_t left = N - static_cast<int64_t>(k) * V;  // columns from this thread's first
+    const int valid_k = k < pieces ? (left < V ? static_cast<int>(left) : V) : 0;
     pdl_wait();
-    const int64_t quads = (p.N + 3) / 4, total = quads * p.M;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
-         i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-        const int64_t row = i / quads, q = i - row * quads;
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (p.drop.on) w = Philox(p.drop.rng).block(static_cast<uint32_t>(q), static_cast<uint32_t>(row));
+    if (warp / chunks >= warps / chunks) return;  // the warps that make no full set of chunks
+
+    Philox g;
+    uint64_t quad_m0 = 0;
+    if (p.drop.on) {
+        g = Philox(p.drop.rng);
+        quad_m0 = kPhiloxM0 * (static_cast<uint32_t>(k) * (V / 4));
+    }
+    auto load = [&](const T* start, bool in) -> uint4 {
+        if constexpr (SHIFT) {
+            const uint32_t mis = granule_offset(start);
+            const uint4* at = reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(start) - mis) + k;
+            uint4 a = make_uint4(0, 0, 0, 0), b = a;
+            if (in) a = __ldg(at);
+            if (in && (k + int64_t(1)) * 16 - mis < N * static_cast<int64_t>(sizeof(T))) b = __ldg(at + 1);
+            return cut16(a, b, mis);
+        } else {
+            return in ? ld_stream_v4(start + static_cast<int64_t>(k) * V) : make_uint4(0, 0, 0, 0);
+        }
+    };
+    for (int64_t base = first - lane / team; base < p.M; base += U * step) {
+        Piece<T, V> x[U], r[U];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int64_t j = q * 4 + k;
-            if (j >= p.N) continue;
-            float v = to_f32(p.x[row * p.ldx + j]);
-            if (p.drop.on) v = dropped(v, word_of(w, k), p.drop);
-            if (p.res) v = __fadd_rn(to_f32(p.res[row * p.ld_res + j]), v);
-            p.y[row * p.ldy + j] = from_f32<T>(v);
+        for (int u = 0; u < U; ++u) {
+            const int64_t row = base + lane / team + u * step;
+            const bool in = row < p.M && valid_k > 0;
+            x[u].raw = load(p.x + (in ? row : 0) * p.ldx, in);
+            if constexpr (RES) r[u].raw = load(p.res + (in ? row : 0) * p.ld_res, in);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t row = base + lane / team + u * step;
+            const int valid = row < p.M ? valid_k : 0;
+            if (!SHIFT && valid == 0) continue;
+            float v[V];
+            x[u].unpack(v);
+            if (p.drop.on) {
+                uint32_t w[V];
+                words_at<V>(g, quad_m0, g.row(static_cast<uint32_t>(row)), w);
+#pragma unroll
+                for (int i = 0; i < V; ++i) v[i] = dropped(v[i], w[i], p.drop);
+            }
+            if constexpr (RES) {
+                float f[V];
+                r[u].unpack(f);
+#pragma unroll
+                for (int i = 0; i < V; ++i) v[i] = __fadd_rn(f[i], v[i]);
+            }
+            x[u].pack(v);
+            if constexpr (SHIFT) store_shifted<T>(x[u].raw, p.y + row * p.ldy, k, valid, team);
+            else x[u].store(p.y + row * p.ldy + static_cast<int64_t>(k) * V);
         }
     }
     pdl_launch_dependents();
 }
 
-// Division of n < 2^31 by a fixed d >= 1 as a product: n / d = (n * m) >> (31 + s)
-// with s = ceil(log2 d), m = ceil(2^(31 + s) / d) (below 2^32); the excess
-// n * (m d - 2^(31 + s)) / (d 2^(31 + s)) is below n / 2^31 / d < 1 / d, so
-// the quotient is exact.
-struct FastDiv {
-    uint32_t m;
-    int s;
-    __host__ explicit FastDiv(uint32_t d) : s(31) {
-        while ((1u << (s - 31)) < d) ++s;
-        m = static_cast<uint32_t>(((uint64_t(1) << s) + d - 1) / d);
-    }
-    __device__ __forceinline__ uint32_t div(uint32_t n) const {
-        return static_cast<uint32_t>((static_cast<uint64_t>(n) * m) >> s);
-    }
-};
-
-// Rows on the 16-byte grid: a thread takes U 16-byte pieces, loads first.
-template <typename T, int U, bool RES>
-__global__ void __launch_bounds__(256) dropout_piece_kernel(const DropParams<T> p, uint32_t total, uint32_t per_row,
-                                                            const FastDiv div) {
+template <typename T, bool RES, bool SHIFT>
+cudaError_t launch_rows(const DropParams<T>& p, cudaStream_t stream) {
     constexpr int V = 16 / sizeof(T);
-    pdl_wait();
-    const uint32_t first = blockIdx.x * (256u * U) + threadIdx.x;
-    Piece<T, V> x[U], r[U];
-    uint32_t row[U], k[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const uint32_t i = first + u * 256u;
-        row[u] = div.div(i);
-        k[u] = i - row[u] * per_row;
-        if (i < total) x[u].load(p.x + static_cast<int64_t>(row[u]) * p.ldx + static_cast<int64_t>(k[u]) * V);
+    static std::atomic<int> per_sm;  // CTAs that run at a time
+    const auto kern = dropout_rows_kernel<T, RES, SHIFT>;
+    int n = per_sm.load(std::memory_order_relaxed);
+    if (n == 0) {
+        const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, 256, 0);
+        if (e != cudaSuccess) return e;
+        n = std::max(n, 1);
+        per_sm.store(n, std::memory_order_relaxed);
     }
-    if constexpr (RES) {
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (first + u * 256u < total)
-                r[u].load(p.res + static_cast<int64_t>(row[u]) * p.ld_res + static_cast<int64_t>(k[u]) * V);
-    }
-    Philox g;
-    if (p.drop.on) g = Philox(p.drop.rng);
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        if (first + u * 256u >= total) continue;
-        float v[V];
-        x[u].unpack(v);
-        if (p.drop.on) {
-            uint32_t w[V];
-            words_at<V>(g, k[u] * V, row[u], w);
-#pragma unroll
-            for (int i = 0; i < V; ++i) v[i] = dropped(v[i], w[i], p.drop);
-        }
-        if constexpr (RES) {
-            float f[V];
-            r[u].unpack(f);
-#pragma unroll
-            for (int i = 0; i < V; ++i) v[i] = __fadd_rn(f[i], v[i]);
-        }
-        x[u].pack(v);
-        x[u].store(p.y + static_cast<int64_t>(row[u]) * p.ldy + static_cast<int64_t>(k[u]) * V);
-    }
-    pdl_launch_dependents();
+    const int64_t pieces = (p.N + V - 1) / V;
+    const int team = team_of(pieces);
+    const int64_t chunks = (pieces + 31) / 32, rows_warp = 32 / team;
+    const int64_t want = ((p.M + rows_warp - 1) / rows_warp * chunks + 7) / 8;
+    const int64_t least = (chunks + 7) / 8;  // one full set of chunks
+    const int64_t grid = std::max(least, std::min<int64_t>(want, int64_t(n) * sm_count()));
+    return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(256), 0, stream, p, team, static_cast<int>(chunks));
 }
 
 template <typename T>
@@ -116,23 +127,13 @@ int launch_drop(const void* x, int64_t ldx, const void* res, int64_t ld_res, voi
                 const Dropout& drop, cudaStream_t stream) {
     const DropParams<T> p = {M, N, static_cast<const T*>(x), ldx, static_cast<const T*>(res), ld_res,
                              static_cast<T*>(y), ldy, drop};
-    constexpr int V = 16 / sizeof(T), U = 2;
-    if (N % V == 0 && rows16(x, ldx, sizeof(T)) && rows16(res, ld_res, sizeof(T)) && rows16(y, ldy, sizeof(T)) &&
-        N / V < (int64_t(1) << 31) / M) {
-        const uint32_t per_row = static_cast<uint32_t>(N / V), total = per_row * static_cast<uint32_t>(M);
-        const dim3 grid((total + 256 * U - 1) / (256 * U));
-        const FastDiv div(per_row);
-        if ((res ? launch_pdl(dropout_piece_kernel<T, U, true>, grid, dim3(256), 0, stream, p, total, per_row, div)
-                 : launch_pdl(dropout_piece_kernel<T, U, false>, grid, dim3(256), 0, stream, p, total, per_row, div)) !=
-            cudaSuccess) {
-            (void)cudaGetLastError();
-            return FP8Q_ERR_CUDA;
-        }
-        return FP8Q_OK;
-    }
-    const int64_t want = ((N + 3) / 4 * M + 255) / 256;
-    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(want, int64_t(sm_count()) * 64));
-    if (launch_pdl(dropout_quad_kernel<T>, dim3(grid), dim3(256), 0, stream, p) != cudaSuccess) {
+    constexpr int V = 16 / sizeof(T);
+    cudaError_t e;
+    if (N % V == 0 && rows16(x, ldx, sizeof(T)) && rows16(res, ld_res, sizeof(T)) && rows16(y, ldy, sizeof(T)))
+        e = res ? launch_rows<T, true, false>(p, stream) : launch_rows<T, false, false>(p, stream);
+    else
+        e = res ? launch_rows<T, true, true>(p, stream) : launch_rows<T, false, true>(p, stream);
+    if (e != cudaSuccess) {
         (void)cudaGetLastError();
         return FP8Q_ERR_CUDA;
     }

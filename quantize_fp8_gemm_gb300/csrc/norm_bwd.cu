@@ -8,36 +8,21 @@
 // The column sums go through float32 partial rows in the caller's workspace,
 // which a second kernel adds in a fixed order: no atomics, so the same call
 // gives the same bits.
-#include "common.cuh"
-#include "norm_ops.cuh"
+#include "norm_bwd.cuh"
 
 #include <algorithm>
-#include <atomic>
 
 namespace fp8q {
 
-namespace {
+// in norm_bwd_*.cu
+extern template cudaError_t launch_bwd_ring<__nv_bfloat16, false>(BwdParams<__nv_bfloat16>&, cudaStream_t);
+extern template cudaError_t launch_bwd_ring<__nv_bfloat16, true>(BwdParams<__nv_bfloat16>&, cudaStream_t);
+extern template cudaError_t launch_bwd_ring<__half, false>(BwdParams<__half>&, cudaStream_t);
+extern template cudaError_t launch_bwd_ring<__half, true>(BwdParams<__half>&, cudaStream_t);
+extern template cudaError_t launch_bwd_ring<float, false>(BwdParams<float>&, cudaStream_t);
+extern template cudaError_t launch_bwd_ring<float, true>(BwdParams<float>&, cudaStream_t);
 
-template <typename T>
-struct BwdParams {
-    int64_t M, N;
-    const T* dy;
-    int64_t ld_dy;
-    const T* r;
-    int64_t ld_r;
-    const float* mean;
-    const float* rstd;
-    Params<T> w;
-    const T* dres;
-    int64_t ld_dres;
-    T* dx;
-    int64_t ld_dx;
-    T* dbranch;
-    int64_t ld_db;
-    Dropout drop;
-    float* part;  // [parts][2][N]: dweight and dbias sums of a set of rows
-    int parts;
-};
+namespace {
 
 // Any width: one CTA per row, two passes over it.
 template <typename T>
@@ -62,7 +47,7 @@ __global__ void __launch_bounds__(256) ln_bwd_loop_kernel(const BwdParams<T> p) 
         for (int64_t q = threadIdx.x; q < quads; q += blockDim.x) {
             uint4 w = make_uint4(0, 0, 0, 0);
             if (p.dbranch && p.drop.on)
-                w = Philox(p.drop.rng).block(static_cast<uint32_t>(q), static_cast<uint32_t>(row));
+                w = Philox(p.drop.rng).at(static_cast<uint32_t>(q), static_cast<uint32_t>(row));
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int64_t j = q * 4 + i;
@@ -128,295 +113,10 @@ __global__ void __launch_bounds__(1024) ln_bwd_reduce_kernel(const float* part, 
     pdl_launch_dependents();
 }
 
-// One pass: every input is read once.  A thread keeps its C pieces' columns for
-// all the rows that its CTA takes (row blockIdx.x, + the grid, ...), so the
-// column sums stay in registers until the end.  16-byte pieces come through a
-// ring of kStages rows in shared memory, filled by cp.async: a thread copies
-// and reads its own pieces only, so it waits for its own copies and no barrier
-// guards the ring.  Single elements are loaded where they are used.
-enum RowsMode {
-    NARROW,  // `team` lanes (a power of two) take a row, 32 / team rows a warp, 4 warps
-    WIDE,    // a CTA of up to 512 threads takes a row
-    BROAD    // the same with up to 1024 threads, whose 64 registers hold no weights
-};
-
-// Rows of the ring: what a CTA's shared memory holds of its widest row.  A
-// stage is 48 C bytes a thread: 96 KB for 512 threads of C = 4, or 1024 of C = 2.
-constexpr int ring_stages(int V, int C, RowsMode mode) {
-    return V == 1 ? 0 : mode == BROAD ? (C == 4 ? 1 : 2) : mode == WIDE && C == 4 ? 2 : 3;
-}
-
-template <typename T, int V, int C, RowsMode MODE, bool DROP>
-__global__ void __launch_bounds__(MODE == NARROW ? 128 : MODE == WIDE ? 512 : 1024)
-ln_bwd_rows_kernel(const BwdParams<T> p, int team) {
-    extern __shared__ uint4 s_ring[];  // [stage][dy, r, dresidual][c][thread]
-    __shared__ float s_part[MODE == NARROW ? 2 * 32 * C * V : 1];
-    __shared__ float2 s_sum[2][32];
-    constexpr int S = ring_stages(V, C, MODE);
-    constexpr bool kHeld = V > 1 && MODE != BROAD;  // weights in registers
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-    const int t = MODE == NARROW ? lane & (team - 1) : threadIdx.x;
-    const int span = MODE == NARROW ? team : blockDim.x;
-    const int pieces = static_cast<int>(p.N / V);
-    const float inv_n = 1.0f / static_cast<float>(p.N);
-    pdl_wait();
-
-    float w[kHeld ? C : 1][V], dw[C][V], db[C][V];
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) dw[c][i] = db[c][i] = 0.0f;
-        if constexpr (kHeld) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) w[c][i] = 0.0f;
-            if (t + c * span < pieces) load_params<T, V>(p.w, static_cast<int64_t>(t + c * span) * V, w[c]);
-        }
-    }
-    Philox g;
-    if constexpr (DROP) g = Philox(p.drop.rng);
-
-    const int rows_warp = MODE == NARROW ? 32 / team : 1;
-    const int rows_cta = MODE == NARROW ? rows_warp * nw : 1;
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * rows_cta;
-    const int64_t base0 = static_cast<int64_t>(blockIdx.x) * rows_cta;
-    const int64_t sub = MODE == NARROW ? warp * rows_warp + lane / team : 0;
-
-    // pieces past the row, and rows past the last, are zeros
-    auto slot = [&](int stage, int tensor, int c) {
-        return s_ring + ((stage * 3 + tensor) * C + c) * static_cast<int>(blockDim.x) + threadIdx.x;
-    };
-    auto fill = [&](int stage, int64_t row) {
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const bool in = row < p.M && t + c * span < pieces;
-            const int64_t j = static_cast<int64_t>(t + c * span) * V;
-            cp_async16_or_zero(smem_u32(slot(stage, 0, c)), in ? p.dy + row * p.ld_dy + j : p.dy, in);
-            cp_async16_or_zero(smem_u32(slot(stage, 1, c)), in ? p.r + row * p.ld_r + j : p.r, in);
-            if (p.dres) cp_async16_or_zero(smem_u32(slot(stage, 2, c)), in ? p.dres + row * p.ld_dres + j : p.dres, in);
-        }
-        cp_async_commit();
-    };
-    if constexpr (S > 0) {
-#pragma unroll
-        for (int k = 0; k < S - 1; ++k) fill(k, base0 + sub + k * stride);
-    }
-    float mean = base0 + sub < p.M ? p.mean[base0 + sub] : 0.0f;
-    float rstd = base0 + sub < p.M ? p.rstd[base0 + sub] : 0.0f;
-    int buf = 0, stage = 0;
-    for (int64_t base = base0; base < p.M; base += stride) {
-        const int64_t row = base + sub, ahead = row + stride;
-        const float mean_next = ahead < p.M ? p.mean[ahead] : 0.0f, rstd_next = ahead < p.M ? p.rstd[ahead] : 0.0f;
-        Piece<T, V> dyp[V == 1 ? C : 1], rp[V == 1 ? C : 1];
-        if constexpr (S > 0) {
-            fill(stage == 0 ? S - 1 : stage - 1, row + (S - 1) * stride);
-            cp_async_wait<S - 1>();
-        } else {
-#pragma unroll
-            for (int c = 0; c < C; ++c) {
-                const int k = t + c * span;
-                dyp[c].zero();
-                rp[c].zero();
-                if (row < p.M && k < pieces) {
-                    dyp[c].load(p.dy + row * p.ld_dy + k);
-                    rp[c].load(p.r + row * p.ld_r + k);
-                }
-            }
-        }
-        auto inputs = [&](int c, float (&dy)[V], float (&xhat)[V]) {
-            Piece<T, V> a, b;
-            if constexpr (S > 0) {
-                a.raw = *slot(stage, 0, c);
-                b.raw = *slot(stage, 1, c);
-            } else {
-                a = dyp[c];
-                b = rp[c];
-            }
-            a.unpack(dy);
-            b.unpack(xhat);
-#pragma unroll
-            for (int i = 0; i < V; ++i) xhat[i] = (xhat[i] - mean) * rstd;
-        };
-        auto weights = [&](int c, float (&v)[V]) {
-            if constexpr (kHeld) {
-#pragma unroll
-                for (int i = 0; i < V; ++i) v[i] = w[c][i];
-            } else {
-                load_params<T, V>(p.w, static_cast<int64_t>(t + c * span) * V, v);
-            }
-        };
-        float c1 = 0.0f, c2 = 0.0f;
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-            if (t + c * span >= pieces) continue;
-            float dy[V], xhat[V], wc[V];
-            inputs(c, dy, xhat);
-            weights(c, wc);
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float gi = dy[i] * wc[i];
-                c1 += gi;
-                c2 = __fmaf_rn(gi, xhat[i], c2);
-                dw[c][i] = __fmaf_rn(dy[i], xhat[i], dw[c][i]);
-                db[c][i] += dy[i];
-            }
-        }
-        const int width = MODE == NARROW ? team : 32;
-        for (int o = width / 2; o; o >>= 1) {
-            c1 += __shfl_xor_sync(0xFFFFFFFFu, c1, o);
-            c2 += __shfl_xor_sync(0xFFFFFFFFu, c2, o);
-        }
-        if constexpr (MODE != NARROW) {
-            // two buffers: a warp that runs ahead writes the other one, and cannot reach this one
-            // again before every warp has passed the next row's barrier
-            if (lane == 0) s_sum[buf][warp] = make_float2(c1, c2);
-            __syncthreads();
-            c1 = c2 = 0.0f;
-            for (int k = 0; k < nw; ++k) {
-                const float2 f = s_sum[buf][k];
-                c1 += f.x;
-                c2 += f.y;
-            }
-            buf ^= 1;
-        }
-        c1 *= inv_n;
-        c2 *= inv_n;
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const int k = t + c * span;
-            if (row >= p.M || k >= pieces) continue;
-            const int64_t j = static_cast<int64_t>(k) * V;
-            float d[V], xhat[V], wc[V];
-            inputs(c, d, xhat);
-            weights(c, wc);
-#pragma unroll
-            for (int i = 0; i < V; ++i) d[i] = rstd * (d[i] * wc[i] - c1 - xhat[i] * c2);
-            if (p.dres) {
-                Piece<T, V> a;
-                if constexpr (S > 0) a.raw = *slot(stage, 2, c);
-                else a.load(p.dres + row * p.ld_dres + k);
-                a.unpack(xhat);
-#pragma unroll
-                for (int i = 0; i < V; ++i) d[i] += xhat[i];
-            }
-            Piece<T, V> out;
-            out.pack(d);
-            out.store(p.dx + row * p.ld_dx + j);
-            if (p.dbranch) {
-                if constexpr (DROP) {
-                    uint32_t words[V];
-                    words_at<V>(g, static_cast<uint32_t>(j), static_cast<uint32_t>(row), words);
-#pragma unroll
-                    for (int i = 0; i < V; ++i) d[i] = dropped(d[i], words[i], p.drop);
-                    out.pack(d);
-                }
-                out.store(p.dbranch + row * p.ld_db + j);
-            }
-        }
-        mean = mean_next;
-        rstd = rstd_next;
-        if constexpr (S > 0) stage = stage == S - 1 ? 0 : stage + 1;
-    }
-    pdl_launch_dependents();
-    if constexpr (S > 0) cp_async_wait<0>();
-    if (p.part == nullptr) return;
-
-    float* part = p.part + static_cast<int64_t>(blockIdx.x) * 2 * p.N;
-    if constexpr (MODE == NARROW) {
-        // lanes of the warp that took other rows of the same columns, then the warps in order
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                for (int o = team; o < 32; o *= 2) {
-                    dw[c][i] += __shfl_xor_sync(0xFFFFFFFFu, dw[c][i], o);
-                    db[c][i] += __shfl_xor_sync(0xFFFFFFFFu, db[c][i], o);
-                }
-        const int n = static_cast<int>(p.N);
-        for (int k = 0; k < nw; ++k) {
-            if (warp == k && lane < team) {
-#pragma unroll
-                for (int c = 0; c < C; ++c) {
-                    if (t + c * span >= pieces) continue;
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        const int j = (t + c * span) * V + i;
-                        s_part[j] = k ? s_part[j] + dw[c][i] : dw[c][i];
-                        s_part[n + j] = k ? s_part[n + j] + db[c][i] : db[c][i];
-                    }
-                }
-            }
-            __syncthreads();
-        }
-        for (int j = threadIdx.x; j < 2 * n; j += blockDim.x) part[j] = s_part[j];
-    } else {
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-            if (t + c * span >= pieces) continue;
-            const int64_t j = static_cast<int64_t>(t + c * span) * V;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                part[j + i] = dw[c][i];
-                part[p.N + j + i] = db[c][i];
-            }
-        }
-    }
-}
-
 // Most partial rows of a call: CTAs of the row kernels that run at a time.
 int parts_of(int64_t M, int64_t N) {
     const int64_t rows = N <= 1024 ? 4 : 1;  // rows that a CTA takes at a time, or so
     return static_cast<int>(std::min<int64_t>((M + rows - 1) / rows, std::min(1024, 4 * sm_count())));
-}
-
-template <typename T, int V, int C, RowsMode MODE, bool DROP>
-cudaError_t launch_rows_as(BwdParams<T>& p, int team, unsigned block, cudaStream_t stream) {
-    // one wave: as many CTAs as run at a time (the answer is kept per CTA size)
-    static std::atomic<int> per_sm[33];
-    const auto kern = ln_bwd_rows_kernel<T, V, C, MODE, DROP>;
-    const size_t smem = size_t(ring_stages(V, C, MODE)) * 3 * C * block * 16;
-    int n = per_sm[block / 32].load(std::memory_order_relaxed);
-    if (n == 0) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - 16 * 1024);
-        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, static_cast<int>(block), smem);
-        if (e != cudaSuccess) return e;
-        n = std::max(n, 1);
-        per_sm[block / 32].store(n, std::memory_order_relaxed);
-    }
-    p.parts = std::min(p.parts, n * sm_count());
-    return launch_pdl(kern, dim3(p.parts), dim3(block), smem, stream, p, team);
-}
-
-template <typename T, int V, int C, RowsMode MODE>
-cudaError_t launch_rows(BwdParams<T>& p, int team, unsigned block, cudaStream_t stream) {
-    return p.drop.on && p.dbranch ? launch_rows_as<T, V, C, MODE, true>(p, team, block, stream)
-                                  : launch_rows_as<T, V, C, MODE, false>(p, team, block, stream);
-}
-
-// The one-pass kernels, where the row fits one; cudaErrorNotSupported where it
-// does not.  Lowers p.parts to the partial rows that are written.
-template <typename T, int V>
-cudaError_t launch_bwd_rows(BwdParams<T>& p, cudaStream_t stream) {
-    const int64_t pieces = p.N / V;
-    constexpr int kMost = 16 / V;  // pieces of a thread of a CTA's row: 16 columns
-    const auto threads = [&](int c) { return static_cast<unsigned>((pieces + 32 * c - 1) / (32 * c)) * 32; };
-    if (pieces > 512 * kMost) {
-        if constexpr (V > 1) {
-            if (pieces <= 1024 * kMost) return launch_rows<T, V, kMost, BROAD>(p, 0, threads(kMost), stream);
-        }
-        return cudaErrorNotSupported;
-    }
-    if (pieces > 128) {
-        if (pieces <= 256 * (kMost / 2)) return launch_rows<T, V, kMost / 2, WIDE>(p, 0, threads(kMost / 2), stream);
-        return launch_rows<T, V, kMost, WIDE>(p, 0, threads(kMost), stream);
-    }
-    int team = 1;
-    while (team < 32 && team < pieces) team *= 2;
-    switch ((pieces + team - 1) / team) {
-        case 1: return launch_rows<T, V, 1, NARROW>(p, team, 128, stream);
-        case 2: return launch_rows<T, V, 2, NARROW>(p, team, 128, stream);
-        case 3: return launch_rows<T, V, 3, NARROW>(p, team, 128, stream);
-        default: return launch_rows<T, V, 4, NARROW>(p, team, 128, stream);
-    }
 }
 
 template <typename T>
@@ -430,7 +130,7 @@ int launch_bwd(const fp8q_layer_norm_bwd_args& a, const Dropout& drop, cudaStrea
     p.ld_r = a.ld_r;
     p.mean = a.mean;
     p.rstd = a.rstd;
-    p.w = Params<T>{a.weight, a.param_dtype == FP8Q_FP32, 1.0f};
+    p.w = Params<T>{a.weight, a.param_dtype == FP8Q_FP32, 1.0f, aligned16(a.weight)};
     p.dres = static_cast<const T*>(a.dresidual);
     p.ld_dres = a.ld_dresidual;
     p.dx = static_cast<T*>(a.dx);
@@ -446,7 +146,7 @@ int launch_bwd(const fp8q_layer_norm_bwd_args& a, const Dropout& drop, cudaStrea
     const bool pieces = a.N % V == 0 && rows16(a.dy, a.ld_dy, sizeof(T)) && rows16(a.r, a.ld_r, sizeof(T)) &&
                         rows16(a.dresidual, a.ld_dresidual, sizeof(T)) && rows16(a.dx, a.ld_dx, sizeof(T)) &&
                         rows16(a.dbranch, a.ld_dbranch, sizeof(T)) && aligned16(a.weight);
-    cudaError_t e = pieces ? launch_bwd_rows<T, V>(p, stream) : launch_bwd_rows<T, 1>(p, stream);
+    cudaError_t e = pieces ? launch_bwd_ring<T, false>(p, stream) : launch_bwd_ring<T, true>(p, stream);
     if (e == cudaErrorNotSupported) {
         e = cudaSuccess;
         if (cols)

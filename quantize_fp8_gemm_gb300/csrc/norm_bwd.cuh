@@ -1,0 +1,336 @@
+// norm_bwd.cuh -- the one-pass kernels of layer_norm_bwd, which norm_bwd.cu
+// launches; each element type is a translation unit of its own (norm_bwd_*.cu),
+// so that they compile side by side.
+#pragma once
+
+#include "common.cuh"
+#include "norm_ops.cuh"
+
+#include <algorithm>
+#include <atomic>
+
+namespace fp8q {
+
+template <typename T>
+struct BwdParams {
+    int64_t M, N;
+    const T* dy;
+    int64_t ld_dy;
+    const T* r;
+    int64_t ld_r;
+    const float* mean;
+    const float* rstd;
+    Params<T> w;
+    const T* dres;
+    int64_t ld_dres;
+    T* dx;
+    int64_t ld_dx;
+    T* dbranch;
+    int64_t ld_db;
+    Dropout drop;
+    float* part;  // [parts][2][N]: dweight and dbias sums of a set of rows
+    int parts;
+};
+
+namespace {
+
+// One pass: every input is read once.  A thread keeps its C pieces' columns for
+// all the rows that its CTA takes (row blockIdx.x, + the grid, ...), so the
+// column sums stay in registers until the end.  The next rows' pieces are in
+// flight in a ring of S rows in shared memory, filled by cp.async: a thread
+// copies and reads its own pieces only, so it waits for its own copies and no
+// barrier guards the ring.  SHIFT: rows off the 16-byte grid (norm_ops.cuh); a
+// lane then reads its own granule and the next lane's.
+// WIDE = false: `team` lanes (a power of two <= 32) of a warp take a row, up to
+// 64 columns a lane: the row's two sums are shuffles, and a row costs the fewest
+// instructions.  WIDE = true: a CTA takes a row, 32 columns a thread.
+__host__ __device__ constexpr int bwd_ring_rows(int C, bool wide) {
+    // what a CTA's shared memory holds: a stage is 48 C bytes a thread
+    return wide ? (C > 4 ? 1 : 2) : C > 4 ? 2 : 3;
+}
+
+template <typename T, int C, bool WIDE, bool DROP, bool SHIFT>
+__global__ void __launch_bounds__(WIDE ? 512 : 128) ln_bwd_ring_kernel(const BwdParams<T> p, int team) {
+    extern __shared__ uint4 s_ring[];  // [stage][dy, r, dresidual][c][slot]; at the end NARROW's partial row
+    __shared__ float2 s_sum[2][16];
+    constexpr int V = 16 / sizeof(T), H = V / 2, S = bwd_ring_rows(C, WIDE);
+    constexpr bool kHeld = !WIDE && C * V <= 32;  // weights in registers; otherwise from L1 in every row
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    const int t = WIDE ? threadIdx.x : lane & (team - 1);
+    const int span = WIDE ? blockDim.x : team;
+    const int N = static_cast<int>(p.N), pieces = SHIFT ? (N + V - 1) / V : N / V;
+    const float inv_n = 1.0f / static_cast<float>(N);
+    const f32x2 zero2 = pair_of(0.0f, 0.0f);
+    pdl_wait();
+
+    f32x2 w[kHeld ? C : 1][H], dw[C][H], db[C][H];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+#pragma unroll
+        for (int i = 0; i < H; ++i) dw[c][i] = db[c][i] = zero2;
+        if constexpr (kHeld) {
+#pragma unroll
+            for (int i = 0; i < H; ++i) w[c][i] = zero2;
+            if (t + c * span < pieces) load_params2<T, V, SHIFT>(p.w, (t + c * span) * V, N, w[c]);
+        }
+    }
+    Philox g;
+    if constexpr (DROP) g = Philox(p.drop.rng);
+    const uint64_t first_m0 = kPhiloxM0 * static_cast<uint32_t>(t * (V / 4));
+
+    const int rows_warp = WIDE ? 1 : 32 / team, rows_cta = WIDE ? 1 : rows_warp * nw;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * rows_cta;
+    const int64_t base0 = static_cast<int64_t>(blockIdx.x) * rows_cta;
+    const int64_t sub = WIDE ? 0 : warp * rows_warp + lane / team;
+
+    const int slots = warp_slots(SHIFT, WIDE ? 32 : team);
+    const int my_slot = warp * slots + lane + (SHIFT && !WIDE ? lane / team : 0);
+    auto slot = [&](int stage, int tensor, int c) { return s_ring + ((stage * 3 + tensor) * C + c) * (nw * slots) + my_slot; };
+    const bool team_end = SHIFT && (WIDE ? lane == 31 : t == team - 1);
+    auto fill_one = [&](int stage, int tensor, int c, const T* x, int64_t ld, int64_t row) {
+        const int k = t + c * span;
+        if constexpr (SHIFT)
+            copy_granules(slot(stage, tensor, c), x, x + row * ld, k, row < p.M ? N * static_cast<int>(sizeof(T)) : 0, team_end);
+        else {
+            const bool in = row < p.M && k < pieces;
+            cp_async16_or_zero(smem_u32(slot(stage, tensor, c)), in ? x + row * ld + k * V : x, in);
+        }
+    };
+    // pieces past the row, and rows past the last, are zeros
+    auto fill = [&](int stage, int64_t row) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            fill_one(stage, 0, c, p.dy, p.ld_dy, row);
+            fill_one(stage, 1, c, p.r, p.ld_r, row);
+            if (p.dres) fill_one(stage, 2, c, p.dres, p.ld_dres, row);
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int k = 0; k < S - 1; ++k) fill(k, base0 + sub + k * stride);
+    float mean = base0 + sub < p.M ? p.mean[base0 + sub] : 0.0f;
+    float rstd = base0 + sub < p.M ? p.rstd[base0 + sub] : 0.0f;
+    if constexpr (WIDE) {
+        if (threadIdx.x < 32) s_sum[threadIdx.x >> 4][threadIdx.x & 15] = make_float2(0.0f, 0.0f);
+        __syncthreads();
+    }
+    int buf = 0, stage = 0;
+    for (int64_t base = base0; base < p.M; base += stride) {
+        const int64_t row = base + sub, ahead = row + stride;
+        const float mean_next = ahead < p.M ? p.mean[ahead] : 0.0f, rstd_next = ahead < p.M ? p.rstd[ahead] : 0.0f;
+        fill(stage == 0 ? S - 1 : stage - 1, row + (S - 1) * stride);
+        cp_async_wait<S - 1>();
+        if constexpr (SHIFT) __syncwarp();
+        const uint32_t mis_dy = SHIFT ? granule_offset(p.dy + row * p.ld_dy) : 0;
+        const uint32_t mis_r = SHIFT ? granule_offset(p.r + row * p.ld_r) : 0;
+        const uint32_t mis_dres = SHIFT && p.dres ? granule_offset(p.dres + row * p.ld_dres) : 0;
+        const f32x2 shift = pair_of(-mean, -mean), scale = pair_of(rstd, rstd);
+        // dy, xhat and g = dy * w of piece c
+        auto inputs = [&](int c, f32x2 (&dy)[H], f32x2 (&xhat)[H], f32x2 (&gw)[H]) {
+            Piece<T, V> a;
+            a.raw = read_piece<SHIFT>(slot(stage, 0, c), mis_dy);
+            unpack2(a, dy);
+            a.raw = read_piece<SHIFT>(slot(stage, 1, c), mis_r);
+            unpack2(a, xhat);
+            if (SHIFT && (t + c * span) * V + V > N) {  // the row's end: what follows in the granule is not its own
+                zero_from<V>(dy, N - (t + c * span) * V);
+                zero_from<V>(xhat, N - (t + c * span) * V);
+            }
+            f32x2 wl[H];
+            if constexpr (!kHeld) load_params2<T, V, SHIFT>(p.w, (t + c * span) * V, N, wl);
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                xhat[i] = mul2(add2(xhat[i], shift), scale);
+                gw[i] = mul2(dy[i], kHeld ? w[kHeld ? c : 0][i] : wl[i]);
+            }
+        };
+        f32x2 c1v = zero2, c2v = zero2;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            if (t + c * span >= pieces) continue;
+            f32x2 dy[H], xhat[H], gw[H];
+            inputs(c, dy, xhat, gw);
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                c1v = add2(c1v, gw[i]);
+                c2v = fma2(gw[i], xhat[i], c2v);
+                dw[c][i] = fma2(dy[i], xhat[i], dw[c][i]);
+                db[c][i] = add2(db[c][i], dy[i]);
+            }
+        }
+        const float2 h1 = split(c1v), h2 = split(c2v);
+        float c1 = h1.x + h1.y, c2 = h2.x + h2.y;
+        for (int o = (WIDE ? 32 : team) / 2; o; o >>= 1) {
+            c1 += __shfl_xor_sync(0xFFFFFFFFu, c1, o);
+            c2 += __shfl_xor_sync(0xFFFFFFFFu, c2, o);
+        }
+        if constexpr (WIDE) {
+            // two buffers: a warp that runs ahead writes the other one, and cannot reach this one
+            // again before every warp has passed the next row's barrier
+            if (lane == 0) s_sum[buf][warp] = make_float2(c1, c2);
+            __syncthreads();
+            c1 = c2 = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {  // absent warps are zeros
+                const float2 f = s_sum[buf][k];
+                c1 += f.x;
+                c2 += f.y;
+            }
+            buf ^= 1;
+        }
+        c1 *= -inv_n;
+        c2 *= -inv_n;
+        const f32x2 c1n = pair_of(c1, c1), c2n = pair_of(c2, c2);
+        uint64_t row_m0 = 0;
+        if constexpr (DROP) row_m0 = g.row(static_cast<uint32_t>(row));
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int k = t + c * span;
+            const int valid = row < p.M && k < pieces ? (SHIFT ? min(V, N - k * V) : V) : 0;
+            if (!SHIFT && valid == 0) continue;
+            f32x2 dy[H], xhat[H], d[H];
+            Piece<T, V> out;
+            if (valid > 0) {
+                inputs(c, dy, xhat, d);
+#pragma unroll
+                for (int i = 0; i < H; ++i) d[i] = fma2(xhat[i], c2n, add2(d[i], c1n));
+                if (p.dres) {
+                    out.raw = read_piece<SHIFT>(slot(stage, 2, c), mis_dres);
+                    unpack2(out, xhat);
+#pragma unroll
+                    for (int i = 0; i < H; ++i) d[i] = fma2(d[i], scale, xhat[i]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < H; ++i) d[i] = mul2(d[i], scale);
+                }
+                pack2(out, d);
+            }
+            if constexpr (SHIFT) store_shifted<T>(out.raw, p.dx + row * p.ld_dx, k, valid, WIDE ? 32 : team);
+            else out.store(p.dx + row * p.ld_dx + k * V);
+            if (p.dbranch) {
+                if constexpr (DROP) {
+                    uint32_t words[V];
+                    words_at<V>(g, first_m0 + kPhiloxM0 * static_cast<uint32_t>(c * span * (V / 4)), row_m0, words);
+                    float f[V];
+#pragma unroll
+                    for (int i = 0; i < H; ++i) {
+                        const float2 e = split(d[i]);
+                        f[2 * i] = dropped(e.x, words[2 * i], p.drop);
+                        f[2 * i + 1] = dropped(e.y, words[2 * i + 1], p.drop);
+                    }
+                    out.pack(f);
+                }
+                if constexpr (SHIFT) store_shifted<T>(out.raw, p.dbranch + row * p.ld_db, k, valid, WIDE ? 32 : team);
+                else out.store(p.dbranch + row * p.ld_db + k * V);
+            }
+        }
+        mean = mean_next;
+        rstd = rstd_next;
+        stage = stage == S - 1 ? 0 : stage + 1;
+        if constexpr (SHIFT) __syncwarp();  // the granules that a neighbour read may be overwritten now
+    }
+    pdl_launch_dependents();
+    cp_async_wait<0>();
+    if (p.part == nullptr) return;
+
+    float* part = p.part + static_cast<int64_t>(blockIdx.x) * 2 * p.N;
+    if constexpr (!WIDE) {
+        // lanes of the warp that took other rows of the same columns, then the warps in order
+        float* s_part = reinterpret_cast<float*>(s_ring);
+        for (int k = 0; k < nw; ++k) {
+            __syncthreads();  // k = 0: every thread is done with the ring
+            if (warp != k) continue;
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const int j0 = (t + c * span) * V;
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float2 pw = split(dw[c][i / 2]), pb = split(db[c][i / 2]);
+                    float a = i & 1 ? pw.y : pw.x, b = i & 1 ? pb.y : pb.x;
+                    for (int o = team; o < 32; o *= 2) {
+                        a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+                        b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+                    }
+                    if (lane >= team || j0 + i >= N) continue;
+                    s_part[j0 + i] = k ? s_part[j0 + i] + a : a;
+                    s_part[N + j0 + i] = k ? s_part[N + j0 + i] + b : b;
+                }
+            }
+        }
+        __syncthreads();
+        for (int j = threadIdx.x; j < 2 * N; j += blockDim.x) part[j] = s_part[j];
+    } else {
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int j0 = (t + c * span) * V;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                if (j0 + i >= N) continue;
+                const float2 pw = split(dw[c][i / 2]), pb = split(db[c][i / 2]);
+                part[j0 + i] = i & 1 ? pw.y : pw.x;
+                part[p.N + j0 + i] = i & 1 ? pb.y : pb.x;
+            }
+        }
+    }
+}
+
+template <typename T, int C, bool WIDE, bool DROP, bool SHIFT>
+cudaError_t launch_ring_as(BwdParams<T>& p, int team, unsigned block, cudaStream_t stream) {
+    // one wave: as many CTAs as run at a time (the answer is kept by CTA and team size)
+    static std::atomic<int> per_sm[17][6];
+    const auto kern = ln_bwd_ring_kernel<T, C, WIDE, DROP, SHIFT>;
+    const size_t smem = size_t(bwd_ring_rows(C, WIDE)) * 3 * C * (block / 32) * warp_slots(SHIFT, team) * 16;
+    int log_team = 0;
+    while ((1 << log_team) < team) ++log_team;
+    std::atomic<int>& known = per_sm[block / 32][log_team];
+    int n = known.load(std::memory_order_relaxed);
+    if (n == 0) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxRing);
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, static_cast<int>(block), smem);
+        if (e != cudaSuccess) return e;
+        n = std::max(n, 1);
+        known.store(n, std::memory_order_relaxed);
+    }
+    p.parts = std::min(p.parts, n * sm_count());
+    return launch_pdl(kern, dim3(p.parts), dim3(block), smem, stream, p, team);
+}
+
+template <typename T, int C, bool WIDE, bool SHIFT>
+cudaError_t launch_ring(BwdParams<T>& p, int team, unsigned block, cudaStream_t stream) {
+    return p.drop.on && p.dbranch ? launch_ring_as<T, C, WIDE, true, SHIFT>(p, team, block, stream)
+                                  : launch_ring_as<T, C, WIDE, false, SHIFT>(p, team, block, stream);
+}
+
+}  // namespace
+
+// The one-pass kernels, where the row fits one; cudaErrorNotSupported where it
+// does not.  Lowers p.parts to the partial rows that are written.
+template <typename T, bool SHIFT>
+cudaError_t launch_bwd_ring(BwdParams<T>& p, cudaStream_t stream) {
+    constexpr int V = 16 / sizeof(T);
+    const int64_t pieces = (p.N + V - 1) / V;
+    const int team = team_of(pieces);
+    switch (columns_of((pieces + team - 1) / team, SHIFT)) {
+        case 1: return launch_ring<T, 1, false, SHIFT>(p, team, 128, stream);
+        case 2: return launch_ring<T, 2, false, SHIFT>(p, team, 128, stream);
+        case 4: return launch_ring<T, 4, false, SHIFT>(p, team, 128, stream);
+        case 8: return launch_ring<T, 8, false, SHIFT>(p, team, 128, stream);
+        default: break;
+    }
+    if constexpr (!SHIFT) {
+        switch ((pieces + team - 1) / team) {
+            case 3: return launch_ring<T, 3, false, SHIFT>(p, team, 128, stream);
+            case 5: return launch_ring<T, 5, false, SHIFT>(p, team, 128, stream);
+            case 6: return launch_ring<T, 6, false, SHIFT>(p, team, 128, stream);
+            case 7: return launch_ring<T, 7, false, SHIFT>(p, team, 128, stream);
+            default: break;
+        }
+    }
+    if (pieces <= 512 * 4) return launch_ring<T, 4, true, SHIFT>(p, 32, threads_of(pieces, 4), stream);
+    if constexpr (V == 4) {
+        if (pieces <= 512 * 8) return launch_ring<T, 8, true, SHIFT>(p, 32, threads_of(pieces, 8), stream);
+    }
+    return cudaErrorNotSupported;
+}
+
+}  // namespace fp8q

@@ -1,0 +1,340 @@
+// norm_fwd.cuh -- the one-pass kernels of layer_norm_fwd, which norm_fwd.cu
+// launches; each element type is a translation unit of its own (norm_fwd_*.cu),
+// so that they compile side by side.
+#pragma once
+
+#include "common.cuh"
+#include "norm_ops.cuh"
+
+#include <algorithm>
+#include <atomic>
+
+namespace fp8q {
+
+template <typename T>
+struct FwdParams {
+    int64_t M, N;
+    const T* x;
+    int64_t ldx;
+    const T* res;
+    int64_t ld_res;
+    T* r_out;
+    int64_t ld_r;
+    Params<T> w, b;
+    float eps;
+    T* y;
+    int64_t ldy;
+    float* mean;
+    float* rstd;
+    Dropout drop;
+    QuantOut quant;
+};
+
+namespace {
+
+// One pass over rows of 16-byte pieces.  One wave of CTAs takes rows in turn;
+// the next rows' pieces are in flight in a ring of S rows in shared memory, and
+// the row at hand is in registers from its one read to its one write.
+//   NARROW  `team` lanes (a power of two <= 32) of a warp take a row, up to 64
+//           columns a lane; statistics by shuffles
+//   WIDE    a CTA of up to 256 threads takes a row, 32 columns a thread
+//   BROAD   the same with up to 512 threads, whose registers hold no weights
+// A CTA's warps each form the mean and the squared deviations of their part; the
+// parts are joined in one exchange:  mean = sum n_w mean_w / N,
+// sum dev^2 = sum (dev^2_w + n_w (mean_w - mean)^2).
+// SHIFT: rows off the 16-byte grid (norm_ops.cuh).  A thread copies its own
+// granule, the last lane of a team one more; a lane reads its own and the next.
+// Without SHIFT a thread reads what it copied, and waits for its own copies only.
+enum FwdMode { NARROW, WIDE, BROAD };
+
+// With 40 columns a lane or more the generator's registers beside 128 of weights
+// would leave two warps a scheduler: the weights then come from L1 in every row.
+__host__ __device__ constexpr bool weights_held(int columns, bool drop, FwdMode mode) {
+    return mode != BROAD && !(drop && columns >= 40);
+}
+// Rows of the ring: what leaves room for three CTAs a multiprocessor, or fits at all.
+__host__ __device__ constexpr int ring_rows(int C, int columns, bool drop, bool res, FwdMode mode) {
+    if (mode == BROAD) return !res ? 3 : C == 8 ? 1 : 2;
+    return drop && res && columns >= 40 ? 2 : 3;
+}
+
+template <typename T, int C, bool DROP, bool RES, FwdMode MODE, bool SHIFT>
+__global__ void __launch_bounds__(MODE == BROAD ? 512 : MODE == WIDE ? 256 : 128,
+                                  MODE == NARROW && DROP && C * 16 / sizeof(T) >= 32 ? 3 : 1)
+ln_fwd_ring_kernel(const FwdParams<T> p, int team) {
+    extern __shared__ uint4 s_ring[];  // [stage][x, residual][c][slot]
+    __shared__ float4 s_warp[2][16];   // a warp's n, n * mean, mean, squared deviations
+    constexpr int V = 16 / sizeof(T), H = V / 2, TENSORS = RES ? 2 : 1;
+    constexpr int S = ring_rows(C, C * V, DROP, RES, MODE);
+    constexpr bool kHeld = weights_held(C * V, DROP, MODE), kCta = MODE != NARROW;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    const int t = kCta ? threadIdx.x : lane & (team - 1);
+    const int span = kCta ? blockDim.x : team;
+    const int N = static_cast<int>(p.N), pieces = SHIFT ? (N + V - 1) / V : N / V;
+    const float inv_n = 1.0f / static_cast<float>(N);
+    const f32x2 zero2 = pair_of(0.0f, 0.0f);
+    pdl_wait();
+
+    f32x2 w[kHeld ? C : 1][H], b[kHeld ? C : 1][H];
+    int own = 0;  // elements of this thread; of this warp later
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int k = t + c * span;
+        if constexpr (kHeld) {
+#pragma unroll
+            for (int i = 0; i < H; ++i) w[c][i] = b[c][i] = zero2;
+        }
+        if (k >= pieces) continue;
+        own += SHIFT ? min(V, N - k * V) : V;
+        if constexpr (kHeld) {
+            load_params2<T, V, SHIFT>(p.w, k * V, N, w[c]);
+            load_params2<T, V, SHIFT>(p.b, k * V, N, b[c]);
+        }
+    }
+    float inv_own = inv_n;  // 1 / (elements whose mean a warp forms)
+    if constexpr (kCta) {
+        own = __reduce_add_sync(0xFFFFFFFFu, own);
+        inv_own = own ? 1.0f / static_cast<float>(own) : 0.0f;
+        if (threadIdx.x < 32) s_warp[threadIdx.x >> 4][threadIdx.x & 15] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        __syncthreads();
+    }
+    Philox g;
+    if constexpr (DROP) g = Philox(p.drop.rng);
+    const uint64_t first_m0 = kPhiloxM0 * static_cast<uint32_t>(t * (V / 4));  // of this thread's first piece
+    const float s = p.quant.on ? *p.quant.scale : 0.0f;
+    uint32_t amax = 0, amax2 = 0, nsat = 0;
+
+    const int rows_warp = kCta ? 1 : 32 / team, rows_cta = kCta ? 1 : rows_warp * nw;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * rows_cta;
+    const int64_t base0 = static_cast<int64_t>(blockIdx.x) * rows_cta;
+    const int64_t sub = kCta ? 0 : warp * rows_warp + lane / team;
+    const int slots = warp_slots(SHIFT, kCta ? 32 : team);
+    const int my_slot = warp * slots + lane + (SHIFT && !kCta ? lane / team : 0);
+    auto slot = [&](int stage, int tensor, int c) {
+        return s_ring + ((stage * TENSORS + tensor) * C + c) * (nw * slots) + my_slot;
+    };
+    const bool team_end = SHIFT && (kCta ? lane == 31 : t == team - 1);
+    auto fill_one = [&](int stage, int tensor, int c, const T* x, int64_t ld, int64_t row) {
+        const int k = t + c * span;
+        if constexpr (SHIFT)
+            copy_granules(slot(stage, tensor, c), x, x + row * ld, k, row < p.M ? N * static_cast<int>(sizeof(T)) : 0, team_end);
+        else {
+            const bool in = row < p.M && k < pieces;
+            cp_async16_or_zero(smem_u32(slot(stage, tensor, c)), in ? x + row * ld + k * V : x, in);
+        }
+    };
+    // pieces past the row, and rows past the last, are zeros
+    auto fill = [&](int stage, int64_t row) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            fill_one(stage, 0, c, p.x, p.ldx, row);
+            if constexpr (RES) fill_one(stage, 1, c, p.res, p.ld_res, row);
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int k = 0; k < S - 1; ++k) fill(k, base0 + sub + k * stride);
+
+    int stage = 0, buf = 0;
+    for (int64_t base = base0; base < p.M; base += stride) {
+        const int64_t row = base + sub;
+        fill(stage == 0 ? S - 1 : stage - 1, row + (S - 1) * stride);
+        cp_async_wait<S - 1>();
+        if constexpr (SHIFT) __syncwarp();
+        uint64_t row_m0 = 0;
+        if constexpr (DROP) row_m0 = g.row(static_cast<uint32_t>(row));
+        const uint32_t mis_x = SHIFT ? granule_offset(p.x + row * p.ldx) : 0;
+        const uint32_t mis_r = SHIFT && RES ? granule_offset(p.res + row * p.ld_res) : 0;
+        f32x2 v[C][H], sum2 = zero2;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int k = t + c * span;
+            const int valid = SHIFT ? (k < pieces ? min(V, N - k * V) : 0) : V;
+            Piece<T, V> a;
+            a.raw = read_piece<SHIFT>(slot(stage, 0, c), mis_x);
+            if constexpr (DROP || RES) {
+                float f[V];
+                a.unpack(f);
+                if constexpr (DROP) {
+                    uint32_t words[V];
+                    words_at<V>(g, first_m0 + kPhiloxM0 * static_cast<uint32_t>(c * span * (V / 4)), row_m0, words);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) f[i] = dropped(f[i], words[i], p.drop);
+                }
+                if constexpr (RES) {
+                    Piece<T, V> r;
+                    r.raw = read_piece<SHIFT>(slot(stage, 1, c), mis_r);
+                    unpack2(r, v[c]);
+#pragma unroll
+                    for (int i = 0; i < H; ++i) v[c][i] = add2(v[c][i], pair_of(f[2 * i], f[2 * i + 1]));
+                    pack2(a, v[c]);
+                } else {
+                    a.pack(f);
+                }
+                if (p.r_out) {
+                    if constexpr (SHIFT) store_shifted<T>(a.raw, p.r_out + row * p.ld_r, k, row < p.M ? valid : 0, kCta ? 32 : team);
+                    else if (row < p.M && k < pieces) a.store(p.r_out + row * p.ld_r + k * V);
+                }
+            }
+            unpack2(a, v[c]);
+            if (SHIFT && valid < V) zero_from<V>(v[c], valid);
+            f32x2 part = add2(v[c][0], v[c][1]);
+            if constexpr (H == 4) part = add2(part, add2(v[c][2], v[c][3]));
+            sum2 = add2(sum2, part);
+        }
+        const int width = kCta ? 32 : team;
+        const float2 halves = split(sum2);
+        float sum = halves.x + halves.y;
+        for (int o = width / 2; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        float mean = sum * inv_own;
+        f32x2 shift = pair_of(-mean, -mean), dev2[2] = {zero2, zero2};
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int k = t + c * span;
+            if (k >= pieces) continue;
+            f32x2 d[H];
+#pragma unroll
+            for (int i = 0; i < H; ++i) d[i] = add2(v[c][i], shift);
+            if (SHIFT && k * V + V > N) zero_from<V>(d, N - k * V);
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                if constexpr (!kCta) v[c][i] = d[i];
+                dev2[i & 1] = fma2(d[i], d[i], dev2[i & 1]);
+            }
+        }
+        const float2 devs = split(add2(dev2[0], dev2[1]));
+        float dev = devs.x + devs.y;
+        for (int o = width / 2; o; o >>= 1) dev += __shfl_xor_sync(0xFFFFFFFFu, dev, o);
+        if constexpr (kCta) {
+            // two buffers: a warp that runs ahead writes the other one, and cannot reach this one
+            // again before every warp has passed the next row's barrier
+            const float n = static_cast<float>(own);
+            if (lane == 0) s_warp[buf][warp] = make_float4(n, n * mean, mean, dev);
+            __syncthreads();
+            constexpr int kWarps = MODE == WIDE ? 8 : 16;  // absent ones are zeros
+            sum = dev = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) sum += s_warp[buf][k].y;
+            mean = sum * inv_n;
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) {
+                const float4 f = s_warp[buf][k];
+                const float m = f.z - mean;
+                dev += __fmaf_rn(f.x * m, m, f.w);
+            }
+            buf ^= 1;
+            shift = pair_of(-mean, -mean);
+        }
+        const float rstd = 1.0f / sqrtf(__fmaf_rn(dev, inv_n, p.eps));
+        const f32x2 scale = pair_of(rstd, rstd);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int k = t + c * span;
+            const int valid = row < p.M && k < pieces ? (SHIFT ? min(V, N - k * V) : V) : 0;
+            if (!SHIFT && valid == 0) continue;
+            f32x2 wl[H], bl[H];
+            if constexpr (!kHeld) {
+                if (valid > 0) {
+                    load_params2<T, V, SHIFT>(p.w, k * V, N, wl);
+                    load_params2<T, V, SHIFT>(p.b, k * V, N, bl);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                const f32x2 d = kCta ? add2(v[c][i], shift) : v[c][i];
+                v[c][i] = fma2(mul2(d, scale), kHeld ? w[kHeld ? c : 0][i] : wl[i], kHeld ? b[kHeld ? c : 0][i] : bl[i]);
+            }
+            Piece<T, V> y;
+            pack2(y, v[c]);
+            if (p.y) {
+                if constexpr (SHIFT) store_shifted<T>(y.raw, p.y + row * p.ldy, k, valid, kCta ? 32 : team);
+                else y.store(p.y + row * p.ldy + k * V);
+            }
+            if (p.quant.on && valid > 0) {
+                uint8_t* dst = p.quant.q ? p.quant.q + row * p.N + k * V : nullptr;
+                const bool whole = !SHIFT || (valid == V && (reinterpret_cast<uintptr_t>(dst) & (V - 1)) == 0);
+                if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+                    if (whole) {
+                        if (p.quant.fmt == FP8Q_E5M2) quant_bf16x8<FP8Q_E5M2>(s, y.raw, dst, amax2, nsat);
+                        else quant_bf16x8<FP8Q_E4M3>(s, y.raw, dst, amax2, nsat);
+                        continue;
+                    }
+                }
+                quant_piece<T, V>(p.quant, s, y, dst, valid, whole, amax, nsat);
+            }
+        }
+        if (row < p.M && t == 0) {
+            if (p.mean) p.mean[row] = mean;
+            if (p.rstd) p.rstd[row] = rstd;
+        }
+        stage = stage == S - 1 ? 0 : stage + 1;
+        if constexpr (SHIFT) __syncwarp();  // the granules that a neighbour read may be overwritten now
+    }
+    pdl_launch_dependents();
+    cp_async_wait<0>();
+    if (p.quant.on) publish_quant(p.quant, max(amax, max16x2(amax2) << 16), nsat);
+}
+
+template <typename T, int C, bool DROP, bool RES, FwdMode MODE, bool SHIFT>
+cudaError_t launch_ring_as(const FwdParams<T>& p, int team, unsigned block, cudaStream_t stream) {
+    constexpr int V = 16 / sizeof(T);
+    // one wave: as many CTAs as run at a time (the answer is kept by CTA and team size)
+    static std::atomic<int> per_sm[17][6];
+    const auto kern = ln_fwd_ring_kernel<T, C, DROP, RES, MODE, SHIFT>;
+    const size_t smem = size_t(ring_rows(C, C * V, DROP, RES, MODE)) * (RES ? 2 : 1) * C * (block / 32) *
+                        warp_slots(SHIFT, MODE == NARROW ? team : 32) * 16;
+    int log_team = 0;
+    while ((1 << log_team) < team) ++log_team;
+    std::atomic<int>& known = per_sm[block / 32][log_team];
+    int n = known.load(std::memory_order_relaxed);
+    if (n == 0) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxRing);
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, static_cast<int>(block), smem);
+        if (e != cudaSuccess) return e;
+        n = std::max(n, 1);
+        known.store(n, std::memory_order_relaxed);
+    }
+    const int64_t rows = MODE == NARROW ? 128 / team : 1;
+    const int64_t grid = std::min<int64_t>((p.M + rows - 1) / rows, int64_t(n) * sm_count());
+    return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(block), smem, stream, p, team);
+}
+
+template <typename T, int C, FwdMode MODE, bool SHIFT>
+cudaError_t launch_ring(const FwdParams<T>& p, int team, unsigned block, cudaStream_t stream) {
+    if (p.drop.on)
+        return p.res ? launch_ring_as<T, C, true, true, MODE, SHIFT>(p, team, block, stream)
+                     : launch_ring_as<T, C, true, false, MODE, SHIFT>(p, team, block, stream);
+    return p.res ? launch_ring_as<T, C, false, true, MODE, SHIFT>(p, team, block, stream)
+                 : launch_ring_as<T, C, false, false, MODE, SHIFT>(p, team, block, stream);
+}
+
+}  // namespace
+
+// The one-pass kernels, where the row fits one; cudaErrorNotSupported where it does not.
+template <typename T, bool SHIFT>
+cudaError_t launch_fwd_ring(const FwdParams<T>& p, cudaStream_t stream) {
+    constexpr int V = 16 / sizeof(T), kMost = 32 / V;
+    const int64_t pieces = (p.N + V - 1) / V;
+    const int team = team_of(pieces);
+    switch (columns_of((pieces + team - 1) / team, SHIFT)) {
+        case 1: return launch_ring<T, 1, NARROW, SHIFT>(p, team, 128, stream);
+        case 2: return launch_ring<T, 2, NARROW, SHIFT>(p, team, 128, stream);
+        case 4: return launch_ring<T, 4, NARROW, SHIFT>(p, team, 128, stream);
+        case 8: return launch_ring<T, 8, NARROW, SHIFT>(p, team, 128, stream);
+        default: break;
+    }
+    if constexpr (!SHIFT) {
+        switch ((pieces + team - 1) / team) {
+            case 3: return launch_ring<T, 3, NARROW, SHIFT>(p, team, 128, stream);
+            case 5: return launch_ring<T, 5, NARROW, SHIFT>(p, team, 128, stream);
+            case 6: return launch_ring<T, 6, NARROW, SHIFT>(p, team, 128, stream);
+            case 7: return launch_ring<T, 7, NARROW, SHIFT>(p, team, 128, stream);
+            default: break;
+        }
+    }
+    if (pieces <= 256 * kMost) return launch_ring<T, kMost, WIDE, SHIFT>(p, 32, threads_of(pieces, kMost), stream);
+    if (pieces <= 512 * kMost) return launch_ring<T, kMost, BROAD, SHIFT>(p, 32, threads_of(pieces, kMost), stream);
+    return cudaErrorNotSupported;
+}
+
+}  // namespace fp8q

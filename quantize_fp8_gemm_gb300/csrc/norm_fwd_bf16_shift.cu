@@ -1,0 +1,4 @@
+// norm_fwd_bf16_shift.cu -- layer_norm_fwd's one-pass kernels for bf16, rows off the 16-byte grid.
+#include "norm_fwd.cuh"
+
+template cudaError_t fp8q::launch_fwd_ring<__nv_bfloat16, true>(const FwdParams<__nv_bfloat16>&, cudaStream_t);

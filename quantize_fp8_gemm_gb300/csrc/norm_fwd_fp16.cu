@@ -1,0 +1,4 @@
+// norm_fwd_fp16.cu -- layer_norm_fwd's one-pass kernels for fp16, rows on the 16-byte grid.
+#include "norm_fwd.cuh"
+
+template cudaError_t fp8q::launch_fwd_ring<__half, false>(const FwdParams<__half>&, cudaStream_t);

@@ -1,0 +1,4 @@
+// norm_fwd_fp32.cu -- layer_norm_fwd's one-pass kernels for fp32, rows on the 16-byte grid.
+#include "norm_fwd.cuh"
+
+template cudaError_t fp8q::launch_fwd_ring<float, false>(const FwdParams<float>&, cudaStream_t);

@@ -35,16 +35,17 @@ struct Params {
     const void* p;  // NULL: every value is `none`
     bool f32;
     float none;
+    bool aligned;   // on a 16-byte boundary
     __device__ __forceinline__ float at(int64_t j) const {
         if (p == nullptr) return none;
         return f32 ? static_cast<const float*>(p)[j] : to_f32(static_cast<const T*>(p)[j]);
     }
 };
 
-// V adjacent elements of a row: 16 bytes in one access, or one element.
+// V adjacent elements of a row, 16 bytes.
 template <typename T, int V>
 struct Piece {
-    static_assert(V * sizeof(T) == 16, "16-byte pieces or single elements");
+    static_assert(V * sizeof(T) == 16, "16-byte pieces");
     uint4 raw;
     __device__ __forceinline__ void load(const T* p) { raw = ld_stream_v4(p); }
     __device__ __forceinline__ void store(T* p) const { st_v4(p, raw); }
@@ -81,16 +82,6 @@ struct Piece {
         raw = make_uint4(u[0], u[1], u[2], u[3]);
     }
 };
-template <typename T>
-struct Piece<T, 1> {
-    T raw;
-    __device__ __forceinline__ void load(const T* p) { raw = *p; }
-    __device__ __forceinline__ void store(T* p) const { *p = raw; }
-    __device__ __forceinline__ void zero() { raw = from_f32<T>(0.0f); }
-    __device__ __forceinline__ void unpack(float (&v)[1]) const { v[0] = to_f32(raw); }
-    __device__ __forceinline__ void pack(const float (&v)[1]) { raw = from_f32<T>(v[0]); }
-};
-
 // Two float32 values in one 64-bit register pair; each lane of an operation is
 // the IEEE operation rounded once, at half the instructions.
 using f32x2 = uint64_t;
@@ -139,28 +130,138 @@ __device__ __forceinline__ void pack2(Piece<T, V>& q, const f32x2 (&v)[V / 2]) {
     q.pack(f);
 }
 
-// V parameters from column j (16-byte accesses need the vector 16-byte aligned).
-template <typename T, int V>
-__device__ __forceinline__ void load_params(const Params<T>& w, int64_t j, float (&v)[V]) {
+// V parameters from column j.  ANY: the vector may sit anywhere and end inside
+// the piece (n columns; those past it are 0), and goes element by element then.
+template <typename T, int V, bool ANY>
+__device__ __forceinline__ void load_params2(const Params<T>& w, int j, int n, f32x2 (&v)[V / 2]) {
+    float f[V];
     if (w.p == nullptr) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = w.none;
-    } else if constexpr (V == 1) {
-        v[0] = w.at(j);
+        for (int i = 0; i < V; ++i) f[i] = w.none;
+    } else if (ANY && (!w.aligned || j + V > n)) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] = j + i < n ? w.at(j + i) : 0.0f;
     } else if (w.f32) {
 #pragma unroll
         for (int i = 0; i < V; i += 4) {
-            const float4 f = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(w.p) + j + i));
-            v[i] = f.x;
-            v[i + 1] = f.y;
-            v[i + 2] = f.z;
-            v[i + 3] = f.w;
+            const float4 q = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(w.p) + j + i));
+            f[i] = q.x;
+            f[i + 1] = q.y;
+            f[i + 2] = q.z;
+            f[i + 3] = q.w;
         }
     } else {
         Piece<T, V> q;
         q.raw = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(w.p) + j));
-        q.unpack(v);
+        q.unpack(f);
     }
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) v[i] = pair_of(f[2 * i], f[2 * i + 1]);
+}
+
+// ------------------------------------------- rows off the 16-byte grid (SHIFT) --
+// A row that does not start on a 16-byte boundary is moved in the granules (16
+// aligned bytes) that it touches, and its pieces of V columns are cut from two
+// neighbouring ones, so the arithmetic and its order do not depend on where the
+// rows lie.  A granule that holds an element of the row is read whole; its other
+// bytes are not used.  Writes touch the row's own elements only.
+
+// Bytes mis .. mis + 15 of a:b (0 <= mis < 16; whole elements of 2 or 4 bytes).
+__device__ __forceinline__ uint4 cut16(uint4 a, uint4 b, uint32_t mis) {
+    uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    if (mis & 8) {
+#pragma unroll
+        for (int i = 0; i < 6; ++i) u[i] = u[i + 2];
+    }
+    if (mis & 4) {
+#pragma unroll
+        for (int i = 0; i < 5; ++i) u[i] = u[i + 1];
+    }
+    const uint32_t bits = (mis & 3) * 8;
+    return make_uint4(__funnelshift_r(u[0], u[1], bits), __funnelshift_r(u[1], u[2], bits),
+                      __funnelshift_r(u[2], u[3], bits), __funnelshift_r(u[3], u[4], bits));
+}
+
+// Bytes between a row's granule boundary and its first element.
+template <typename T>
+__device__ __forceinline__ uint32_t granule_offset(const T* start) {
+    return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(start) & 15);
+}
+// cp.async of granule k of the `bytes` bytes at start (nothing of it in the row:
+// zeros, and `base` for an address that is not read), and of granule k + 1 into
+// the next slot if `two`.
+template <typename T>
+__device__ __forceinline__ void copy_granules(uint4* slot, const T* base, const T* start, int k, int bytes, bool two) {
+    const int mis = static_cast<int>(granule_offset(start));
+    const uint8_t* first = reinterpret_cast<const uint8_t*>(start) - mis;
+    const int64_t at = static_cast<int64_t>(k) * 16;
+    // no bytes (a row past the last): nothing, although granule 0 of a shifted row begins before it
+    const bool has = bytes > 0 && at - mis < bytes, has2 = at + 16 - mis < bytes;
+    const uint8_t* none = reinterpret_cast<const uint8_t*>(base) - granule_offset(base);
+    cp_async16_or_zero(smem_u32(slot), has ? first + at : none, has);
+    if (two) cp_async16_or_zero(smem_u32(slot + 1), has2 ? first + at + 16 : none, has2);
+}
+// This lane's piece from the ring: its slot, or cut from its slot and the next.
+template <bool SHIFT>
+__device__ __forceinline__ uint4 read_piece(const uint4* slot, uint32_t mis) {
+    if constexpr (SHIFT) return cut16(slot[0], slot[1], mis);
+    return slot[0];
+}
+// Zero the columns from `valid` on.
+template <int V>
+__device__ __forceinline__ void zero_from(f32x2 (&v)[V / 2], int valid) {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+        const float2 f = split(v[i]);
+        v[i] = pair_of(2 * i < valid ? f.x : 0.0f, 2 * i + 1 < valid ? f.y : 0.0f);
+    }
+}
+
+// Elements lo .. hi - 1 of a piece, one by one, to dst + their index.
+template <typename T>
+__device__ __forceinline__ void store_elements(T* dst, uint4 q, int lo, int hi) {
+    constexpr int V = 16 / sizeof(T);
+    const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        if (i < lo || i >= hi) continue;
+        if constexpr (sizeof(T) == 4)
+            *reinterpret_cast<uint32_t*>(dst + i) = u[i];
+        else
+            *reinterpret_cast<uint16_t*>(dst + i) = static_cast<uint16_t>(u[i / 2] >> (16 * (i & 1)));
+    }
+}
+
+// Store a warp's pieces: this lane's is piece k of the row at `start`, with
+// `valid` elements (0: none; fewer than V only in the row's last piece).  The
+// lanes of a `team` hold adjacent pieces of one row.  All lanes of the warp call
+// it.  A lane writes the granule in which its piece begins, whose first bytes are
+// the end of the previous lane's piece; the first lane's granule and what is
+// left of the last piece go element by element.
+template <typename T>
+__device__ __forceinline__ void store_shifted(uint4 q, T* start, int k, int valid, int team) {
+    constexpr int V = 16 / sizeof(T);
+    uint4 prev;
+    prev.x = __shfl_up_sync(0xFFFFFFFFu, q.x, 1);
+    prev.y = __shfl_up_sync(0xFFFFFFFFu, q.y, 1);
+    prev.z = __shfl_up_sync(0xFFFFFFFFu, q.z, 1);
+    prev.w = __shfl_up_sync(0xFFFFFFFFu, q.w, 1);
+    const int place = threadIdx.x & (team - 1);
+    const int after = __shfl_down_sync(0xFFFFFFFFu, valid, 1);  // elements of the next lane's piece
+    if (valid == 0) return;
+    T* dst = start + static_cast<int64_t>(k) * V;
+    const uint32_t mis = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(start) & 15);
+    const int lead = (16 - static_cast<int>(mis)) / static_cast<int>(sizeof(T));  // of this piece in its first granule
+    if (mis == 0 && valid == V) {
+        st_v4(dst, q);
+    } else if (mis != 0 && place != 0 && valid >= lead) {
+        st_v4(reinterpret_cast<uint8_t*>(dst) - mis, cut16(prev, q, 16 - mis));
+    } else {
+        if (mis != 0 && place != 0) store_elements<T>(dst - V, prev, lead, V);
+        store_elements<T>(dst, q, 0, valid < lead ? valid : lead);
+    }
+    const bool next = place != team - 1 && after > 0;  // the next lane writes this piece's end
+    if (mis != 0 && !next) store_elements<T>(dst, q, lead, valid);
 }
 
 // ----------------------------------------------------------------- dropout --
@@ -171,31 +272,55 @@ __device__ __forceinline__ void load_params(const Params<T>& w, int64_t j, float
 // low, offset high), so a block gives the four words of columns 4j .. 4j + 3
 // of one row, and the mask depends on seed, offset, row and column alone:
 // not on the element type, the strides, the launch shape or the kernel.
+//
+// The 32 x 32 -> 64 bit products bound these kernels next to the memory (each
+// takes the multiply pipe four cycles a warp), so those that do not depend on
+// the block are formed once: round 1's second product (of the offset) per
+// thread, round 2's first one (of the row) per row.  Round 1's first product,
+// of the column quad, is linear in it: a caller adds kPhiloxM0 times a step
+// instead.  That leaves 17 of 20 products a block.
+constexpr uint64_t kPhiloxM0 = 0xD2511F53u, kPhiloxM1 = 0xCD9E8D57u;
+
 struct Philox {
-    uint32_t k0, k1, o0, o1;
+    uint32_t k0, k1, o1;
+    uint64_t off;           // M1 * (offset low half)
+    uint32_t a[9], b[9];    // the keys of rounds 2 .. 10
     Philox() = default;
     __device__ __forceinline__ explicit Philox(const uint64_t* rng) {
-        const uint64_t seed = rng[0], off = rng[1];
+        const uint64_t seed = rng[0], o = rng[1];
         k0 = static_cast<uint32_t>(seed);
         k1 = static_cast<uint32_t>(seed >> 32);
-        o0 = static_cast<uint32_t>(off);
-        o1 = static_cast<uint32_t>(off >> 32);
-    }
-    __device__ __forceinline__ uint4 block(uint32_t quad, uint32_t row) const {
-        uint32_t c0 = quad, c1 = row, c2 = o0, c3 = o1, a = k0, b = k1;
+        o1 = static_cast<uint32_t>(o >> 32);
+        off = kPhiloxM1 * static_cast<uint32_t>(o);
 #pragma unroll
-        for (int i = 0; i < 10; ++i) {
-            const uint64_t p0 = static_cast<uint64_t>(0xD2511F53u) * c0;
-            const uint64_t p1 = static_cast<uint64_t>(0xCD9E8D57u) * c2;
-            c0 = static_cast<uint32_t>(p1 >> 32) ^ c1 ^ a;
-            c2 = static_cast<uint32_t>(p0 >> 32) ^ c3 ^ b;
+        for (int i = 0; i < 9; ++i) {
+            a[i] = k0 + (i + 1) * 0x9E3779B9u;
+            b[i] = k1 + (i + 1) * 0xBB67AE85u;
+            // kept in registers: formed anew they are two additions a round of every block
+            asm volatile("" : "+r"(a[i]), "+r"(b[i]));
+        }
+    }
+    // Round 2's product of the row: a row's blocks share it.
+    __device__ __forceinline__ uint64_t row(uint32_t i) const {
+        return kPhiloxM0 * (static_cast<uint32_t>(off >> 32) ^ i ^ k0);
+    }
+    // The block of a column quad; quad_m0 = M0 * quad.
+    __device__ __forceinline__ uint4 block(uint64_t quad_m0, uint64_t row_m0) const {
+        const uint64_t p = kPhiloxM1 * (static_cast<uint32_t>(quad_m0 >> 32) ^ o1 ^ k1);
+        uint32_t c0 = static_cast<uint32_t>(p >> 32) ^ static_cast<uint32_t>(off) ^ a[0], c1 = static_cast<uint32_t>(p);
+        uint32_t c2 = static_cast<uint32_t>(row_m0 >> 32) ^ static_cast<uint32_t>(quad_m0) ^ b[0],
+                 c3 = static_cast<uint32_t>(row_m0);
+#pragma unroll
+        for (int i = 1; i < 9; ++i) {
+            const uint64_t p0 = kPhiloxM0 * c0, p1 = kPhiloxM1 * c2;
+            c0 = static_cast<uint32_t>(p1 >> 32) ^ c1 ^ a[i];
+            c2 = static_cast<uint32_t>(p0 >> 32) ^ c3 ^ b[i];
             c1 = static_cast<uint32_t>(p1);
             c3 = static_cast<uint32_t>(p0);
-            a += 0x9E3779B9u;
-            b += 0xBB67AE85u;
         }
         return make_uint4(c0, c1, c2, c3);
     }
+    __device__ __forceinline__ uint4 at(uint32_t quad, uint32_t i) const { return block(kPhiloxM0 * quad, row(i)); }
 };
 
 // Drop probability as the kernels use it.  An element is dropped when its word
@@ -231,20 +356,16 @@ __device__ __forceinline__ float dropped(float x, uint32_t word, const Dropout& 
     return word > d.last ? __fmul_rn(x, d.inv) : 0.0f;
 }
 
-// The generator words of the V columns from j of a row (V = 1: the word of column j).
+// The generator words of V columns whose first quad's M0 * quad is given.
 template <int V>
-__device__ __forceinline__ void words_at(const Philox& g, uint32_t j, uint32_t row, uint32_t (&w)[V]) {
-    if constexpr (V == 1) {
-        w[0] = word_of(g.block(j >> 2, row), j & 3);
-    } else {
+__device__ __forceinline__ void words_at(const Philox& g, uint64_t quad_m0, uint64_t row_m0, uint32_t (&w)[V]) {
 #pragma unroll
-        for (int i = 0; i < V; i += 4) {
-            const uint4 b = g.block((j + i) >> 2, row);
-            w[i] = b.x;
-            w[i + 1] = b.y;
-            w[i + 2] = b.z;
-            w[i + 3] = b.w;
-        }
+    for (int i = 0; i < V; i += 4) {
+        const uint4 b = g.block(quad_m0 + (i / 4) * kPhiloxM0, row_m0);
+        w[i] = b.x;
+        w[i + 1] = b.y;
+        w[i + 2] = b.z;
+        w[i + 3] = b.w;
     }
 }
 
@@ -265,31 +386,36 @@ __device__ __forceinline__ uint16_t cast_pair(float v0, float v1, int fmt) {
     return fmt == FP8Q_E5M2 ? cvt_fp8x2<FP8Q_E5M2>(v0, v1) : cvt_fp8x2<FP8Q_E4M3>(v0, v1);
 }
 
-// Scale and cast V values of the rounded output from a row's column j; folds
-// their magnitudes and saturations into amax / nsat.
+// Scale and cast the first `valid` of V values of the rounded output; folds their
+// magnitudes and saturations into amax / nsat.  `whole`: dst takes all V codes
+// in one store.
 template <typename T, int V>
-__device__ __forceinline__ void quant_piece(const QuantOut& o, float s, const Piece<T, V>& y, uint8_t* dst,
-                                            uint32_t& amax, uint32_t& nsat) {
+__device__ __forceinline__ void quant_piece(const QuantOut& o, float s, const Piece<T, V>& y, uint8_t* dst, int valid,
+                                            bool whole, uint32_t& amax, uint32_t& nsat) {
     float f[V], v[V];
     y.unpack(f);
     const float fmax = fp8_max_value(o.fmt);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         v[i] = __fmul_rn(f[i], s);
-        amax = max(amax, __float_as_uint(fabsf(f[i])));
-        nsat += fabsf(v[i]) > fmax;
+        if (i < valid) {
+            amax = max(amax, __float_as_uint(fabsf(f[i])));
+            nsat += fabsf(v[i]) > fmax;
+        }
     }
     if (dst == nullptr) return;
-    if constexpr (V == 1) {
-        *dst = static_cast<uint8_t>(cast_pair(v[0], 0.0f, o.fmt));
-    } else {
-        uint32_t q[V / 4];
+    uint32_t q[V / 4];
 #pragma unroll
-        for (int i = 0; i < V / 4; ++i)
-            q[i] = cast_pair(v[4 * i], v[4 * i + 1], o.fmt) |
-                   (static_cast<uint32_t>(cast_pair(v[4 * i + 2], v[4 * i + 3], o.fmt)) << 16);
+    for (int i = 0; i < V / 4; ++i)
+        q[i] = cast_pair(v[4 * i], v[4 * i + 1], o.fmt) |
+               (static_cast<uint32_t>(cast_pair(v[4 * i + 2], v[4 * i + 3], o.fmt)) << 16);
+    if (whole) {
         if constexpr (V == 8) st_v2(dst, make_uint2(q[0], q[1]));
         else *reinterpret_cast<uint32_t*>(dst) = q[0];
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (i < valid) dst[i] = static_cast<uint8_t>(q[i / 4] >> (8 * (i & 3)));
     }
 }
 
@@ -327,6 +453,24 @@ inline size_t dtype_size(int t) { return t == FP8Q_FP32 ? 4 : 2; }
 inline bool rows16(const void* p, int64_t ld, size_t es) {
     return p == nullptr || (aligned16(p) && (static_cast<uint64_t>(ld) * es) % 16 == 0);
 }
+// Granules that a warp holds of one piece index: with SHIFT one more a row.
+__host__ __device__ inline int warp_slots(bool shift, int team) { return shift ? 32 + 32 / team : 32; }
+// Pieces a lane of the kernel that takes so many: the number itself on the
+// 16-byte grid, the next power of two off it (half the kernels to build; the
+// surplus pieces are zeros and change no result).
+inline int64_t columns_of(int64_t c, bool shift) {
+    if (!shift) return c;
+    return c <= 2 ? c : c <= 4 ? 4 : c <= 8 ? 8 : c;
+}
+// Lanes of a warp that take a row of so many pieces: a power of two, 32 at most.
+inline int team_of(int64_t pieces) {
+    int team = 1;
+    while (team < 32 && team < pieces) team *= 2;
+    return team;
+}
+// Threads of a CTA that takes a row at c pieces a thread.
+inline unsigned threads_of(int64_t pieces, int c) { return static_cast<unsigned>((pieces + 32 * c - 1) / (32 * c)) * 32; }
+constexpr int kMaxRing = 208 * 1024;  // dynamic shared memory that a ring may take
 inline bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 // Sum over the CTA's threads of two values, in every thread; the order of the
