@@ -32,8 +32,8 @@ struct DropParams {
 // SHIFT: rows off the 16-byte grid (norm_ops.cuh); a lane loads the two granules
 // that hold its piece (the second from L1, where its neighbour brought it).
 template <typename T, bool RES, bool SHIFT>
-__global__ void __launch_bounds__(256) dropout_rows_kernel(const DropParams<T> p, int team, int chunks) {
-    constexpr int V = 16 / sizeof(T), U = 4;
+__global__ void __launch_bounds__(256, 4) dropout_rows_kernel(const DropParams<T> p, int team, int chunks) {
+    constexpr int V = 16 / sizeof(T), H = V / 2, U = 2;
     const int lane = threadIdx.x & 31;
     const int64_t N = p.N, pieces = SHIFT ? (N + V - 1) / V : N / V;
     const int64_t warp = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
@@ -65,6 +65,7 @@ __global__ void __launch_bounds__(256) dropout_rows_kernel(const DropParams<T> p
             return in ? ld_stream_v4(start + static_cast<int64_t>(k) * V) : make_uint4(0, 0, 0, 0);
         }
     };
+    const f32x2 inv2 = pair_of(p.drop.inv, p.drop.inv);
     for (int64_t base = first - lane / team; base < p.M; base += U * step) {
         Piece<T, V> x[U], r[U];
 #pragma unroll
@@ -79,21 +80,21 @@ __global__ void __launch_bounds__(256) dropout_rows_kernel(const DropParams<T> p
             const int64_t row = base + lane / team + u * step;
             const int valid = row < p.M ? valid_k : 0;
             if (!SHIFT && valid == 0) continue;
-            float v[V];
-            x[u].unpack(v);
+            f32x2 v[H];
+            unpack2(x[u], v);
             if (p.drop.on) {
                 uint32_t w[V];
                 words_at<V>(g, quad_m0, g.row(static_cast<uint32_t>(row)), w);
 #pragma unroll
-                for (int i = 0; i < V; ++i) v[i] = dropped(v[i], w[i], p.drop);
+                for (int i = 0; i < H; ++i) v[i] = dropped2(mul2(v[i], inv2), w[2 * i], w[2 * i + 1], p.drop);
             }
             if constexpr (RES) {
-                float f[V];
-                r[u].unpack(f);
+                f32x2 f[H];
+                unpack2(r[u], f);
 #pragma unroll
-                for (int i = 0; i < V; ++i) v[i] = __fadd_rn(f[i], v[i]);
+                for (int i = 0; i < H; ++i) v[i] = add2(f[i], v[i]);
             }
-            x[u].pack(v);
+            pack2(x[u], v);
             if constexpr (SHIFT) store_shifted<T>(x[u].raw, p.y + row * p.ldy, k, valid, team);
             else x[u].store(p.y + row * p.ldy + static_cast<int64_t>(k) * V);
         }

@@ -41,26 +41,34 @@ namespace {
 // copies and reads its own pieces only, so it waits for its own copies and no
 // barrier guards the ring.  SHIFT: rows off the 16-byte grid (norm_ops.cuh); a
 // lane then reads its own granule and the next lane's.
-// WIDE = false: `team` lanes (a power of two <= 32) of a warp take a row, up to
-// 64 columns a lane: the row's two sums are shuffles, and a row costs the fewest
-// instructions.  WIDE = true: a CTA takes a row, 32 columns a thread.
-__host__ __device__ constexpr int bwd_ring_rows(int C, bool wide) {
-    // what a CTA's shared memory holds: a stage is 48 C bytes a thread
-    return wide ? (C > 4 ? 1 : 2) : C > 4 ? 2 : 3;
+//   NARROW  `team` lanes (a power of two <= 32) of a warp take a row, up to 32
+//           columns a lane: the row's two sums are shuffles
+//   WIDE    a CTA of up to 256 threads takes a row, 32 columns a thread
+//   BROAD   the same with up to 512 threads, whose registers hold no weights
+enum BwdMode { NARROW, WIDE, BROAD };
+
+// Rows of the ring, a stage being 48 C bytes a thread: what a CTA's shared memory
+// holds of its widest row, or two or three CTAs a multiprocessor.
+__host__ __device__ constexpr int bwd_ring_rows(int C, BwdMode mode) {
+    return mode == BROAD ? (C > 4 ? 1 : 2) : C > 4 ? 2 : 3;
 }
 
-template <typename T, int C, bool WIDE, bool DROP, bool SHIFT>
-__global__ void __launch_bounds__(WIDE ? 512 : 128) ln_bwd_ring_kernel(const BwdParams<T> p, int team) {
+template <typename T, int C, BwdMode MODE, bool DROP, bool SHIFT>
+__global__ void __launch_bounds__(MODE == BROAD ? 512 : MODE == WIDE ? 256 : 128) ln_bwd_ring_kernel(const BwdParams<T> p, int team) {
     extern __shared__ uint4 s_ring[];  // [stage][dy, r, dresidual][c][slot]; at the end NARROW's partial row
-    __shared__ float2 s_sum[2][16];
-    constexpr int V = 16 / sizeof(T), H = V / 2, S = bwd_ring_rows(C, WIDE);
-    constexpr bool kHeld = !WIDE && C * V <= 32;  // weights in registers; otherwise from L1 in every row
+    __shared__ __align__(16) float2 s_sum[2][16];
+    constexpr int V = 16 / sizeof(T), H = V / 2, S = bwd_ring_rows(C, MODE);
+    constexpr bool kHeld = MODE != BROAD, kCta = MODE != NARROW;  // weights in registers; otherwise from L1 in every row
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-    const int t = WIDE ? threadIdx.x : lane & (team - 1);
-    const int span = WIDE ? blockDim.x : team;
+    if constexpr (C > 1) team = 32;
+    const int t = kCta ? threadIdx.x : lane & (team - 1);
+    const int span = kCta ? blockDim.x : team;
     const int N = static_cast<int>(p.N), pieces = SHIFT ? (N + V - 1) / V : N / V;
     const float inv_n = 1.0f / static_cast<float>(N);
     const f32x2 zero2 = pair_of(0.0f, 0.0f);
+    // whether this thread's piece c lies in the row: all but the last of a warp's do
+    auto has = [&](int c) { return (!kCta && !SHIFT && c < C - 1) || t + c * span < pieces; };
+    auto count = [&](int c) { return SHIFT ? min(V, N - (t + c * span) * V) : V; };  // of its elements, where it does
     pdl_wait();
 
     f32x2 w[kHeld ? C : 1][H], dw[C][H], db[C][H];
@@ -71,38 +79,38 @@ __global__ void __launch_bounds__(WIDE ? 512 : 128) ln_bwd_ring_kernel(const Bwd
         if constexpr (kHeld) {
 #pragma unroll
             for (int i = 0; i < H; ++i) w[c][i] = zero2;
-            if (t + c * span < pieces) load_params2<T, V, SHIFT>(p.w, (t + c * span) * V, N, w[c]);
+            if (has(c)) load_params2<T, V, SHIFT>(p.w, (t + c * span) * V, N, w[c]);
         }
     }
     Philox g;
     if constexpr (DROP) g = Philox(p.drop.rng);
     const uint64_t first_m0 = kPhiloxM0 * static_cast<uint32_t>(t * (V / 4));
 
-    const int rows_warp = WIDE ? 1 : 32 / team, rows_cta = WIDE ? 1 : rows_warp * nw;
+    const int rows_warp = kCta ? 1 : 32 / team, rows_cta = kCta ? 1 : rows_warp * nw;
     const int64_t stride = static_cast<int64_t>(gridDim.x) * rows_cta;
     const int64_t base0 = static_cast<int64_t>(blockIdx.x) * rows_cta;
-    const int64_t sub = WIDE ? 0 : warp * rows_warp + lane / team;
+    const int64_t sub = kCta ? 0 : warp * rows_warp + lane / team;
 
-    const int slots = warp_slots(SHIFT, WIDE ? 32 : team);
-    const int my_slot = warp * slots + lane + (SHIFT && !WIDE ? lane / team : 0);
+    const int slots = warp_slots(SHIFT, kCta ? 32 : team);
+    const int my_slot = warp * slots + lane + (SHIFT && !kCta ? lane / team : 0);
     auto slot = [&](int stage, int tensor, int c) { return s_ring + ((stage * 3 + tensor) * C + c) * (nw * slots) + my_slot; };
-    const bool team_end = SHIFT && (WIDE ? lane == 31 : t == team - 1);
-    auto fill_one = [&](int stage, int tensor, int c, const T* x, int64_t ld, int64_t row) {
-        const int k = t + c * span;
-        if constexpr (SHIFT)
-            copy_granules(slot(stage, tensor, c), x, x + row * ld, k, row < p.M ? N * static_cast<int>(sizeof(T)) : 0, team_end);
-        else {
-            const bool in = row < p.M && k < pieces;
-            cp_async16_or_zero(smem_u32(slot(stage, tensor, c)), in ? x + row * ld + k * V : x, in);
-        }
-    };
-    // pieces past the row, and rows past the last, are zeros
-    auto fill = [&](int stage, int64_t row) {
+    const bool team_end = SHIFT && (kCta ? lane == 31 : t == team - 1);
+    auto fill_tensor = [&](int stage, int tensor, const T* x, int64_t ld, int64_t row) {
+        const T* start = x + row * ld;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            fill_one(stage, 0, c, p.dy, p.ld_dy, row);
-            fill_one(stage, 1, c, p.r, p.ld_r, row);
-            if (p.dres) fill_one(stage, 2, c, p.dres, p.ld_dres, row);
+            if constexpr (SHIFT)
+                copy_granules(slot(stage, tensor, c), x, start, t + c * span, N * static_cast<int>(sizeof(T)), team_end);
+            else if (has(c))
+                cp_async16(smem_u32(slot(stage, tensor, c)), start + t * V + c * span * V);
+        }
+    };
+    // the pieces of a row; nothing for a row past the last, which nothing is taken from
+    auto fill = [&](int stage, int64_t row) {
+        if (row < p.M) {
+            fill_tensor(stage, 0, p.dy, p.ld_dy, row);
+            fill_tensor(stage, 1, p.r, p.ld_r, row);
+            if (p.dres) fill_tensor(stage, 2, p.dres, p.ld_dres, row);
         }
         cp_async_commit();
     };
@@ -110,13 +118,18 @@ __global__ void __launch_bounds__(WIDE ? 512 : 128) ln_bwd_ring_kernel(const Bwd
     for (int k = 0; k < S - 1; ++k) fill(k, base0 + sub + k * stride);
     float mean = base0 + sub < p.M ? p.mean[base0 + sub] : 0.0f;
     float rstd = base0 + sub < p.M ? p.rstd[base0 + sub] : 0.0f;
-    if constexpr (WIDE) {
+    if constexpr (kCta) {
         if (threadIdx.x < 32) s_sum[threadIdx.x >> 4][threadIdx.x & 15] = make_float2(0.0f, 0.0f);
         __syncthreads();
     }
+    const f32x2 inv2 = pair_of(p.drop.inv, p.drop.inv);
     int buf = 0, stage = 0;
-    for (int64_t base = base0; base < p.M; base += stride) {
+    // where a warp takes one row, it is done at its own last; where it shares a barrier or
+    // its lanes take several, at the CTA's
+    constexpr bool kOwnEnd = !kCta && C > 1;
+    for (int64_t base = base0; (kOwnEnd ? base + sub : base) < p.M; base += stride) {
         const int64_t row = base + sub, ahead = row + stride;
+        const bool in = kOwnEnd || kCta || row < p.M;
         const float mean_next = ahead < p.M ? p.mean[ahead] : 0.0f, rstd_next = ahead < p.M ? p.rstd[ahead] : 0.0f;
         fill(stage == 0 ? S - 1 : stage - 1, row + (S - 1) * stride);
         cp_async_wait<S - 1>();
@@ -132,9 +145,9 @@ __global__ void __launch_bounds__(WIDE ? 512 : 128) ln_bwd_ring_kernel(const Bwd
             unpack2(a, dy);
             a.raw = read_piece<SHIFT>(slot(stage, 1, c), mis_r);
             unpack2(a, xhat);
-            if (SHIFT && (t + c * span) * V + V > N) {  // the row's end: what follows in the granule is not its own
-                zero_from<V>(dy, N - (t + c * span) * V);
-                zero_from<V>(xhat, N - (t + c * span) * V);
+            if (SHIFT && count(c) < V) {  // the row's end: what follows in the granule is not its own
+                zero_from<V>(dy, count(c));
+                zero_from<V>(xhat, count(c));
             }
             f32x2 wl[H];
             if constexpr (!kHeld) load_params2<T, V, SHIFT>(p.w, (t + c * span) * V, N, wl);
@@ -147,7 +160,7 @@ __global__ void __launch_bounds__(WIDE ? 512 : 128) ln_bwd_ring_kernel(const Bwd
         f32x2 c1v = zero2, c2v = zero2;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            if (t + c * span >= pieces) continue;
+            if (!in || !has(c)) continue;
             f32x2 dy[H], xhat[H], gw[H];
             inputs(c, dy, xhat, gw);
 #pragma unroll
@@ -160,33 +173,33 @@ __global__ void __launch_bounds__(WIDE ? 512 : 128) ln_bwd_ring_kernel(const Bwd
         }
         const float2 h1 = split(c1v), h2 = split(c2v);
         float c1 = h1.x + h1.y, c2 = h2.x + h2.y;
-        for (int o = (WIDE ? 32 : team) / 2; o; o >>= 1) {
+        for (int o = (kCta ? 32 : team) / 2; o; o >>= 1) {
             c1 += __shfl_xor_sync(0xFFFFFFFFu, c1, o);
             c2 += __shfl_xor_sync(0xFFFFFFFFu, c2, o);
         }
-        if constexpr (WIDE) {
+        if constexpr (kCta) {
             // two buffers: a warp that runs ahead writes the other one, and cannot reach this one
             // again before every warp has passed the next row's barrier
             if (lane == 0) s_sum[buf][warp] = make_float2(c1, c2);
             __syncthreads();
             c1 = c2 = 0.0f;
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {  // absent warps are zeros
-                const float2 f = s_sum[buf][k];
-                c1 += f.x;
-                c2 += f.y;
+            for (int k = 0; k < nw; k += 2) {  // absent warps are zeros
+                const float4 f = *reinterpret_cast<const float4*>(&s_sum[buf][k]);
+                c1 += f.x + f.z;
+                c2 += f.y + f.w;
             }
             buf ^= 1;
         }
         c1 *= -inv_n;
         c2 *= -inv_n;
+        T* dx_row = p.dx + row * p.ld_dx;
+        T* db_row = p.dbranch + row * p.ld_db;
         const f32x2 c1n = pair_of(c1, c1), c2n = pair_of(c2, c2);
         uint64_t row_m0 = 0;
         if constexpr (DROP) row_m0 = g.row(static_cast<uint32_t>(row));
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const int k = t + c * span;
-            const int valid = row < p.M && k < pieces ? (SHIFT ? min(V, N - k * V) : V) : 0;
+            const int valid = in && has(c) ? count(c) : 0;
             if (!SHIFT && valid == 0) continue;
             f32x2 dy[H], xhat[H], d[H];
             Piece<T, V> out;
@@ -205,23 +218,18 @@ __global__ void __launch_bounds__(WIDE ? 512 : 128) ln_bwd_ring_kernel(const Bwd
                 }
                 pack2(out, d);
             }
-            if constexpr (SHIFT) store_shifted<T>(out.raw, p.dx + row * p.ld_dx, k, valid, WIDE ? 32 : team);
-            else out.store(p.dx + row * p.ld_dx + k * V);
+            if constexpr (SHIFT) store_shifted<T>(out.raw, dx_row, t + c * span, valid, kCta ? 32 : team);
+            else out.store(dx_row + t * V + c * span * V);
             if (p.dbranch) {
                 if constexpr (DROP) {
                     uint32_t words[V];
                     words_at<V>(g, first_m0 + kPhiloxM0 * static_cast<uint32_t>(c * span * (V / 4)), row_m0, words);
-                    float f[V];
 #pragma unroll
-                    for (int i = 0; i < H; ++i) {
-                        const float2 e = split(d[i]);
-                        f[2 * i] = dropped(e.x, words[2 * i], p.drop);
-                        f[2 * i + 1] = dropped(e.y, words[2 * i + 1], p.drop);
-                    }
-                    out.pack(f);
+                    for (int i = 0; i < H; ++i) d[i] = dropped2(mul2(d[i], inv2), words[2 * i], words[2 * i + 1], p.drop);
+                    pack2(out, d);
                 }
-                if constexpr (SHIFT) store_shifted<T>(out.raw, p.dbranch + row * p.ld_db, k, valid, WIDE ? 32 : team);
-                else out.store(p.dbranch + row * p.ld_db + k * V);
+                if constexpr (SHIFT) store_shifted<T>(out.raw, db_row, t + c * span, valid, kCta ? 32 : team);
+                else out.store(db_row + t * V + c * span * V);
             }
         }
         mean = mean_next;
@@ -234,7 +242,7 @@ __global__ void __launch_bounds__(WIDE ? 512 : 128) ln_bwd_ring_kernel(const Bwd
     if (p.part == nullptr) return;
 
     float* part = p.part + static_cast<int64_t>(blockIdx.x) * 2 * p.N;
-    if constexpr (!WIDE) {
+    if constexpr (!kCta) {
         // lanes of the warp that took other rows of the same columns, then the warps in order
         float* s_part = reinterpret_cast<float*>(s_ring);
         for (int k = 0; k < nw; ++k) {
@@ -274,12 +282,12 @@ __global__ void __launch_bounds__(WIDE ? 512 : 128) ln_bwd_ring_kernel(const Bwd
     }
 }
 
-template <typename T, int C, bool WIDE, bool DROP, bool SHIFT>
+template <typename T, int C, BwdMode MODE, bool DROP, bool SHIFT>
 cudaError_t launch_ring_as(BwdParams<T>& p, int team, unsigned block, cudaStream_t stream) {
     // one wave: as many CTAs as run at a time (the answer is kept by CTA and team size)
     static std::atomic<int> per_sm[17][6];
-    const auto kern = ln_bwd_ring_kernel<T, C, WIDE, DROP, SHIFT>;
-    const size_t smem = size_t(bwd_ring_rows(C, WIDE)) * 3 * C * (block / 32) * warp_slots(SHIFT, team) * 16;
+    const auto kern = ln_bwd_ring_kernel<T, C, MODE, DROP, SHIFT>;
+    const size_t smem = size_t(bwd_ring_rows(C, MODE)) * 3 * C * (block / 32) * warp_slots(SHIFT, team) * 16;
     int log_team = 0;
     while ((1 << log_team) < team) ++log_team;
     std::atomic<int>& known = per_sm[block / 32][log_team];
@@ -295,10 +303,10 @@ cudaError_t launch_ring_as(BwdParams<T>& p, int team, unsigned block, cudaStream
     return launch_pdl(kern, dim3(p.parts), dim3(block), smem, stream, p, team);
 }
 
-template <typename T, int C, bool WIDE, bool SHIFT>
+template <typename T, int C, BwdMode MODE, bool SHIFT>
 cudaError_t launch_ring(BwdParams<T>& p, int team, unsigned block, cudaStream_t stream) {
-    return p.drop.on && p.dbranch ? launch_ring_as<T, C, WIDE, true, SHIFT>(p, team, block, stream)
-                                  : launch_ring_as<T, C, WIDE, false, SHIFT>(p, team, block, stream);
+    return p.drop.on && p.dbranch ? launch_ring_as<T, C, MODE, true, SHIFT>(p, team, block, stream)
+                                  : launch_ring_as<T, C, MODE, false, SHIFT>(p, team, block, stream);
 }
 
 }  // namespace
@@ -310,26 +318,29 @@ cudaError_t launch_bwd_ring(BwdParams<T>& p, cudaStream_t stream) {
     constexpr int V = 16 / sizeof(T);
     const int64_t pieces = (p.N + V - 1) / V;
     const int team = team_of(pieces);
-    switch (columns_of((pieces + team - 1) / team, SHIFT)) {
-        case 1: return launch_ring<T, 1, false, SHIFT>(p, team, 128, stream);
-        case 2: return launch_ring<T, 2, false, SHIFT>(p, team, 128, stream);
-        case 4: return launch_ring<T, 4, false, SHIFT>(p, team, 128, stream);
-        case 8: return launch_ring<T, 8, false, SHIFT>(p, team, 128, stream);
-        default: break;
-    }
-    if constexpr (!SHIFT) {
-        switch ((pieces + team - 1) / team) {
-            case 3: return launch_ring<T, 3, false, SHIFT>(p, team, 128, stream);
-            case 5: return launch_ring<T, 5, false, SHIFT>(p, team, 128, stream);
-            case 6: return launch_ring<T, 6, false, SHIFT>(p, team, 128, stream);
-            case 7: return launch_ring<T, 7, false, SHIFT>(p, team, 128, stream);
+    constexpr int kMost = 32 / V;
+    const int64_t c = columns_of((pieces + team - 1) / team, SHIFT);
+    if (c <= kMost) {
+        switch (c) {
+            case 1: return launch_ring<T, 1, NARROW, SHIFT>(p, team, 128, stream);
+            case 2: return launch_ring<T, 2, NARROW, SHIFT>(p, team, 128, stream);
+            case 4: return launch_ring<T, 4, NARROW, SHIFT>(p, team, 128, stream);
             default: break;
         }
+        if constexpr (V == 4) {
+            if (c == 8) return launch_ring<T, 8, NARROW, SHIFT>(p, team, 128, stream);
+        }
+        if constexpr (!SHIFT) {
+            if (c == 3) return launch_ring<T, 3, NARROW, SHIFT>(p, team, 128, stream);
+            if constexpr (V == 4) {
+                if (c == 5) return launch_ring<T, 5, NARROW, SHIFT>(p, team, 128, stream);
+                if (c == 6) return launch_ring<T, 6, NARROW, SHIFT>(p, team, 128, stream);
+                if (c == 7) return launch_ring<T, 7, NARROW, SHIFT>(p, team, 128, stream);
+            }
+        }
     }
-    if (pieces <= 512 * 4) return launch_ring<T, 4, true, SHIFT>(p, 32, threads_of(pieces, 4), stream);
-    if constexpr (V == 4) {
-        if (pieces <= 512 * 8) return launch_ring<T, 8, true, SHIFT>(p, 32, threads_of(pieces, 8), stream);
-    }
+    if (pieces <= 256 * kMost) return launch_ring<T, kMost, WIDE, SHIFT>(p, 32, threads_of(pieces, kMost), stream);
+    if (pieces <= 512 * kMost) return launch_ring<T, kMost, BROAD, SHIFT>(p, 32, threads_of(pieces, kMost), stream);
     return cudaErrorNotSupported;
 }
 

@@ -68,27 +68,30 @@ ln_fwd_ring_kernel(const FwdParams<T> p, int team) {
     constexpr int S = ring_rows(C, C * V, DROP, RES, MODE);
     constexpr bool kHeld = weights_held(C * V, DROP, MODE), kCta = MODE != NARROW;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    if constexpr (C > 1) team = 32;
     const int t = kCta ? threadIdx.x : lane & (team - 1);
     const int span = kCta ? blockDim.x : team;
     const int N = static_cast<int>(p.N), pieces = SHIFT ? (N + V - 1) / V : N / V;
     const float inv_n = 1.0f / static_cast<float>(N);
     const f32x2 zero2 = pair_of(0.0f, 0.0f);
+    // whether this thread's piece c lies in the row: all but the last of a warp's do
+    auto has = [&](int c) { return (MODE == NARROW && !SHIFT && c < C - 1) || t + c * span < pieces; };
+    auto count = [&](int c) { return SHIFT ? min(V, N - (t + c * span) * V) : V; };  // of its elements, where it does
     pdl_wait();
 
     f32x2 w[kHeld ? C : 1][H], b[kHeld ? C : 1][H];
     int own = 0;  // elements of this thread; of this warp later
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-        const int k = t + c * span;
         if constexpr (kHeld) {
 #pragma unroll
             for (int i = 0; i < H; ++i) w[c][i] = b[c][i] = zero2;
         }
-        if (k >= pieces) continue;
-        own += SHIFT ? min(V, N - k * V) : V;
+        if (!has(c)) continue;
+        own += count(c);
         if constexpr (kHeld) {
-            load_params2<T, V, SHIFT>(p.w, k * V, N, w[c]);
-            load_params2<T, V, SHIFT>(p.b, k * V, N, b[c]);
+            load_params2<T, V, SHIFT>(p.w, (t + c * span) * V, N, w[c]);
+            load_params2<T, V, SHIFT>(p.b, (t + c * span) * V, N, b[c]);
         }
     }
     float inv_own = inv_n;  // 1 / (elements whose mean a warp forms)
@@ -114,30 +117,41 @@ ln_fwd_ring_kernel(const FwdParams<T> p, int team) {
         return s_ring + ((stage * TENSORS + tensor) * C + c) * (nw * slots) + my_slot;
     };
     const bool team_end = SHIFT && (kCta ? lane == 31 : t == team - 1);
-    auto fill_one = [&](int stage, int tensor, int c, const T* x, int64_t ld, int64_t row) {
-        const int k = t + c * span;
-        if constexpr (SHIFT)
-            copy_granules(slot(stage, tensor, c), x, x + row * ld, k, row < p.M ? N * static_cast<int>(sizeof(T)) : 0, team_end);
-        else {
-            const bool in = row < p.M && k < pieces;
-            cp_async16_or_zero(smem_u32(slot(stage, tensor, c)), in ? x + row * ld + k * V : x, in);
-        }
-    };
-    // pieces past the row, and rows past the last, are zeros
-    auto fill = [&](int stage, int64_t row) {
+    auto fill_tensor = [&](int stage, int tensor, const T* x, int64_t ld, int64_t row) {
+        const T* start = x + row * ld;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            fill_one(stage, 0, c, p.x, p.ldx, row);
-            if constexpr (RES) fill_one(stage, 1, c, p.res, p.ld_res, row);
+            if constexpr (SHIFT)
+                copy_granules(slot(stage, tensor, c), x, start, t + c * span, N * static_cast<int>(sizeof(T)), team_end);
+            else if (has(c))
+                cp_async16(smem_u32(slot(stage, tensor, c)), start + t * V + c * span * V);
+        }
+    };
+    // the pieces of a row; nothing for a row past the last, whose results are not used
+    auto fill = [&](int stage, int64_t row) {
+        if (row < p.M) {
+            fill_tensor(stage, 0, p.x, p.ldx, row);
+            if constexpr (RES) fill_tensor(stage, 1, p.res, p.ld_res, row);
         }
         cp_async_commit();
     };
+    if constexpr (!SHIFT) {  // pieces past the row are zeros in every stage, and stay so
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+            if (!has(c))
+                for (int k = 0; k < S * TENSORS; ++k) *slot(k / TENSORS, k % TENSORS, c) = make_uint4(0, 0, 0, 0);
+    }
 #pragma unroll
     for (int k = 0; k < S - 1; ++k) fill(k, base0 + sub + k * stride);
 
+    const f32x2 inv2 = pair_of(p.drop.inv, p.drop.inv);
     int stage = 0, buf = 0;
-    for (int64_t base = base0; base < p.M; base += stride) {
+    // where a warp takes one row, it is done at its own last; where it shares a barrier or
+    // its lanes take several, at the CTA's
+    constexpr bool kOwnEnd = MODE == NARROW && C > 1;
+    for (int64_t base = base0; (kOwnEnd ? base + sub : base) < p.M; base += stride) {
         const int64_t row = base + sub;
+        const bool in = kOwnEnd || kCta || row < p.M;
         fill(stage == 0 ? S - 1 : stage - 1, row + (S - 1) * stride);
         cp_async_wait<S - 1>();
         if constexpr (SHIFT) __syncwarp();
@@ -145,39 +159,38 @@ ln_fwd_ring_kernel(const FwdParams<T> p, int team) {
         if constexpr (DROP) row_m0 = g.row(static_cast<uint32_t>(row));
         const uint32_t mis_x = SHIFT ? granule_offset(p.x + row * p.ldx) : 0;
         const uint32_t mis_r = SHIFT && RES ? granule_offset(p.res + row * p.ld_res) : 0;
+        T* r_row = p.r_out + row * p.ld_r;
         f32x2 v[C][H], sum2 = zero2;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const int k = t + c * span;
-            const int valid = SHIFT ? (k < pieces ? min(V, N - k * V) : 0) : V;
             Piece<T, V> a;
             a.raw = read_piece<SHIFT>(slot(stage, 0, c), mis_x);
             if constexpr (DROP || RES) {
-                float f[V];
-                a.unpack(f);
+                unpack2(a, v[c]);
                 if constexpr (DROP) {
                     uint32_t words[V];
                     words_at<V>(g, first_m0 + kPhiloxM0 * static_cast<uint32_t>(c * span * (V / 4)), row_m0, words);
 #pragma unroll
-                    for (int i = 0; i < V; ++i) f[i] = dropped(f[i], words[i], p.drop);
+                    for (int i = 0; i < H; ++i) v[c][i] = dropped2(mul2(v[c][i], inv2), words[2 * i], words[2 * i + 1], p.drop);
                 }
                 if constexpr (RES) {
                     Piece<T, V> r;
                     r.raw = read_piece<SHIFT>(slot(stage, 1, c), mis_r);
-                    unpack2(r, v[c]);
+                    f32x2 f[H];
+                    unpack2(r, f);
 #pragma unroll
-                    for (int i = 0; i < H; ++i) v[c][i] = add2(v[c][i], pair_of(f[2 * i], f[2 * i + 1]));
-                    pack2(a, v[c]);
-                } else {
-                    a.pack(f);
+                    for (int i = 0; i < H; ++i) v[c][i] = add2(f[i], v[c][i]);
                 }
+                pack2(a, v[c]);
                 if (p.r_out) {
-                    if constexpr (SHIFT) store_shifted<T>(a.raw, p.r_out + row * p.ld_r, k, row < p.M ? valid : 0, kCta ? 32 : team);
-                    else if (row < p.M && k < pieces) a.store(p.r_out + row * p.ld_r + k * V);
+                    if constexpr (SHIFT) store_shifted<T>(a.raw, r_row, t + c * span, in && has(c) ? count(c) : 0, kCta ? 32 : team);
+                    else if (in && has(c)) a.store(r_row + t * V + c * span * V);
                 }
             }
             unpack2(a, v[c]);
-            if (SHIFT && valid < V) zero_from<V>(v[c], valid);
+            if constexpr (SHIFT) {
+                if (t + c * span >= pieces || count(c) < V) zero_from<V>(v[c], t + c * span < pieces ? count(c) : 0);
+            }
             f32x2 part = add2(v[c][0], v[c][1]);
             if constexpr (H == 4) part = add2(part, add2(v[c][2], v[c][3]));
             sum2 = add2(sum2, part);
@@ -190,12 +203,11 @@ ln_fwd_ring_kernel(const FwdParams<T> p, int team) {
         f32x2 shift = pair_of(-mean, -mean), dev2[2] = {zero2, zero2};
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const int k = t + c * span;
-            if (k >= pieces) continue;
+            if (!has(c)) continue;
             f32x2 d[H];
 #pragma unroll
             for (int i = 0; i < H; ++i) d[i] = add2(v[c][i], shift);
-            if (SHIFT && k * V + V > N) zero_from<V>(d, N - k * V);
+            if (SHIFT && count(c) < V) zero_from<V>(d, count(c));
 #pragma unroll
             for (int i = 0; i < H; ++i) {
                 if constexpr (!kCta) v[c][i] = d[i];
@@ -227,16 +239,17 @@ ln_fwd_ring_kernel(const FwdParams<T> p, int team) {
         }
         const float rstd = 1.0f / sqrtf(__fmaf_rn(dev, inv_n, p.eps));
         const f32x2 scale = pair_of(rstd, rstd);
+        T* y_row = p.y + row * p.ldy;
+        uint8_t* q_row = p.quant.q + row * p.N;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const int k = t + c * span;
-            const int valid = row < p.M && k < pieces ? (SHIFT ? min(V, N - k * V) : V) : 0;
+            const int valid = in && has(c) ? count(c) : 0;
             if (!SHIFT && valid == 0) continue;
             f32x2 wl[H], bl[H];
             if constexpr (!kHeld) {
                 if (valid > 0) {
-                    load_params2<T, V, SHIFT>(p.w, k * V, N, wl);
-                    load_params2<T, V, SHIFT>(p.b, k * V, N, bl);
+                    load_params2<T, V, SHIFT>(p.w, (t + c * span) * V, N, wl);
+                    load_params2<T, V, SHIFT>(p.b, (t + c * span) * V, N, bl);
                 }
             }
 #pragma unroll
@@ -247,11 +260,11 @@ ln_fwd_ring_kernel(const FwdParams<T> p, int team) {
             Piece<T, V> y;
             pack2(y, v[c]);
             if (p.y) {
-                if constexpr (SHIFT) store_shifted<T>(y.raw, p.y + row * p.ldy, k, valid, kCta ? 32 : team);
-                else y.store(p.y + row * p.ldy + k * V);
+                if constexpr (SHIFT) store_shifted<T>(y.raw, y_row, t + c * span, valid, kCta ? 32 : team);
+                else y.store(y_row + t * V + c * span * V);
             }
             if (p.quant.on && valid > 0) {
-                uint8_t* dst = p.quant.q ? p.quant.q + row * p.N + k * V : nullptr;
+                uint8_t* dst = p.quant.q ? q_row + t * V + c * span * V : nullptr;
                 const bool whole = !SHIFT || (valid == V && (reinterpret_cast<uintptr_t>(dst) & (V - 1)) == 0);
                 if constexpr (std::is_same<T, __nv_bfloat16>::value) {
                     if (whole) {
@@ -263,7 +276,7 @@ ln_fwd_ring_kernel(const FwdParams<T> p, int team) {
                 quant_piece<T, V>(p.quant, s, y, dst, valid, whole, amax, nsat);
             }
         }
-        if (row < p.M && t == 0) {
+        if (in && t == 0) {
             if (p.mean) p.mean[row] = mean;
             if (p.rstd) p.rstd[row] = rstd;
         }

@@ -369,6 +369,12 @@ __device__ __forceinline__ void words_at(const Philox& g, uint64_t quad_m0, uint
     }
 }
 
+// A pair of products x * inv, 0 where dropped.
+__device__ __forceinline__ f32x2 dropped2(f32x2 scaled, uint32_t word0, uint32_t word1, const Dropout& d) {
+    const float2 f = split(scaled);
+    return pair_of(word0 > d.last ? f.x : 0.0f, word1 > d.last ? f.y : 0.0f);
+}
+
 // -------------------------------------------------------- quantize epilogue --
 // The framework's cast of the rounded output: v = y * s, q = FP8(v), max |y|
 // (as float32 bits: those of non-negative floats order like the values, and a
