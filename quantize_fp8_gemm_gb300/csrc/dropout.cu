@@ -28,22 +28,27 @@ struct DropParams {
 
 // A warp takes 32 adjacent pieces of a row (or, where a row has fewer, 32 / team
 // rows), the same columns of every row that it comes to: the generator's
-// products of the columns are formed once.  U rows are in flight a warp.
-// SHIFT: rows off the 16-byte grid (norm_ops.cuh); a lane loads the two granules
-// that hold its piece (the second from L1, where its neighbour brought it).
+// products of the columns are formed once.  The next rows' pieces are in flight
+// in a ring of kRing rows in shared memory (norm_fwd.cuh); the generator is what
+// bounds this kernel beside the memory, so no register holds a load in flight.
+// SHIFT: rows off the 16-byte grid (norm_ops.cuh).
+constexpr int kRing = 4;
+
 template <typename T, bool RES, bool SHIFT>
 __global__ void __launch_bounds__(256, 4) dropout_rows_kernel(const DropParams<T> p, int team, int chunks) {
-    constexpr int V = 16 / sizeof(T), H = V / 2, U = 2;
+    constexpr int V = 16 / sizeof(T), H = V / 2, kSlots = warp_slots(SHIFT, true), kStage = (RES ? 2 : 1) * kSlots;
+    extern __shared__ uint4 s_ring[];  // [warp][stage][x, residual][slot]
     const int lane = threadIdx.x & 31;
     const int64_t N = p.N, pieces = SHIFT ? (N + V - 1) / V : N / V;
     const int64_t warp = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
     const int64_t warps = static_cast<int64_t>(gridDim.x) * blockDim.x >> 5;
-    const int k = static_cast<int>(warp % chunks) * 32 + (lane & (team - 1));
+    const int place = lane & (team - 1);
+    const int first = static_cast<int>(warp % chunks) * 32;  // the warp's first piece
     const int rows_warp = 32 / team;
     const int64_t step = warps / chunks * rows_warp;  // rows that all warps of a chunk take at a time
-    const int64_t first = warp / chunks * rows_warp + lane / team;
-    const int64_t left = N - static_cast<int64_t>(k) * V;  // columns from this thread's first
-    const int valid_k = k < pieces ? (left < V ? static_cast<int>(left) : V) : 0;
+    const int64_t left = N - static_cast<int64_t>(first + place) * V;  // columns from this thread's first
+    const int valid_k = left <= 0 ? 0 : left < V ? static_cast<int>(left) : V;
+    uint4* const ring = s_ring + (threadIdx.x >> 5) * (kRing * kStage) + lane + (SHIFT ? lane / team : 0);
     pdl_wait();
     if (warp / chunks >= warps / chunks) return;  // the warps that make no full set of chunks
 
@@ -51,55 +56,67 @@ __global__ void __launch_bounds__(256, 4) dropout_rows_kernel(const DropParams<T
     uint64_t quad_m0 = 0;
     if (p.drop.on) {
         g = Philox(p.drop.rng);
-        quad_m0 = kPhiloxM0 * (static_cast<uint32_t>(k) * (V / 4));
+        quad_m0 = kPhiloxM0 * (static_cast<uint32_t>(first + place) * (V / 4));
     }
-    auto load = [&](const T* start, bool in) -> uint4 {
-        if constexpr (SHIFT) {
-            const uint32_t mis = granule_offset(start);
-            const uint4* at = reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(start) - mis) + k;
-            uint4 a = make_uint4(0, 0, 0, 0), b = a;
-            if (in) a = __ldg(at);
-            if (in && (k + int64_t(1)) * 16 - mis < N * static_cast<int64_t>(sizeof(T))) b = __ldg(at + 1);
-            return cut16(a, b, mis);
-        } else {
-            return in ? ld_stream_v4(start + static_cast<int64_t>(k) * V) : make_uint4(0, 0, 0, 0);
-        }
+    const int64_t bytes = (N - static_cast<int64_t>(first) * V) * static_cast<int64_t>(sizeof(T));  // of the row from `first` on
+    auto fill_tensor = [&](uint4* to, const T* x, int64_t ld, int64_t row) {
+        const T* start = x + row * ld + static_cast<int64_t>(first) * V;
+        if constexpr (SHIFT)
+            copy_granules(to, x, start, place, static_cast<int>(bytes < 1024 ? bytes : 1024), place == team - 1);
+        else if (valid_k > 0)
+            cp_async16(smem_u32(to), start + place * V);
     };
+    auto fill = [&](int stage, int64_t row) {
+        if (row < p.M) {
+            fill_tensor(ring + stage * kStage, p.x, p.ldx, row);
+            if constexpr (RES) fill_tensor(ring + stage * kStage + kSlots, p.res, p.ld_res, row);
+        }
+        cp_async_commit();
+    };
+    const int64_t base0 = warp / chunks * rows_warp;
+    const int sub = lane / team;
+#pragma unroll
+    for (int k = 0; k < kRing - 1; ++k) fill(k, base0 + sub + k * step);
     const f32x2 inv2 = pair_of(p.drop.inv, p.drop.inv);
-    for (int64_t base = first - lane / team; base < p.M; base += U * step) {
-        Piece<T, V> x[U], r[U];
+    int stage = 0;
+    for (int64_t base = base0; base < p.M; base += step) {
+        const int64_t row = base + sub;
+        fill(stage == 0 ? kRing - 1 : stage - 1, row + (kRing - 1) * step);
+        cp_async_wait<kRing - 1>();
+        if constexpr (SHIFT) __syncwarp();
+        const uint4* at = ring + stage * kStage;
+        const int valid = row < p.M ? valid_k : 0;
+        const T* x_row = p.x + row * p.ldx + static_cast<int64_t>(first) * V;
+        Piece<T, V> x;
+        x.raw = read_piece<SHIFT>(at, SHIFT ? granule_offset(x_row) : 0);
+        f32x2 v[H];
+        unpack2(x, v);
+        if (p.drop.on) {
+            uint32_t w[V];
+            words_at<V>(g, quad_m0, g.row(static_cast<uint32_t>(row)), w);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t row = base + lane / team + u * step;
-            const bool in = row < p.M && valid_k > 0;
-            x[u].raw = load(p.x + (in ? row : 0) * p.ldx, in);
-            if constexpr (RES) r[u].raw = load(p.res + (in ? row : 0) * p.ld_res, in);
+            for (int i = 0; i < H; ++i) v[i] = dropped2(mul2(v[i], inv2), w[2 * i], w[2 * i + 1], p.drop);
         }
+        if constexpr (RES) {
+            Piece<T, V> r;
+            r.raw = read_piece<SHIFT>(at + kSlots, SHIFT ? granule_offset(p.res + row * p.ld_res + static_cast<int64_t>(first) * V) : 0);
+            f32x2 f[H];
+            unpack2(r, f);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t row = base + lane / team + u * step;
-            const int valid = row < p.M ? valid_k : 0;
-            if (!SHIFT && valid == 0) continue;
-            f32x2 v[H];
-            unpack2(x[u], v);
-            if (p.drop.on) {
-                uint32_t w[V];
-                words_at<V>(g, quad_m0, g.row(static_cast<uint32_t>(row)), w);
-#pragma unroll
-                for (int i = 0; i < H; ++i) v[i] = dropped2(mul2(v[i], inv2), w[2 * i], w[2 * i + 1], p.drop);
-            }
-            if constexpr (RES) {
-                f32x2 f[H];
-                unpack2(r[u], f);
-#pragma unroll
-                for (int i = 0; i < H; ++i) v[i] = add2(f[i], v[i]);
-            }
-            pack2(x[u], v);
-            if constexpr (SHIFT) store_shifted<T>(x[u].raw, p.y + row * p.ldy, k, valid, team);
-            else x[u].store(p.y + row * p.ldy + static_cast<int64_t>(k) * V);
+            for (int i = 0; i < H; ++i) v[i] = add2(f[i], v[i]);
         }
+        pack2(x, v);
+        T* y_row = p.y + row * p.ldy + static_cast<int64_t>(first) * V;
+        if constexpr (SHIFT) {
+            store_shifted<T>(x.raw, y_row, place, valid, team);
+            __syncwarp();  // the granules that a neighbour read may be overwritten now
+        } else if (valid > 0) {
+            x.store(y_row + place * V);
+        }
+        stage = stage == kRing - 1 ? 0 : stage + 1;
     }
     pdl_launch_dependents();
+    cp_async_wait<0>();
 }
 
 template <typename T, bool RES, bool SHIFT>
@@ -107,9 +124,11 @@ cudaError_t launch_rows(const DropParams<T>& p, cudaStream_t stream) {
     constexpr int V = 16 / sizeof(T);
     static std::atomic<int> per_sm;  // CTAs that run at a time
     const auto kern = dropout_rows_kernel<T, RES, SHIFT>;
+    const size_t smem = size_t(8) * kRing * (RES ? 2 : 1) * warp_slots(SHIFT, true) * 16;
     int n = per_sm.load(std::memory_order_relaxed);
     if (n == 0) {
-        const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, 256, 0);
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxRing);
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, 256, smem);
         if (e != cudaSuccess) return e;
         n = std::max(n, 1);
         per_sm.store(n, std::memory_order_relaxed);
@@ -120,7 +139,7 @@ cudaError_t launch_rows(const DropParams<T>& p, cudaStream_t stream) {
     const int64_t want = ((p.M + rows_warp - 1) / rows_warp * chunks + 7) / 8;
     const int64_t least = (chunks + 7) / 8;  // one full set of chunks
     const int64_t grid = std::max(least, std::min<int64_t>(want, int64_t(n) * sm_count()));
-    return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(256), 0, stream, p, team, static_cast<int>(chunks));
+    return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(256), smem, stream, p, team, static_cast<int>(chunks));
 }
 
 template <typename T>

@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(1024) ln_bwd_reduce_kernel(const float* part, 
     const int64_t j = static_cast<int64_t>(blockIdx.x) * 32 + lane;  // column of [2][N]
     float sum = 0.0f;
     if (j < 2 * N) {
-#pragma unroll 4
+#pragma unroll 8
         for (int k = warp; k < parts; k += 32) sum += part[static_cast<int64_t>(k) * 2 * N + j];
     }
     s[warp][lane] = sum;

@@ -60,15 +60,15 @@ __global__ void __launch_bounds__(MODE == BROAD ? 512 : MODE == WIDE ? 256 : 128
     constexpr int V = 16 / sizeof(T), H = V / 2, S = bwd_ring_rows(C, MODE);
     constexpr bool kHeld = MODE != BROAD, kCta = MODE != NARROW;  // weights in registers; otherwise from L1 in every row
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-    if constexpr (C > 1) team = 32;
-    const int t = kCta ? threadIdx.x : lane & (team - 1);
-    const int span = kCta ? blockDim.x : team;
+    if constexpr (C > 1 || kCta) team = 32;
+    // piece c of this thread is piece t + 32 c of its row: a warp's are adjacent
+    const int t = kCta ? warp * 32 * C + lane : lane & (team - 1);
     const int N = static_cast<int>(p.N), pieces = SHIFT ? (N + V - 1) / V : N / V;
     const float inv_n = 1.0f / static_cast<float>(N);
     const f32x2 zero2 = pair_of(0.0f, 0.0f);
     // whether this thread's piece c lies in the row: all but the last of a warp's do
-    auto has = [&](int c) { return (!kCta && !SHIFT && c < C - 1) || t + c * span < pieces; };
-    auto count = [&](int c) { return SHIFT ? min(V, N - (t + c * span) * V) : V; };  // of its elements, where it does
+    auto has = [&](int c) { return (!kCta && !SHIFT && c < C - 1) || t + c * 32 < pieces; };
+    auto count = [&](int c) { return SHIFT ? min(V, N - (t + c * 32) * V) : V; };  // of its elements, where it does
     pdl_wait();
 
     f32x2 w[kHeld ? C : 1][H], dw[C][H], db[C][H];
@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(MODE == BROAD ? 512 : MODE == WIDE ? 256 : 128
         if constexpr (kHeld) {
 #pragma unroll
             for (int i = 0; i < H; ++i) w[c][i] = zero2;
-            if (has(c)) load_params2<T, V, SHIFT>(p.w, (t + c * span) * V, N, w[c]);
+            if (has(c)) load_params2<T, V, SHIFT>(p.w, (t + c * 32) * V, N, w[c]);
         }
     }
     Philox g;
@@ -91,26 +91,26 @@ __global__ void __launch_bounds__(MODE == BROAD ? 512 : MODE == WIDE ? 256 : 128
     const int64_t base0 = static_cast<int64_t>(blockIdx.x) * rows_cta;
     const int64_t sub = kCta ? 0 : warp * rows_warp + lane / team;
 
-    const int slots = warp_slots(SHIFT, kCta ? 32 : team);
-    const int my_slot = warp * slots + lane + (SHIFT && !kCta ? lane / team : 0);
-    auto slot = [&](int stage, int tensor, int c) { return s_ring + ((stage * 3 + tensor) * C + c) * (nw * slots) + my_slot; };
+    constexpr int kSlots = warp_slots(SHIFT, !kCta && C == 1), kStage = 3 * C * kSlots;
+    uint4* const ring = s_ring + warp * (S * kStage) + lane + (SHIFT ? lane / team : 0);  // [stage][tensor][c][slot]
     const bool team_end = SHIFT && (kCta ? lane == 31 : t == team - 1);
-    auto fill_tensor = [&](int stage, int tensor, const T* x, int64_t ld, int64_t row) {
+    auto fill_tensor = [&](uint4* to, const T* x, int64_t ld, int64_t row) {
         const T* start = x + row * ld;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             if constexpr (SHIFT)
-                copy_granules(slot(stage, tensor, c), x, start, t + c * span, N * static_cast<int>(sizeof(T)), team_end);
+                copy_granules(to + c * kSlots, x, start, t + c * 32, N * static_cast<int>(sizeof(T)), team_end);
             else if (has(c))
-                cp_async16(smem_u32(slot(stage, tensor, c)), start + t * V + c * span * V);
+                cp_async16(smem_u32(to + c * kSlots), start + t * V + c * 32 * V);
         }
     };
     // the pieces of a row; nothing for a row past the last, which nothing is taken from
     auto fill = [&](int stage, int64_t row) {
         if (row < p.M) {
-            fill_tensor(stage, 0, p.dy, p.ld_dy, row);
-            fill_tensor(stage, 1, p.r, p.ld_r, row);
-            if (p.dres) fill_tensor(stage, 2, p.dres, p.ld_dres, row);
+            uint4* to = ring + stage * kStage;
+            fill_tensor(to, p.dy, p.ld_dy, row);
+            fill_tensor(to + C * kSlots, p.r, p.ld_r, row);
+            if (p.dres) fill_tensor(to + 2 * C * kSlots, p.dres, p.ld_dres, row);
         }
         cp_async_commit();
     };
@@ -133,6 +133,7 @@ __global__ void __launch_bounds__(MODE == BROAD ? 512 : MODE == WIDE ? 256 : 128
         const float mean_next = ahead < p.M ? p.mean[ahead] : 0.0f, rstd_next = ahead < p.M ? p.rstd[ahead] : 0.0f;
         fill(stage == 0 ? S - 1 : stage - 1, row + (S - 1) * stride);
         cp_async_wait<S - 1>();
+        const uint4* at = ring + stage * kStage;
         if constexpr (SHIFT) __syncwarp();
         const uint32_t mis_dy = SHIFT ? granule_offset(p.dy + row * p.ld_dy) : 0;
         const uint32_t mis_r = SHIFT ? granule_offset(p.r + row * p.ld_r) : 0;
@@ -141,16 +142,16 @@ __global__ void __launch_bounds__(MODE == BROAD ? 512 : MODE == WIDE ? 256 : 128
         // dy, xhat and g = dy * w of piece c
         auto inputs = [&](int c, f32x2 (&dy)[H], f32x2 (&xhat)[H], f32x2 (&gw)[H]) {
             Piece<T, V> a;
-            a.raw = read_piece<SHIFT>(slot(stage, 0, c), mis_dy);
+            a.raw = read_piece<SHIFT>(at + c * kSlots, mis_dy);
             unpack2(a, dy);
-            a.raw = read_piece<SHIFT>(slot(stage, 1, c), mis_r);
+            a.raw = read_piece<SHIFT>(at + (C + c) * kSlots, mis_r);
             unpack2(a, xhat);
             if (SHIFT && count(c) < V) {  // the row's end: what follows in the granule is not its own
                 zero_from<V>(dy, count(c));
                 zero_from<V>(xhat, count(c));
             }
             f32x2 wl[H];
-            if constexpr (!kHeld) load_params2<T, V, SHIFT>(p.w, (t + c * span) * V, N, wl);
+            if constexpr (!kHeld) load_params2<T, V, SHIFT>(p.w, (t + c * 32) * V, N, wl);
 #pragma unroll
             for (int i = 0; i < H; ++i) {
                 xhat[i] = mul2(add2(xhat[i], shift), scale);
@@ -208,7 +209,7 @@ __global__ void __launch_bounds__(MODE == BROAD ? 512 : MODE == WIDE ? 256 : 128
 #pragma unroll
                 for (int i = 0; i < H; ++i) d[i] = fma2(xhat[i], c2n, add2(d[i], c1n));
                 if (p.dres) {
-                    out.raw = read_piece<SHIFT>(slot(stage, 2, c), mis_dres);
+                    out.raw = read_piece<SHIFT>(at + (2 * C + c) * kSlots, mis_dres);
                     unpack2(out, xhat);
 #pragma unroll
                     for (int i = 0; i < H; ++i) d[i] = fma2(d[i], scale, xhat[i]);
@@ -218,18 +219,18 @@ __global__ void __launch_bounds__(MODE == BROAD ? 512 : MODE == WIDE ? 256 : 128
                 }
                 pack2(out, d);
             }
-            if constexpr (SHIFT) store_shifted<T>(out.raw, dx_row, t + c * span, valid, kCta ? 32 : team);
-            else out.store(dx_row + t * V + c * span * V);
+            if constexpr (SHIFT) store_shifted<T>(out.raw, dx_row, t + c * 32, valid, kCta ? 32 : team);
+            else out.store(dx_row + t * V + c * 32 * V);
             if (p.dbranch) {
                 if constexpr (DROP) {
                     uint32_t words[V];
-                    words_at<V>(g, first_m0 + kPhiloxM0 * static_cast<uint32_t>(c * span * (V / 4)), row_m0, words);
+                    words_at<V>(g, first_m0 + kPhiloxM0 * static_cast<uint32_t>(c * 32 * (V / 4)), row_m0, words);
 #pragma unroll
                     for (int i = 0; i < H; ++i) d[i] = dropped2(mul2(d[i], inv2), words[2 * i], words[2 * i + 1], p.drop);
                     pack2(out, d);
                 }
-                if constexpr (SHIFT) store_shifted<T>(out.raw, db_row, t + c * span, valid, kCta ? 32 : team);
-                else out.store(db_row + t * V + c * span * V);
+                if constexpr (SHIFT) store_shifted<T>(out.raw, db_row, t + c * 32, valid, kCta ? 32 : team);
+                else out.store(db_row + t * V + c * 32 * V);
             }
         }
         mean = mean_next;
@@ -250,7 +251,7 @@ __global__ void __launch_bounds__(MODE == BROAD ? 512 : MODE == WIDE ? 256 : 128
             if (warp != k) continue;
 #pragma unroll
             for (int c = 0; c < C; ++c) {
-                const int j0 = (t + c * span) * V;
+                const int j0 = (t + c * 32) * V;
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     const float2 pw = split(dw[c][i / 2]), pb = split(db[c][i / 2]);
@@ -270,7 +271,7 @@ __global__ void __launch_bounds__(MODE == BROAD ? 512 : MODE == WIDE ? 256 : 128
     } else {
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const int j0 = (t + c * span) * V;
+            const int j0 = (t + c * 32) * V;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 if (j0 + i >= N) continue;
@@ -284,13 +285,11 @@ __global__ void __launch_bounds__(MODE == BROAD ? 512 : MODE == WIDE ? 256 : 128
 
 template <typename T, int C, BwdMode MODE, bool DROP, bool SHIFT>
 cudaError_t launch_ring_as(BwdParams<T>& p, int team, unsigned block, cudaStream_t stream) {
-    // one wave: as many CTAs as run at a time (the answer is kept by CTA and team size)
-    static std::atomic<int> per_sm[17][6];
+    // one wave: as many CTAs as run at a time (the answer is kept by CTA size)
+    static std::atomic<int> per_sm[17];
     const auto kern = ln_bwd_ring_kernel<T, C, MODE, DROP, SHIFT>;
-    const size_t smem = size_t(bwd_ring_rows(C, MODE)) * 3 * C * (block / 32) * warp_slots(SHIFT, team) * 16;
-    int log_team = 0;
-    while ((1 << log_team) < team) ++log_team;
-    std::atomic<int>& known = per_sm[block / 32][log_team];
+    const size_t smem = size_t(bwd_ring_rows(C, MODE)) * 3 * C * (block / 32) * warp_slots(SHIFT, MODE == NARROW && C == 1) * 16;
+    std::atomic<int>& known = per_sm[block / 32];
     int n = known.load(std::memory_order_relaxed);
     if (n == 0) {
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxRing);

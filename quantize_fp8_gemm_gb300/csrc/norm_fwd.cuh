@@ -48,7 +48,8 @@ namespace {
 enum FwdMode { NARROW, WIDE, BROAD };
 
 // With 40 columns a lane or more the generator's registers beside 128 of weights
-// would leave two warps a scheduler: the weights then come from L1 in every row.
+// would leave two warps a scheduler: the CTA's weights are then in shared memory
+// (BROAD: too many for that, they come from L1).
 __host__ __device__ constexpr bool weights_held(int columns, bool drop, FwdMode mode) {
     return mode != BROAD && !(drop && columns >= 40);
 }
@@ -68,17 +69,20 @@ ln_fwd_ring_kernel(const FwdParams<T> p, int team) {
     constexpr int S = ring_rows(C, C * V, DROP, RES, MODE);
     constexpr bool kHeld = weights_held(C * V, DROP, MODE), kCta = MODE != NARROW;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-    if constexpr (C > 1) team = 32;
-    const int t = kCta ? threadIdx.x : lane & (team - 1);
-    const int span = kCta ? blockDim.x : team;
+    if constexpr (C > 1 || kCta) team = 32;
+    // piece c of this thread is piece t + 32 c of its row: a warp's are adjacent
+    const int t = kCta ? warp * 32 * C + lane : lane & (team - 1);
     const int N = static_cast<int>(p.N), pieces = SHIFT ? (N + V - 1) / V : N / V;
     const float inv_n = 1.0f / static_cast<float>(N);
     const f32x2 zero2 = pair_of(0.0f, 0.0f);
     // whether this thread's piece c lies in the row: all but the last of a warp's do
-    auto has = [&](int c) { return (MODE == NARROW && !SHIFT && c < C - 1) || t + c * span < pieces; };
-    auto count = [&](int c) { return SHIFT ? min(V, N - (t + c * span) * V) : V; };  // of its elements, where it does
+    auto has = [&](int c) { return (MODE == NARROW && !SHIFT && c < C - 1) || t + c * 32 < pieces; };
+    auto count = [&](int c) { return SHIFT ? min(V, N - (t + c * 32) * V) : V; };  // of its elements, where it does
     pdl_wait();
 
+    // [w, b][four columns of a piece][c][lane]: lanes 16 bytes apart
+    constexpr bool kShared = !kHeld && MODE == NARROW;
+    float4* const s_par = reinterpret_cast<float4*>(s_ring + nw * (S * TENSORS * C * warp_slots(SHIFT, !kCta && C == 1))) + lane;
     f32x2 w[kHeld ? C : 1][H], b[kHeld ? C : 1][H];
     int own = 0;  // elements of this thread; of this warp later
 #pragma unroll
@@ -90,10 +94,25 @@ ln_fwd_ring_kernel(const FwdParams<T> p, int team) {
         if (!has(c)) continue;
         own += count(c);
         if constexpr (kHeld) {
-            load_params2<T, V, SHIFT>(p.w, (t + c * span) * V, N, w[c]);
-            load_params2<T, V, SHIFT>(p.b, (t + c * span) * V, N, b[c]);
+            load_params2<T, V, SHIFT>(p.w, (t + c * 32) * V, N, w[c]);
+            load_params2<T, V, SHIFT>(p.b, (t + c * 32) * V, N, b[c]);
+        }
+        if constexpr (kShared) {
+            if (warp == c % 4) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    f32x2 f[H];
+                    load_params2<T, V, SHIFT>(q ? p.b : p.w, (t + c * 32) * V, N, f);
+#pragma unroll
+                    for (int i = 0; i < V / 4; ++i) {
+                        const float2 x = split(f[2 * i]), y = split(f[2 * i + 1]);
+                        s_par[((q * (V / 4) + i) * C + c) * 32] = make_float4(x.x, x.y, y.x, y.y);
+                    }
+                }
+            }
         }
     }
+    if constexpr (kShared) __syncthreads();
     float inv_own = inv_n;  // 1 / (elements whose mean a warp forms)
     if constexpr (kCta) {
         own = __reduce_add_sync(0xFFFFFFFFu, own);
@@ -111,27 +130,25 @@ ln_fwd_ring_kernel(const FwdParams<T> p, int team) {
     const int64_t stride = static_cast<int64_t>(gridDim.x) * rows_cta;
     const int64_t base0 = static_cast<int64_t>(blockIdx.x) * rows_cta;
     const int64_t sub = kCta ? 0 : warp * rows_warp + lane / team;
-    const int slots = warp_slots(SHIFT, kCta ? 32 : team);
-    const int my_slot = warp * slots + lane + (SHIFT && !kCta ? lane / team : 0);
-    auto slot = [&](int stage, int tensor, int c) {
-        return s_ring + ((stage * TENSORS + tensor) * C + c) * (nw * slots) + my_slot;
-    };
+    constexpr int kSlots = warp_slots(SHIFT, !kCta && C == 1), kStage = TENSORS * C * kSlots;
+    uint4* const ring = s_ring + warp * (S * kStage) + lane + (SHIFT ? lane / team : 0);  // [stage][tensor][c][slot]
     const bool team_end = SHIFT && (kCta ? lane == 31 : t == team - 1);
-    auto fill_tensor = [&](int stage, int tensor, const T* x, int64_t ld, int64_t row) {
+    auto fill_tensor = [&](uint4* to, const T* x, int64_t ld, int64_t row) {
         const T* start = x + row * ld;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             if constexpr (SHIFT)
-                copy_granules(slot(stage, tensor, c), x, start, t + c * span, N * static_cast<int>(sizeof(T)), team_end);
+                copy_granules(to + c * kSlots, x, start, t + c * 32, N * static_cast<int>(sizeof(T)), team_end);
             else if (has(c))
-                cp_async16(smem_u32(slot(stage, tensor, c)), start + t * V + c * span * V);
+                cp_async16(smem_u32(to + c * kSlots), start + t * V + c * 32 * V);
         }
     };
     // the pieces of a row; nothing for a row past the last, whose results are not used
     auto fill = [&](int stage, int64_t row) {
         if (row < p.M) {
-            fill_tensor(stage, 0, p.x, p.ldx, row);
-            if constexpr (RES) fill_tensor(stage, 1, p.res, p.ld_res, row);
+            uint4* to = ring + stage * kStage;
+            fill_tensor(to, p.x, p.ldx, row);
+            if constexpr (RES) fill_tensor(to + C * kSlots, p.res, p.ld_res, row);
         }
         cp_async_commit();
     };
@@ -139,7 +156,7 @@ ln_fwd_ring_kernel(const FwdParams<T> p, int team) {
 #pragma unroll
         for (int c = 0; c < C; ++c)
             if (!has(c))
-                for (int k = 0; k < S * TENSORS; ++k) *slot(k / TENSORS, k % TENSORS, c) = make_uint4(0, 0, 0, 0);
+                for (int k = 0; k < S * TENSORS; ++k) ring[(k * C + c) * kSlots] = make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int k = 0; k < S - 1; ++k) fill(k, base0 + sub + k * stride);
@@ -154,6 +171,7 @@ ln_fwd_ring_kernel(const FwdParams<T> p, int team) {
         const bool in = kOwnEnd || kCta || row < p.M;
         fill(stage == 0 ? S - 1 : stage - 1, row + (S - 1) * stride);
         cp_async_wait<S - 1>();
+        const uint4* at = ring + stage * kStage;
         if constexpr (SHIFT) __syncwarp();
         uint64_t row_m0 = 0;
         if constexpr (DROP) row_m0 = g.row(static_cast<uint32_t>(row));
@@ -164,18 +182,18 @@ ln_fwd_ring_kernel(const FwdParams<T> p, int team) {
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             Piece<T, V> a;
-            a.raw = read_piece<SHIFT>(slot(stage, 0, c), mis_x);
+            a.raw = read_piece<SHIFT>(at + c * kSlots, mis_x);
             if constexpr (DROP || RES) {
                 unpack2(a, v[c]);
                 if constexpr (DROP) {
                     uint32_t words[V];
-                    words_at<V>(g, first_m0 + kPhiloxM0 * static_cast<uint32_t>(c * span * (V / 4)), row_m0, words);
+                    words_at<V>(g, first_m0 + kPhiloxM0 * static_cast<uint32_t>(c * 32 * (V / 4)), row_m0, words);
 #pragma unroll
                     for (int i = 0; i < H; ++i) v[c][i] = dropped2(mul2(v[c][i], inv2), words[2 * i], words[2 * i + 1], p.drop);
                 }
                 if constexpr (RES) {
                     Piece<T, V> r;
-                    r.raw = read_piece<SHIFT>(slot(stage, 1, c), mis_r);
+                    r.raw = read_piece<SHIFT>(at + (C + c) * kSlots, mis_r);
                     f32x2 f[H];
                     unpack2(r, f);
 #pragma unroll
@@ -183,13 +201,13 @@ ln_fwd_ring_kernel(const FwdParams<T> p, int team) {
                 }
                 pack2(a, v[c]);
                 if (p.r_out) {
-                    if constexpr (SHIFT) store_shifted<T>(a.raw, r_row, t + c * span, in && has(c) ? count(c) : 0, kCta ? 32 : team);
-                    else if (in && has(c)) a.store(r_row + t * V + c * span * V);
+                    if constexpr (SHIFT) store_shifted<T>(a.raw, r_row, t + c * 32, in && has(c) ? count(c) : 0, kCta ? 32 : team);
+                    else if (in && has(c)) a.store(r_row + t * V + c * 32 * V);
                 }
             }
             unpack2(a, v[c]);
             if constexpr (SHIFT) {
-                if (t + c * span >= pieces || count(c) < V) zero_from<V>(v[c], t + c * span < pieces ? count(c) : 0);
+                if (t + c * 32 >= pieces || count(c) < V) zero_from<V>(v[c], t + c * 32 < pieces ? count(c) : 0);
             }
             f32x2 part = add2(v[c][0], v[c][1]);
             if constexpr (H == 4) part = add2(part, add2(v[c][2], v[c][3]));
@@ -247,9 +265,18 @@ ln_fwd_ring_kernel(const FwdParams<T> p, int team) {
             if (!SHIFT && valid == 0) continue;
             f32x2 wl[H], bl[H];
             if constexpr (!kHeld) {
-                if (valid > 0) {
-                    load_params2<T, V, SHIFT>(p.w, (t + c * span) * V, N, wl);
-                    load_params2<T, V, SHIFT>(p.b, (t + c * span) * V, N, bl);
+                if constexpr (kShared) {
+#pragma unroll
+                    for (int i = 0; i < V / 4; ++i) {
+                        const float4 fw = s_par[(i * C + c) * 32], fb = s_par[((V / 4 + i) * C + c) * 32];
+                        wl[2 * i] = pair_of(fw.x, fw.y);
+                        wl[2 * i + 1] = pair_of(fw.z, fw.w);
+                        bl[2 * i] = pair_of(fb.x, fb.y);
+                        bl[2 * i + 1] = pair_of(fb.z, fb.w);
+                    }
+                } else if (valid > 0) {
+                    load_params2<T, V, SHIFT>(p.w, (t + c * 32) * V, N, wl);
+                    load_params2<T, V, SHIFT>(p.b, (t + c * 32) * V, N, bl);
                 }
             }
 #pragma unroll
@@ -260,11 +287,11 @@ ln_fwd_ring_kernel(const FwdParams<T> p, int team) {
             Piece<T, V> y;
             pack2(y, v[c]);
             if (p.y) {
-                if constexpr (SHIFT) store_shifted<T>(y.raw, y_row, t + c * span, valid, kCta ? 32 : team);
-                else y.store(y_row + t * V + c * span * V);
+                if constexpr (SHIFT) store_shifted<T>(y.raw, y_row, t + c * 32, valid, kCta ? 32 : team);
+                else y.store(y_row + t * V + c * 32 * V);
             }
             if (p.quant.on && valid > 0) {
-                uint8_t* dst = p.quant.q ? q_row + t * V + c * span * V : nullptr;
+                uint8_t* dst = p.quant.q ? q_row + t * V + c * 32 * V : nullptr;
                 const bool whole = !SHIFT || (valid == V && (reinterpret_cast<uintptr_t>(dst) & (V - 1)) == 0);
                 if constexpr (std::is_same<T, __nv_bfloat16>::value) {
                     if (whole) {
@@ -291,14 +318,13 @@ ln_fwd_ring_kernel(const FwdParams<T> p, int team) {
 template <typename T, int C, bool DROP, bool RES, FwdMode MODE, bool SHIFT>
 cudaError_t launch_ring_as(const FwdParams<T>& p, int team, unsigned block, cudaStream_t stream) {
     constexpr int V = 16 / sizeof(T);
-    // one wave: as many CTAs as run at a time (the answer is kept by CTA and team size)
-    static std::atomic<int> per_sm[17][6];
+    // one wave: as many CTAs as run at a time (the answer is kept by CTA size)
+    static std::atomic<int> per_sm[17];
     const auto kern = ln_fwd_ring_kernel<T, C, DROP, RES, MODE, SHIFT>;
-    const size_t smem = size_t(ring_rows(C, C * V, DROP, RES, MODE)) * (RES ? 2 : 1) * C * (block / 32) *
-                        warp_slots(SHIFT, MODE == NARROW ? team : 32) * 16;
-    int log_team = 0;
-    while ((1 << log_team) < team) ++log_team;
-    std::atomic<int>& known = per_sm[block / 32][log_team];
+    size_t smem = size_t(ring_rows(C, C * V, DROP, RES, MODE)) * (RES ? 2 : 1) * C * (block / 32) *
+                        warp_slots(SHIFT, MODE == NARROW && C == 1) * 16;
+    if (!weights_held(C * V, DROP, MODE) && MODE == NARROW) smem += size_t(2) * C * 32 * V * sizeof(float);
+    std::atomic<int>& known = per_sm[block / 32];
     int n = known.load(std::memory_order_relaxed);
     if (n == 0) {
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxRing);

@@ -459,8 +459,9 @@ inline size_t dtype_size(int t) { return t == FP8Q_FP32 ? 4 : 2; }
 inline bool rows16(const void* p, int64_t ld, size_t es) {
     return p == nullptr || (aligned16(p) && (static_cast<uint64_t>(ld) * es) % 16 == 0);
 }
-// Granules that a warp holds of one piece index: with SHIFT one more a row.
-__host__ __device__ inline int warp_slots(bool shift, int team) { return shift ? 32 + 32 / team : 32; }
+// Slots that a warp's ring has of one piece index: with SHIFT one more granule a
+// row (33 for one row of 32 pieces, up to 64 where every lane has a row).
+__host__ __device__ constexpr int warp_slots(bool shift, bool rows) { return !shift ? 32 : rows ? 64 : 33; }
 // Pieces a lane of the kernel that takes so many: the number itself on the
 // 16-byte grid, the next power of two off it (half the kernels to build; the
 // surplus pieces are zeros and change no result).
