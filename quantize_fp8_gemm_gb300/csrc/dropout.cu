@@ -58,62 +58,74 @@ __global__ void __launch_bounds__(256, 4) dropout_rows_kernel(const DropParams<T
         g = Philox(p.drop.rng);
         quad_m0 = kPhiloxM0 * (static_cast<uint32_t>(first + place) * (V / 4));
     }
-    const int64_t bytes = (N - static_cast<int64_t>(first) * V) * static_cast<int64_t>(sizeof(T));  // of the row from `first` on
-    auto fill_tensor = [&](uint4* to, const T* x, int64_t ld, int64_t row) {
-        const T* start = x + row * ld + static_cast<int64_t>(first) * V;
+    // of the row from `first` on: as many bytes as the warp's granules can hold, or fewer
+    const int64_t rest = (N - static_cast<int64_t>(first) * V) * static_cast<int64_t>(sizeof(T));
+    const int bytes = static_cast<int>(rest < 1024 ? rest : 1024);
+    const uint32_t M = static_cast<uint32_t>(p.M), steps = static_cast<uint32_t>(step);
+    uint32_t base = static_cast<uint32_t>(warp / chunks * rows_warp), row = base + lane / team, next = row;
+    const int64_t at0 = static_cast<int64_t>(row), column = static_cast<int64_t>(first) * V;
+    const T *x_in = p.x + at0 * p.ldx + column, *r_in = p.res + at0 * p.ld_res + column, *x_at = x_in, *r_at = r_in;
+    T* y_at = p.y + at0 * p.ldy + column;
+    const int64_t x_step = step * p.ldx, r_step = step * p.ld_res, y_step = step * p.ldy;
+    const uint32_t ring_at = smem_u32(ring);
+    auto fill_tensor = [&](uint32_t to, const T* base_of, const T* start) {
         if constexpr (SHIFT)
-            copy_granules(to, x, start, place, static_cast<int>(bytes < 1024 ? bytes : 1024), place == team - 1);
+            copy_granules(to, base_of, start, place, bytes, place == team - 1);
         else if (valid_k > 0)
-            cp_async16(smem_u32(to), start + place * V);
+            cp_async16(to, start + place * V);
     };
-    auto fill = [&](int stage, int64_t row) {
-        if (row < p.M) {
-            fill_tensor(ring + stage * kStage, p.x, p.ldx, row);
-            if constexpr (RES) fill_tensor(ring + stage * kStage + kSlots, p.res, p.ld_res, row);
+    // the next row that is to be in flight, into a stage; nothing past the last row
+    auto fill = [&](int stage) {
+        if (next < M) {
+            fill_tensor(ring_at + stage * kStage * 16, p.x, x_in);
+            if constexpr (RES) fill_tensor(ring_at + (stage * kStage + kSlots) * 16, p.res, r_in);
         }
         cp_async_commit();
+        next += steps;
+        x_in += x_step;
+        if constexpr (RES) r_in += r_step;
     };
-    const int64_t base0 = warp / chunks * rows_warp;
-    const int sub = lane / team;
 #pragma unroll
-    for (int k = 0; k < kRing - 1; ++k) fill(k, base0 + sub + k * step);
+    for (int k = 0; k < kRing - 1; ++k) fill(k);
     const f32x2 inv2 = pair_of(p.drop.inv, p.drop.inv);
+    uint4 carry = make_uint4(0, 0, 0, 0);
     int stage = 0;
-    for (int64_t base = base0; base < p.M; base += step) {
-        const int64_t row = base + sub;
-        fill(stage == 0 ? kRing - 1 : stage - 1, row + (kRing - 1) * step);
+    for (; base < M; base += steps) {
+        fill(stage == 0 ? kRing - 1 : stage - 1);
         cp_async_wait<kRing - 1>();
         if constexpr (SHIFT) __syncwarp();
         const uint4* at = ring + stage * kStage;
-        const int valid = row < p.M ? valid_k : 0;
-        const T* x_row = p.x + row * p.ldx + static_cast<int64_t>(first) * V;
         Piece<T, V> x;
-        x.raw = read_piece<SHIFT>(at, SHIFT ? granule_offset(x_row) : 0);
+        x.raw = read_piece<SHIFT>(at, SHIFT ? granule_offset(x_at) : 0);
         f32x2 v[H];
         unpack2(x, v);
         if (p.drop.on) {
             uint32_t w[V];
-            words_at<V>(g, quad_m0, g.row(static_cast<uint32_t>(row)), w);
+            words_at<V>(g, quad_m0, g.row(row), w);
 #pragma unroll
             for (int i = 0; i < H; ++i) v[i] = dropped2(mul2(v[i], inv2), w[2 * i], w[2 * i + 1], p.drop);
         }
         if constexpr (RES) {
             Piece<T, V> r;
-            r.raw = read_piece<SHIFT>(at + kSlots, SHIFT ? granule_offset(p.res + row * p.ld_res + static_cast<int64_t>(first) * V) : 0);
+            r.raw = read_piece<SHIFT>(at + kSlots, SHIFT ? granule_offset(r_at) : 0);
             f32x2 f[H];
             unpack2(r, f);
 #pragma unroll
             for (int i = 0; i < H; ++i) v[i] = add2(f[i], v[i]);
         }
         pack2(x, v);
-        T* y_row = p.y + row * p.ldy + static_cast<int64_t>(first) * V;
+        const int valid = row < M ? valid_k : 0;
         if constexpr (SHIFT) {
-            store_shifted<T>(x.raw, y_row, place, valid, team);
+            store_shifted<T>(x.raw, carry, y_at, place, valid, place == 0, place == 31 || first + place == pieces - 1);
             __syncwarp();  // the granules that a neighbour read may be overwritten now
         } else if (valid > 0) {
-            x.store(y_row + place * V);
+            x.store(y_at + place * V);
         }
         stage = stage == kRing - 1 ? 0 : stage + 1;
+        row += steps;
+        x_at += x_step;
+        if constexpr (RES) r_at += r_step;
+        y_at += y_step;
     }
     pdl_launch_dependents();
     cp_async_wait<0>();

@@ -113,12 +113,8 @@ __global__ void __launch_bounds__(1024) ln_bwd_reduce_kernel(const float* part, 
     pdl_launch_dependents();
 }
 
-// Most partial rows of a call: CTAs of the row kernels that run at a time (two
-// warps each where a row is 1025 to 2048 columns of 16 bits).
-int parts_of(int64_t M, int64_t N) {
-    const int64_t rows = N <= 1024 ? 4 : 1;  // rows that a CTA takes at a time, or so
-    return static_cast<int>(std::min<int64_t>((M + rows - 1) / rows, std::min(1024, (N <= 2048 ? 8 : 4) * sm_count())));
-}
+// Most partial rows of a call: CTAs of the row kernels that run at a time.
+int parts_of(int64_t M, int64_t) { return static_cast<int>(std::min<int64_t>(M, std::min(1024, 4 * sm_count()))); }
 
 template <typename T>
 int launch_bwd(const fp8q_layer_norm_bwd_args& a, const Dropout& drop, cudaStream_t stream) {

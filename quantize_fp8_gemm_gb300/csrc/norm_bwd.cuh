@@ -43,31 +43,44 @@ namespace {
 // lane then reads its own granule and the next lane's.
 //   NARROW  `team` lanes (a power of two <= 32) of a warp take a row, up to 32
 //           columns a lane: the row's two sums are shuffles
-//   WIDE    a CTA of up to 256 threads takes a row, 32 columns a thread
-//   BROAD   the same with up to 512 threads, whose registers hold no weights
+//   WIDE    `team` warps take a row, 32 columns a lane, and exchange their sums
+//           at a barrier of their own; a CTA is several such groups
+//   BROAD   the same, one group of up to 16 warps, whose registers hold no weights
+// A CTA is as many warps as the registers hold, so that few partial rows are
+// written and added: 12, or 8 with the generator or with pieces of four columns.
 enum BwdMode { NARROW, WIDE, BROAD };
 
-// Rows of the ring, a stage being 48 C bytes a thread: what a CTA's shared memory
-// holds of its widest row, or two or three CTAs a multiprocessor.
-__host__ __device__ constexpr int bwd_ring_rows(int C, BwdMode mode) {
-    return mode == BROAD ? (C > 4 ? 1 : 2) : C > 4 ? 2 : 3;
+__host__ __device__ constexpr int bwd_warps(int C, BwdMode mode, bool drop) {
+    return mode == BROAD ? 16 : drop || C > 4 ? 8 : 12;
+}
+// Rows of the ring: what the shared memory of a multiprocessor holds for them (a
+// stage is 1536 C bytes a warp).
+__host__ __device__ constexpr int bwd_ring_rows(int C, BwdMode mode, bool drop) {
+    if (mode == BROAD) return C > 4 ? 1 : 2;
+    return C <= 3 ? 3 : C == 4 ? (bwd_warps(C, mode, drop) == 12 ? 2 : 3) : 2;
 }
 
 template <typename T, int C, BwdMode MODE, bool DROP, bool SHIFT>
-__global__ void __launch_bounds__(MODE == BROAD ? 512 : MODE == WIDE ? 256 : 128) ln_bwd_ring_kernel(const BwdParams<T> p, int team) {
-    extern __shared__ uint4 s_ring[];  // [stage][dy, r, dresidual][c][slot]; at the end NARROW's partial row
-    __shared__ __align__(16) float2 s_sum[2][16];
-    constexpr int V = 16 / sizeof(T), H = V / 2, S = bwd_ring_rows(C, MODE);
+__global__ void __launch_bounds__(bwd_warps(C, MODE, DROP) * 32) ln_bwd_ring_kernel(const BwdParams<T> p, int team) {
+    extern __shared__ uint4 s_ring[];  // [warp][stage][dy, r, dresidual][c][slot]; at the end the groups' column sums
+    __shared__ float2 s_sum[2][16];
+    constexpr int V = 16 / sizeof(T), H = V / 2, S = bwd_ring_rows(C, MODE, DROP);
     constexpr bool kHeld = MODE != BROAD, kCta = MODE != NARROW;  // weights in registers; otherwise from L1 in every row
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-    if constexpr (C > 1 || kCta) team = 32;
+    // NARROW: lanes a row, and each warp is a group; otherwise warps a row, and a group
+    const int lanes = kCta || C > 1 ? 32 : team, group_warps = kCta ? team : 1;
+    const int group = warp / group_warps, groups = nw / group_warps;
     // piece c of this thread is piece t + 32 c of its row: a warp's are adjacent
-    const int t = kCta ? warp * 32 * C + lane : lane & (team - 1);
+    const int t = kCta ? (warp - group * group_warps) * 32 * C + lane : lane & (lanes - 1);
     const int N = static_cast<int>(p.N), pieces = SHIFT ? (N + V - 1) / V : N / V;
     const float inv_n = 1.0f / static_cast<float>(N);
     const f32x2 zero2 = pair_of(0.0f, 0.0f);
     // whether this thread's piece c lies in the row: all but the last of a warp's do
     auto has = [&](int c) { return (!kCta && !SHIFT && c < C - 1) || t + c * 32 < pieces; };
+    // (SHIFT) whether it is the first or the last piece of this warp's part of the row
+    auto head = [&](int c) { return c == 0 && (kCta ? lane : t) == 0; };
+    auto tail = [&](int c) { return t + c * 32 == pieces - 1 || (kCta && c == C - 1 && lane == 31); };
+    uint4 carry = make_uint4(0, 0, 0, 0), carry_b = carry;
     auto count = [&](int c) { return SHIFT ? min(V, N - (t + c * 32) * V) : V; };  // of its elements, where it does
     pdl_wait();
 
@@ -86,50 +99,51 @@ __global__ void __launch_bounds__(MODE == BROAD ? 512 : MODE == WIDE ? 256 : 128
     if constexpr (DROP) g = Philox(p.drop.rng);
     const uint64_t first_m0 = kPhiloxM0 * static_cast<uint32_t>(t * (V / 4));
 
-    const int rows_warp = kCta ? 1 : 32 / team, rows_cta = kCta ? 1 : rows_warp * nw;
+    const int rows_group = kCta ? 1 : 32 / lanes, rows_cta = rows_group * groups;
     const int64_t stride = static_cast<int64_t>(gridDim.x) * rows_cta;
-    const int64_t base0 = static_cast<int64_t>(blockIdx.x) * rows_cta;
-    const int64_t sub = kCta ? 0 : warp * rows_warp + lane / team;
+    const int64_t base0 = static_cast<int64_t>(blockIdx.x) * rows_cta + group * rows_group;  // the group's first row
+    const int sub = kCta ? 0 : lane / lanes;
 
     constexpr int kSlots = warp_slots(SHIFT, !kCta && C == 1), kStage = 3 * C * kSlots;
-    uint4* const ring = s_ring + warp * (S * kStage) + lane + (SHIFT ? lane / team : 0);  // [stage][tensor][c][slot]
-    const bool team_end = SHIFT && (kCta ? lane == 31 : t == team - 1);
-    auto fill_tensor = [&](uint4* to, const T* x, int64_t ld, int64_t row) {
+    uint4* const ring = s_ring + warp * (S * kStage) + lane + (SHIFT ? lane / lanes : 0);  // [stage][tensor][c][slot]
+    const bool team_end = SHIFT && (kCta ? lane == 31 : t == lanes - 1);
+    const uint32_t ring_at = smem_u32(ring);
+    auto fill_tensor = [&](uint32_t to, const T* x, int64_t ld, int64_t row) {
         const T* start = x + row * ld;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             if constexpr (SHIFT)
-                copy_granules(to + c * kSlots, x, start, t + c * 32, N * static_cast<int>(sizeof(T)), team_end);
+                copy_granules(to + c * kSlots * 16, x, start, t + c * 32, N * static_cast<int>(sizeof(T)), team_end);
             else if (has(c))
-                cp_async16(smem_u32(to + c * kSlots), start + t * V + c * 32 * V);
+                cp_async16(to + c * kSlots * 16, start + t * V + c * 32 * V);
         }
     };
     // the pieces of a row; nothing for a row past the last, which nothing is taken from
     auto fill = [&](int stage, int64_t row) {
         if (row < p.M) {
-            uint4* to = ring + stage * kStage;
+            const uint32_t to = ring_at + stage * kStage * 16;
             fill_tensor(to, p.dy, p.ld_dy, row);
-            fill_tensor(to + C * kSlots, p.r, p.ld_r, row);
-            if (p.dres) fill_tensor(to + 2 * C * kSlots, p.dres, p.ld_dres, row);
+            fill_tensor(to + C * kSlots * 16, p.r, p.ld_r, row);
+            if (p.dres) fill_tensor(to + 2 * C * kSlots * 16, p.dres, p.ld_dres, row);
         }
         cp_async_commit();
     };
+    if constexpr (!SHIFT) {  // pieces past the row are zeros in every stage, and stay so
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+            if (!has(c))
+                for (int k = 0; k < S * 3; ++k) ring[(k * C + c) * kSlots] = make_uint4(0, 0, 0, 0);
+    }
 #pragma unroll
     for (int k = 0; k < S - 1; ++k) fill(k, base0 + sub + k * stride);
     float mean = base0 + sub < p.M ? p.mean[base0 + sub] : 0.0f;
     float rstd = base0 + sub < p.M ? p.rstd[base0 + sub] : 0.0f;
-    if constexpr (kCta) {
-        if (threadIdx.x < 32) s_sum[threadIdx.x >> 4][threadIdx.x & 15] = make_float2(0.0f, 0.0f);
-        __syncthreads();
-    }
     const f32x2 inv2 = pair_of(p.drop.inv, p.drop.inv);
     int buf = 0, stage = 0;
-    // where a warp takes one row, it is done at its own last; where it shares a barrier or
-    // its lanes take several, at the CTA's
-    constexpr bool kOwnEnd = !kCta && C > 1;
-    for (int64_t base = base0; (kOwnEnd ? base + sub : base) < p.M; base += stride) {
+#pragma unroll 1
+    for (int64_t base = base0; base < p.M; base += stride) {
         const int64_t row = base + sub, ahead = row + stride;
-        const bool in = kOwnEnd || kCta || row < p.M;
+        const bool in = sub == 0 || row < p.M;  // (lanes of a warp that take several rows)
         const float mean_next = ahead < p.M ? p.mean[ahead] : 0.0f, rstd_next = ahead < p.M ? p.rstd[ahead] : 0.0f;
         fill(stage == 0 ? S - 1 : stage - 1, row + (S - 1) * stride);
         cp_async_wait<S - 1>();
@@ -151,7 +165,11 @@ __global__ void __launch_bounds__(MODE == BROAD ? 512 : MODE == WIDE ? 256 : 128
                 zero_from<V>(xhat, count(c));
             }
             f32x2 wl[H];
-            if constexpr (!kHeld) load_params2<T, V, SHIFT>(p.w, (t + c * 32) * V, N, wl);
+            if constexpr (!kHeld) {
+#pragma unroll
+                for (int i = 0; i < H; ++i) wl[i] = zero2;
+                if (has(c)) load_params2<T, V, SHIFT>(p.w, (t + c * 32) * V, N, wl);
+            }
 #pragma unroll
             for (int i = 0; i < H; ++i) {
                 xhat[i] = mul2(add2(xhat[i], shift), scale);
@@ -161,8 +179,8 @@ __global__ void __launch_bounds__(MODE == BROAD ? 512 : MODE == WIDE ? 256 : 128
         f32x2 c1v = zero2, c2v = zero2;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            if (!in || !has(c)) continue;
-            f32x2 dy[H], xhat[H], gw[H];
+            if (C == 1 && !kCta && !in) continue;
+            f32x2 dy[H], xhat[H], gw[H];  // pieces past the row: dy = 0, which adds nothing
             inputs(c, dy, xhat, gw);
 #pragma unroll
             for (int i = 0; i < H; ++i) {
@@ -174,23 +192,28 @@ __global__ void __launch_bounds__(MODE == BROAD ? 512 : MODE == WIDE ? 256 : 128
         }
         const float2 h1 = split(c1v), h2 = split(c2v);
         float c1 = h1.x + h1.y, c2 = h2.x + h2.y;
-        for (int o = (kCta ? 32 : team) / 2; o; o >>= 1) {
+        for (int o = lanes / 2; o; o >>= 1) {
             c1 += __shfl_xor_sync(0xFFFFFFFFu, c1, o);
             c2 += __shfl_xor_sync(0xFFFFFFFFu, c2, o);
         }
         if constexpr (kCta) {
             // two buffers: a warp that runs ahead writes the other one, and cannot reach this one
-            // again before every warp has passed the next row's barrier
+            // again before every warp of its group has passed the next row's barrier
             if (lane == 0) s_sum[buf][warp] = make_float2(c1, c2);
-            __syncthreads();
+            if constexpr (MODE == BROAD) __syncthreads();
+            else named_barrier(1 + group, group_warps * 32);
             c1 = c2 = 0.0f;
-            for (int k = 0; k < nw; k += 2) {  // absent warps are zeros
-                const float4 f = *reinterpret_cast<const float4*>(&s_sum[buf][k]);
-                c1 += f.x + f.z;
-                c2 += f.y + f.w;
+#pragma unroll 4
+            for (int k = 0; k < group_warps; ++k) {
+                const float2 f = s_sum[buf][group * group_warps + k];
+                c1 += f.x;
+                c2 += f.y;
             }
             buf ^= 1;
         }
+        // (also keeps the compiler from carrying the first pass's values into the second, in more
+        // registers than there are; where warps meet, their barrier does)
+        if constexpr (!kCta) __syncwarp();
         c1 *= -inv_n;
         c2 *= -inv_n;
         T* dx_row = p.dx + row * p.ld_dx;
@@ -201,26 +224,23 @@ __global__ void __launch_bounds__(MODE == BROAD ? 512 : MODE == WIDE ? 256 : 128
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int valid = in && has(c) ? count(c) : 0;
-            if (!SHIFT && valid == 0) continue;
             f32x2 dy[H], xhat[H], d[H];
             Piece<T, V> out;
-            if (valid > 0) {
-                inputs(c, dy, xhat, d);
+            inputs(c, dy, xhat, d);
 #pragma unroll
-                for (int i = 0; i < H; ++i) d[i] = fma2(xhat[i], c2n, add2(d[i], c1n));
-                if (p.dres) {
-                    out.raw = read_piece<SHIFT>(at + (2 * C + c) * kSlots, mis_dres);
-                    unpack2(out, xhat);
+            for (int i = 0; i < H; ++i) d[i] = fma2(xhat[i], c2n, add2(d[i], c1n));
+            if (p.dres) {
+                out.raw = read_piece<SHIFT>(at + (2 * C + c) * kSlots, mis_dres);
+                unpack2(out, xhat);
 #pragma unroll
-                    for (int i = 0; i < H; ++i) d[i] = fma2(d[i], scale, xhat[i]);
-                } else {
+                for (int i = 0; i < H; ++i) d[i] = fma2(d[i], scale, xhat[i]);
+            } else {
 #pragma unroll
-                    for (int i = 0; i < H; ++i) d[i] = mul2(d[i], scale);
-                }
-                pack2(out, d);
+                for (int i = 0; i < H; ++i) d[i] = mul2(d[i], scale);
             }
-            if constexpr (SHIFT) store_shifted<T>(out.raw, dx_row, t + c * 32, valid, kCta ? 32 : team);
-            else out.store(dx_row + t * V + c * 32 * V);
+            pack2(out, d);
+            if constexpr (SHIFT) store_shifted<T>(out.raw, carry, dx_row, t + c * 32, valid, head(c), tail(c));
+            else if (valid > 0) out.store(dx_row + t * V + c * 32 * V);
             if (p.dbranch) {
                 if constexpr (DROP) {
                     uint32_t words[V];
@@ -229,8 +249,8 @@ __global__ void __launch_bounds__(MODE == BROAD ? 512 : MODE == WIDE ? 256 : 128
                     for (int i = 0; i < H; ++i) d[i] = dropped2(mul2(d[i], inv2), words[2 * i], words[2 * i + 1], p.drop);
                     pack2(out, d);
                 }
-                if constexpr (SHIFT) store_shifted<T>(out.raw, db_row, t + c * 32, valid, kCta ? 32 : team);
-                else out.store(db_row + t * V + c * 32 * V);
+                if constexpr (SHIFT) store_shifted<T>(out.raw, carry_b, db_row, t + c * 32, valid, head(c), tail(c));
+                else if (valid > 0) out.store(db_row + t * V + c * 32 * V);
             }
         }
         mean = mean_next;
@@ -242,53 +262,47 @@ __global__ void __launch_bounds__(MODE == BROAD ? 512 : MODE == WIDE ? 256 : 128
     cp_async_wait<0>();
     if (p.part == nullptr) return;
 
+    // the groups' sums to shared memory, where the ring was; their sum, in order, is the partial row
+    __syncthreads();
+    float* s_part = reinterpret_cast<float*>(s_ring) + group * 2 * N;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int j0 = (t + c * 32) * V;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const float2 pw = split(dw[c][i / 2]), pb = split(db[c][i / 2]);
+            float a = i & 1 ? pw.y : pw.x, b = i & 1 ? pb.y : pb.x;
+            for (int o = lanes; o < 32; o *= 2) {  // lanes that took other rows of the same columns
+                a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+                b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+            }
+            if (lane >= lanes || j0 + i >= N) continue;
+            s_part[j0 + i] = a;
+            s_part[N + j0 + i] = b;
+        }
+    }
+    __syncthreads();
     float* part = p.part + static_cast<int64_t>(blockIdx.x) * 2 * p.N;
-    if constexpr (!kCta) {
-        // lanes of the warp that took other rows of the same columns, then the warps in order
-        float* s_part = reinterpret_cast<float*>(s_ring);
-        for (int k = 0; k < nw; ++k) {
-            __syncthreads();  // k = 0: every thread is done with the ring
-            if (warp != k) continue;
-#pragma unroll
-            for (int c = 0; c < C; ++c) {
-                const int j0 = (t + c * 32) * V;
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float2 pw = split(dw[c][i / 2]), pb = split(db[c][i / 2]);
-                    float a = i & 1 ? pw.y : pw.x, b = i & 1 ? pb.y : pb.x;
-                    for (int o = team; o < 32; o *= 2) {
-                        a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
-                        b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
-                    }
-                    if (lane >= team || j0 + i >= N) continue;
-                    s_part[j0 + i] = k ? s_part[j0 + i] + a : a;
-                    s_part[N + j0 + i] = k ? s_part[N + j0 + i] + b : b;
-                }
-            }
-        }
-        __syncthreads();
-        for (int j = threadIdx.x; j < 2 * N; j += blockDim.x) part[j] = s_part[j];
-    } else {
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const int j0 = (t + c * 32) * V;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                if (j0 + i >= N) continue;
-                const float2 pw = split(dw[c][i / 2]), pb = split(db[c][i / 2]);
-                part[j0 + i] = i & 1 ? pw.y : pw.x;
-                part[p.N + j0 + i] = i & 1 ? pb.y : pb.x;
-            }
-        }
+    for (int j = threadIdx.x; j < 2 * N; j += blockDim.x) {
+        const float* from = reinterpret_cast<const float*>(s_ring) + j;
+        float sum = from[0];
+        for (int k = 1; k < groups; ++k) sum += from[k * 2 * N];
+        part[j] = sum;
     }
 }
 
 template <typename T, int C, BwdMode MODE, bool DROP, bool SHIFT>
-cudaError_t launch_ring_as(BwdParams<T>& p, int team, unsigned block, cudaStream_t stream) {
+cudaError_t launch_ring_as(BwdParams<T>& p, int team, cudaStream_t stream) {
+    // groups (rows, or warps of narrow rows) a CTA: as many as fit, fewer where that leaves multiprocessors idle
+    const int warps = MODE == NARROW ? 1 : team;
+    const int64_t rows = MODE == NARROW ? 32 / (C > 1 ? 32 : team) : 1;
+    const int64_t all = (p.M + rows - 1) / rows;
+    const int64_t groups = std::min<int64_t>(std::max(1, bwd_warps(C, MODE, DROP) / warps), (all + sm_count() - 1) / sm_count());
+    const unsigned block = static_cast<unsigned>(groups) * warps * 32;
     // one wave: as many CTAs as run at a time (the answer is kept by CTA size)
     static std::atomic<int> per_sm[17];
     const auto kern = ln_bwd_ring_kernel<T, C, MODE, DROP, SHIFT>;
-    const size_t smem = size_t(bwd_ring_rows(C, MODE)) * 3 * C * (block / 32) * warp_slots(SHIFT, MODE == NARROW && C == 1) * 16;
+    const size_t smem = size_t(bwd_ring_rows(C, MODE, DROP)) * 3 * C * (block / 32) * warp_slots(SHIFT, MODE == NARROW && C == 1) * 16;
     std::atomic<int>& known = per_sm[block / 32];
     int n = known.load(std::memory_order_relaxed);
     if (n == 0) {
@@ -298,14 +312,14 @@ cudaError_t launch_ring_as(BwdParams<T>& p, int team, unsigned block, cudaStream
         n = std::max(n, 1);
         known.store(n, std::memory_order_relaxed);
     }
-    p.parts = std::min(p.parts, n * sm_count());
+    p.parts = static_cast<int>(std::min<int64_t>({p.parts, int64_t(n) * sm_count(), (all + groups - 1) / groups}));
     return launch_pdl(kern, dim3(p.parts), dim3(block), smem, stream, p, team);
 }
 
 template <typename T, int C, BwdMode MODE, bool SHIFT>
-cudaError_t launch_ring(BwdParams<T>& p, int team, unsigned block, cudaStream_t stream) {
-    return p.drop.on && p.dbranch ? launch_ring_as<T, C, MODE, true, SHIFT>(p, team, block, stream)
-                                  : launch_ring_as<T, C, MODE, false, SHIFT>(p, team, block, stream);
+cudaError_t launch_ring(BwdParams<T>& p, int team, cudaStream_t stream) {
+    return p.drop.on && p.dbranch ? launch_ring_as<T, C, MODE, true, SHIFT>(p, team, stream)
+                                  : launch_ring_as<T, C, MODE, false, SHIFT>(p, team, stream);
 }
 
 }  // namespace
@@ -321,25 +335,25 @@ cudaError_t launch_bwd_ring(BwdParams<T>& p, cudaStream_t stream) {
     const int64_t c = columns_of((pieces + team - 1) / team, SHIFT);
     if (c <= kMost) {
         switch (c) {
-            case 1: return launch_ring<T, 1, NARROW, SHIFT>(p, team, 128, stream);
-            case 2: return launch_ring<T, 2, NARROW, SHIFT>(p, team, 128, stream);
-            case 4: return launch_ring<T, 4, NARROW, SHIFT>(p, team, 128, stream);
+            case 1: return launch_ring<T, 1, NARROW, SHIFT>(p, team, stream);
+            case 2: return launch_ring<T, 2, NARROW, SHIFT>(p, team, stream);
+            case 4: return launch_ring<T, 4, NARROW, SHIFT>(p, team, stream);
             default: break;
         }
         if constexpr (V == 4) {
-            if (c == 8) return launch_ring<T, 8, NARROW, SHIFT>(p, team, 128, stream);
+            if (c == 8) return launch_ring<T, 8, NARROW, SHIFT>(p, team, stream);
         }
         if constexpr (!SHIFT) {
-            if (c == 3) return launch_ring<T, 3, NARROW, SHIFT>(p, team, 128, stream);
+            if (c == 3) return launch_ring<T, 3, NARROW, SHIFT>(p, team, stream);
             if constexpr (V == 4) {
-                if (c == 5) return launch_ring<T, 5, NARROW, SHIFT>(p, team, 128, stream);
-                if (c == 6) return launch_ring<T, 6, NARROW, SHIFT>(p, team, 128, stream);
-                if (c == 7) return launch_ring<T, 7, NARROW, SHIFT>(p, team, 128, stream);
+                if (c == 5) return launch_ring<T, 5, NARROW, SHIFT>(p, team, stream);
+                if (c == 6) return launch_ring<T, 6, NARROW, SHIFT>(p, team, stream);
+                if (c == 7) return launch_ring<T, 7, NARROW, SHIFT>(p, team, stream);
             }
         }
     }
-    if (pieces <= 256 * kMost) return launch_ring<T, kMost, WIDE, SHIFT>(p, 32, threads_of(pieces, kMost), stream);
-    if (pieces <= 512 * kMost) return launch_ring<T, kMost, BROAD, SHIFT>(p, 32, threads_of(pieces, kMost), stream);
+    if (pieces <= 256 * kMost) return launch_ring<T, kMost, WIDE, SHIFT>(p, static_cast<int>(threads_of(pieces, kMost) / 32), stream);
+    if (pieces <= 512 * kMost) return launch_ring<T, kMost, BROAD, SHIFT>(p, static_cast<int>(threads_of(pieces, kMost) / 32), stream);
     return cudaErrorNotSupported;
 }
 

@@ -77,6 +77,10 @@ ln_fwd_ring_kernel(const FwdParams<T> p, int team) {
     const f32x2 zero2 = pair_of(0.0f, 0.0f);
     // whether this thread's piece c lies in the row: all but the last of a warp's do
     auto has = [&](int c) { return (MODE == NARROW && !SHIFT && c < C - 1) || t + c * 32 < pieces; };
+    // (SHIFT) whether it is the first or the last piece of this warp's part of the row
+    auto head = [&](int c) { return c == 0 && (kCta ? lane : t) == 0; };
+    auto tail = [&](int c) { return t + c * 32 == pieces - 1 || (kCta && c == C - 1 && lane == 31); };
+    uint4 carry = make_uint4(0, 0, 0, 0);
     auto count = [&](int c) { return SHIFT ? min(V, N - (t + c * 32) * V) : V; };  // of its elements, where it does
     pdl_wait();
 
@@ -133,22 +137,23 @@ ln_fwd_ring_kernel(const FwdParams<T> p, int team) {
     constexpr int kSlots = warp_slots(SHIFT, !kCta && C == 1), kStage = TENSORS * C * kSlots;
     uint4* const ring = s_ring + warp * (S * kStage) + lane + (SHIFT ? lane / team : 0);  // [stage][tensor][c][slot]
     const bool team_end = SHIFT && (kCta ? lane == 31 : t == team - 1);
-    auto fill_tensor = [&](uint4* to, const T* x, int64_t ld, int64_t row) {
+    const uint32_t ring_at = smem_u32(ring);
+    auto fill_tensor = [&](uint32_t to, const T* x, int64_t ld, int64_t row) {
         const T* start = x + row * ld;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             if constexpr (SHIFT)
-                copy_granules(to + c * kSlots, x, start, t + c * 32, N * static_cast<int>(sizeof(T)), team_end);
+                copy_granules(to + c * kSlots * 16, x, start, t + c * 32, N * static_cast<int>(sizeof(T)), team_end);
             else if (has(c))
-                cp_async16(smem_u32(to + c * kSlots), start + t * V + c * 32 * V);
+                cp_async16(to + c * kSlots * 16, start + t * V + c * 32 * V);
         }
     };
     // the pieces of a row; nothing for a row past the last, whose results are not used
     auto fill = [&](int stage, int64_t row) {
         if (row < p.M) {
-            uint4* to = ring + stage * kStage;
+            const uint32_t to = ring_at + stage * kStage * 16;
             fill_tensor(to, p.x, p.ldx, row);
-            if constexpr (RES) fill_tensor(to + C * kSlots, p.res, p.ld_res, row);
+            if constexpr (RES) fill_tensor(to + C * kSlots * 16, p.res, p.ld_res, row);
         }
         cp_async_commit();
     };
@@ -201,7 +206,7 @@ ln_fwd_ring_kernel(const FwdParams<T> p, int team) {
                 }
                 pack2(a, v[c]);
                 if (p.r_out) {
-                    if constexpr (SHIFT) store_shifted<T>(a.raw, r_row, t + c * 32, in && has(c) ? count(c) : 0, kCta ? 32 : team);
+                    if constexpr (SHIFT) store_shifted<T>(a.raw, carry, r_row, t + c * 32, in && has(c) ? count(c) : 0, head(c), tail(c));
                     else if (in && has(c)) a.store(r_row + t * V + c * 32 * V);
                 }
             }
@@ -287,7 +292,7 @@ ln_fwd_ring_kernel(const FwdParams<T> p, int team) {
             Piece<T, V> y;
             pack2(y, v[c]);
             if (p.y) {
-                if constexpr (SHIFT) store_shifted<T>(y.raw, y_row, t + c * 32, valid, kCta ? 32 : team);
+                if constexpr (SHIFT) store_shifted<T>(y.raw, carry, y_row, t + c * 32, valid, head(c), tail(c));
                 else y.store(y_row + t * V + c * 32 * V);
             }
             if (p.quant.on && valid > 0) {

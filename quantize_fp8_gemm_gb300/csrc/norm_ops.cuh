@@ -187,19 +187,19 @@ template <typename T>
 __device__ __forceinline__ uint32_t granule_offset(const T* start) {
     return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(start) & 15);
 }
-// cp.async of granule k of the `bytes` bytes at start (nothing of it in the row:
+// cp.async, to shared address `slot`, of granule k of the `bytes` bytes at start (nothing of it in the row:
 // zeros, and `base` for an address that is not read), and of granule k + 1 into
 // the next slot if `two`.
 template <typename T>
-__device__ __forceinline__ void copy_granules(uint4* slot, const T* base, const T* start, int k, int bytes, bool two) {
+__device__ __forceinline__ void copy_granules(uint32_t slot, const T* base, const T* start, int k, int bytes, bool two) {
     const int mis = static_cast<int>(granule_offset(start));
     const uint8_t* first = reinterpret_cast<const uint8_t*>(start) - mis;
     const int64_t at = static_cast<int64_t>(k) * 16;
     // no bytes (a row past the last): nothing, although granule 0 of a shifted row begins before it
     const bool has = bytes > 0 && at - mis < bytes, has2 = at + 16 - mis < bytes;
     const uint8_t* none = reinterpret_cast<const uint8_t*>(base) - granule_offset(base);
-    cp_async16_or_zero(smem_u32(slot), has ? first + at : none, has);
-    if (two) cp_async16_or_zero(smem_u32(slot + 1), has2 ? first + at + 16 : none, has2);
+    cp_async16_or_zero(slot, has ? first + at : none, has);
+    if (two) cp_async16_or_zero(slot + 16, has2 ? first + at + 16 : none, has2);
 }
 // This lane's piece from the ring: its slot, or cut from its slot and the next.
 template <bool SHIFT>
@@ -233,35 +233,39 @@ __device__ __forceinline__ void store_elements(T* dst, uint4 q, int lo, int hi) 
 }
 
 // Store a warp's pieces: this lane's is piece k of the row at `start`, with
-// `valid` elements (0: none; fewer than V only in the row's last piece).  The
-// lanes of a `team` hold adjacent pieces of one row.  All lanes of the warp call
-// it.  A lane writes the granule in which its piece begins, whose first bytes are
-// the end of the previous lane's piece; the first lane's granule and what is
-// left of the last piece go element by element.
+// `valid` elements (0: none; fewer than V only in the row's last piece).  Lanes
+// hold adjacent pieces, and a call for the warp's next 32 pieces follows with the
+// same `carry`.  All lanes of the warp call it.  A lane writes the granule in
+// which its piece begins, whose first bytes are the end of the piece before (of
+// lane 0's from the call before); where a warp's part of the row begins (`head`),
+// and what is left of the last piece of it (`tail`), go element by element.
 template <typename T>
-__device__ __forceinline__ void store_shifted(uint4 q, T* start, int k, int valid, int team) {
+__device__ __forceinline__ void store_shifted(uint4 q, uint4& carry, T* start, int k, int valid, bool head, bool tail) {
     constexpr int V = 16 / sizeof(T);
+    const int lane = threadIdx.x & 31, from = (lane + 31) & 31;
     uint4 prev;
-    prev.x = __shfl_up_sync(0xFFFFFFFFu, q.x, 1);
-    prev.y = __shfl_up_sync(0xFFFFFFFFu, q.y, 1);
-    prev.z = __shfl_up_sync(0xFFFFFFFFu, q.z, 1);
-    prev.w = __shfl_up_sync(0xFFFFFFFFu, q.w, 1);
-    const int place = threadIdx.x & (team - 1);
-    const int after = __shfl_down_sync(0xFFFFFFFFu, valid, 1);  // elements of the next lane's piece
-    if (valid == 0) return;
+    prev.x = __shfl_sync(0xFFFFFFFFu, q.x, from);
+    prev.y = __shfl_sync(0xFFFFFFFFu, q.y, from);
+    prev.z = __shfl_sync(0xFFFFFFFFu, q.z, from);
+    prev.w = __shfl_sync(0xFFFFFFFFu, q.w, from);
+    const uint4 next_carry = prev;
+    if (lane == 0) prev = carry;
+    carry = next_carry;
+    if (valid <= 0) return;
     T* dst = start + static_cast<int64_t>(k) * V;
-    const uint32_t mis = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(start) & 15);
+    const uint32_t mis = granule_offset(start);
     const int lead = (16 - static_cast<int>(mis)) / static_cast<int>(sizeof(T));  // of this piece in its first granule
-    if (mis == 0 && valid == V) {
+    if (mis == 0 && valid >= V) {
         st_v4(dst, q);
-    } else if (mis != 0 && place != 0 && valid >= lead) {
+        return;
+    }
+    if (mis != 0 && !head && valid >= lead) {
         st_v4(reinterpret_cast<uint8_t*>(dst) - mis, cut16(prev, q, 16 - mis));
     } else {
-        if (mis != 0 && place != 0) store_elements<T>(dst - V, prev, lead, V);
+        if (mis != 0 && !head) store_elements<T>(dst - V, prev, lead, V);
         store_elements<T>(dst, q, 0, valid < lead ? valid : lead);
     }
-    const bool next = place != team - 1 && after > 0;  // the next lane writes this piece's end
-    if (mis != 0 && !next) store_elements<T>(dst, q, lead, valid);
+    if (mis != 0 && tail) store_elements<T>(dst, q, lead, valid);
 }
 
 // ----------------------------------------------------------------- dropout --
