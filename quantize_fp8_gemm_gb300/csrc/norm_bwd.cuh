@@ -76,12 +76,17 @@ __global__ void __launch_bounds__(bwd_warps(C, MODE, DROP) * 32) ln_bwd_ring_ker
     const float inv_n = 1.0f / static_cast<float>(N);
     const f32x2 zero2 = pair_of(0.0f, 0.0f);
     // whether this thread's piece c lies in the row: all but the last of a warp's do
-    auto has = [&](int c) { return (!kCta && !SHIFT && c < C - 1) || t + c * 32 < pieces; };
-    // (SHIFT) whether it is the first or the last piece of this warp's part of the row
-    auto head = [&](int c) { return c == 0 && (kCta ? lane : t) == 0; };
-    auto tail = [&](int c) { return t + c * 32 == pieces - 1 || (kCta && c == C - 1 && lane == 31); };
+    auto has = [&](int c) { return (!kCta && c < C - 1) || t + c * 32 < pieces; };
     uint4 carry = make_uint4(0, 0, 0, 0), carry_b = carry;
-    auto count = [&](int c) { return SHIFT ? min(V, N - (t + c * 32) * V) : V; };  // of its elements, where it does
+    auto count = [&](int c) { return SHIFT && (kCta || c == C - 1) ? min(V, N - (t + c * 32) * V) : V; };  // of its elements, where it does
+    // (SHIFT) store of piece c; a row's first piece is in its first lane's first, its last one in the last
+    auto put = [&](uint4 q, uint4& carried, T* start, int c, int valid) {
+        const bool head = c == 0 && (kCta ? lane : t) == 0, tail = t + c * 32 == pieces - 1 || (kCta && c == C - 1 && lane == 31);
+        if (C == 1 || (kCta && c == 0)) store_shifted<T, true, true>(q, carried, start, t + c * 32, valid, head, tail);
+        else if (c == 0) store_shifted<T, true, false>(q, carried, start, t + c * 32, valid, head, tail);
+        else if (c == C - 1 || kCta) store_shifted<T, false, true>(q, carried, start, t + c * 32, valid, head, tail);
+        else store_shifted<T, false, false>(q, carried, start, t + c * 32, valid, head, tail);
+    };
     pdl_wait();
 
     f32x2 w[kHeld ? C : 1][H], dw[C][H], db[C][H];
@@ -110,12 +115,17 @@ __global__ void __launch_bounds__(bwd_warps(C, MODE, DROP) * 32) ln_bwd_ring_ker
     const uint32_t ring_at = smem_u32(ring);
     auto fill_tensor = [&](uint32_t to, const T* x, int64_t ld, int64_t row) {
         const T* start = x + row * ld;
+        const uint32_t mis = SHIFT ? granule_offset(start) : 0;
+        const uint8_t* first = reinterpret_cast<const uint8_t*>(start) - mis;
+        const int end = N * static_cast<int>(sizeof(T)) + static_cast<int>(mis);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            if constexpr (SHIFT)
-                copy_granules(to + c * kSlots * 16, x, start, t + c * 32, N * static_cast<int>(sizeof(T)), team_end);
-            else if (has(c))
+            if constexpr (SHIFT) {
+                if (!kCta && c < C - 1) copy_granules<true>(to + c * kSlots * 16, first, t + c * 32, end, team_end);
+                else copy_granules<false>(to + c * kSlots * 16, first, t + c * 32, end, team_end);
+            } else if (has(c)) {
                 cp_async16(to + c * kSlots * 16, start + t * V + c * 32 * V);
+            }
         }
     };
     // the pieces of a row; nothing for a row past the last, which nothing is taken from
@@ -239,7 +249,7 @@ __global__ void __launch_bounds__(bwd_warps(C, MODE, DROP) * 32) ln_bwd_ring_ker
                 for (int i = 0; i < H; ++i) d[i] = mul2(d[i], scale);
             }
             pack2(out, d);
-            if constexpr (SHIFT) store_shifted<T>(out.raw, carry, dx_row, t + c * 32, valid, head(c), tail(c));
+            if constexpr (SHIFT) put(out.raw, carry, dx_row, c, valid);
             else if (valid > 0) out.store(dx_row + t * V + c * 32 * V);
             if (p.dbranch) {
                 if constexpr (DROP) {
@@ -249,7 +259,7 @@ __global__ void __launch_bounds__(bwd_warps(C, MODE, DROP) * 32) ln_bwd_ring_ker
                     for (int i = 0; i < H; ++i) d[i] = dropped2(mul2(d[i], inv2), words[2 * i], words[2 * i + 1], p.drop);
                     pack2(out, d);
                 }
-                if constexpr (SHIFT) store_shifted<T>(out.raw, carry_b, db_row, t + c * 32, valid, head(c), tail(c));
+                if constexpr (SHIFT) put(out.raw, carry_b, db_row, c, valid);
                 else if (valid > 0) out.store(db_row + t * V + c * 32 * V);
             }
         }
@@ -332,24 +342,20 @@ cudaError_t launch_bwd_ring(BwdParams<T>& p, cudaStream_t stream) {
     const int64_t pieces = (p.N + V - 1) / V;
     const int team = team_of(pieces);
     constexpr int kMost = 32 / V;
-    const int64_t c = columns_of((pieces + team - 1) / team, SHIFT);
+    const int64_t c = (pieces + team - 1) / team;
     if (c <= kMost) {
         switch (c) {
             case 1: return launch_ring<T, 1, NARROW, SHIFT>(p, team, stream);
             case 2: return launch_ring<T, 2, NARROW, SHIFT>(p, team, stream);
+            case 3: return launch_ring<T, 3, NARROW, SHIFT>(p, team, stream);
             case 4: return launch_ring<T, 4, NARROW, SHIFT>(p, team, stream);
             default: break;
         }
         if constexpr (V == 4) {
+            if (c == 5) return launch_ring<T, 5, NARROW, SHIFT>(p, team, stream);
+            if (c == 6) return launch_ring<T, 6, NARROW, SHIFT>(p, team, stream);
+            if (c == 7) return launch_ring<T, 7, NARROW, SHIFT>(p, team, stream);
             if (c == 8) return launch_ring<T, 8, NARROW, SHIFT>(p, team, stream);
-        }
-        if constexpr (!SHIFT) {
-            if (c == 3) return launch_ring<T, 3, NARROW, SHIFT>(p, team, stream);
-            if constexpr (V == 4) {
-                if (c == 5) return launch_ring<T, 5, NARROW, SHIFT>(p, team, stream);
-                if (c == 6) return launch_ring<T, 6, NARROW, SHIFT>(p, team, stream);
-                if (c == 7) return launch_ring<T, 7, NARROW, SHIFT>(p, team, stream);
-            }
         }
     }
     if (pieces <= 256 * kMost) return launch_ring<T, kMost, WIDE, SHIFT>(p, static_cast<int>(threads_of(pieces, kMost) / 32), stream);

@@ -76,12 +76,17 @@ ln_fwd_ring_kernel(const FwdParams<T> p, int team) {
     const float inv_n = 1.0f / static_cast<float>(N);
     const f32x2 zero2 = pair_of(0.0f, 0.0f);
     // whether this thread's piece c lies in the row: all but the last of a warp's do
-    auto has = [&](int c) { return (MODE == NARROW && !SHIFT && c < C - 1) || t + c * 32 < pieces; };
-    // (SHIFT) whether it is the first or the last piece of this warp's part of the row
-    auto head = [&](int c) { return c == 0 && (kCta ? lane : t) == 0; };
-    auto tail = [&](int c) { return t + c * 32 == pieces - 1 || (kCta && c == C - 1 && lane == 31); };
+    auto has = [&](int c) { return (!kCta && c < C - 1) || t + c * 32 < pieces; };
     uint4 carry = make_uint4(0, 0, 0, 0);
-    auto count = [&](int c) { return SHIFT ? min(V, N - (t + c * 32) * V) : V; };  // of its elements, where it does
+    auto count = [&](int c) { return SHIFT && (kCta || c == C - 1) ? min(V, N - (t + c * 32) * V) : V; };  // of its elements, where it does
+    // (SHIFT) store of piece c; a row's first piece is in its first lane's first, its last one in the last
+    auto put = [&](uint4 q, uint4& carried, T* start, int c, int valid) {
+        const bool head = c == 0 && (kCta ? lane : t) == 0, tail = t + c * 32 == pieces - 1 || (kCta && c == C - 1 && lane == 31);
+        if (C == 1 || (kCta && c == 0)) store_shifted<T, true, true>(q, carried, start, t + c * 32, valid, head, tail);
+        else if (c == 0) store_shifted<T, true, false>(q, carried, start, t + c * 32, valid, head, tail);
+        else if (c == C - 1 || kCta) store_shifted<T, false, true>(q, carried, start, t + c * 32, valid, head, tail);
+        else store_shifted<T, false, false>(q, carried, start, t + c * 32, valid, head, tail);
+    };
     pdl_wait();
 
     // [w, b][four columns of a piece][c][lane]: lanes 16 bytes apart
@@ -140,12 +145,17 @@ ln_fwd_ring_kernel(const FwdParams<T> p, int team) {
     const uint32_t ring_at = smem_u32(ring);
     auto fill_tensor = [&](uint32_t to, const T* x, int64_t ld, int64_t row) {
         const T* start = x + row * ld;
+        const uint32_t mis = SHIFT ? granule_offset(start) : 0;
+        const uint8_t* first = reinterpret_cast<const uint8_t*>(start) - mis;
+        const int end = N * static_cast<int>(sizeof(T)) + static_cast<int>(mis);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            if constexpr (SHIFT)
-                copy_granules(to + c * kSlots * 16, x, start, t + c * 32, N * static_cast<int>(sizeof(T)), team_end);
-            else if (has(c))
+            if constexpr (SHIFT) {
+                if (!kCta && c < C - 1) copy_granules<true>(to + c * kSlots * 16, first, t + c * 32, end, team_end);
+                else copy_granules<false>(to + c * kSlots * 16, first, t + c * 32, end, team_end);
+            } else if (has(c)) {
                 cp_async16(to + c * kSlots * 16, start + t * V + c * 32 * V);
+            }
         }
     };
     // the pieces of a row; nothing for a row past the last, whose results are not used
@@ -206,7 +216,7 @@ ln_fwd_ring_kernel(const FwdParams<T> p, int team) {
                 }
                 pack2(a, v[c]);
                 if (p.r_out) {
-                    if constexpr (SHIFT) store_shifted<T>(a.raw, carry, r_row, t + c * 32, in && has(c) ? count(c) : 0, head(c), tail(c));
+                    if constexpr (SHIFT) put(a.raw, carry, r_row, c, in && has(c) ? count(c) : 0);
                     else if (in && has(c)) a.store(r_row + t * V + c * 32 * V);
                 }
             }
@@ -292,7 +302,7 @@ ln_fwd_ring_kernel(const FwdParams<T> p, int team) {
             Piece<T, V> y;
             pack2(y, v[c]);
             if (p.y) {
-                if constexpr (SHIFT) store_shifted<T>(y.raw, carry, y_row, t + c * 32, valid, head(c), tail(c));
+                if constexpr (SHIFT) put(y.raw, carry, y_row, c, valid);
                 else y.store(y_row + t * V + c * 32 * V);
             }
             if (p.quant.on && valid > 0) {
@@ -360,21 +370,16 @@ cudaError_t launch_fwd_ring(const FwdParams<T>& p, cudaStream_t stream) {
     constexpr int V = 16 / sizeof(T), kMost = 32 / V;
     const int64_t pieces = (p.N + V - 1) / V;
     const int team = team_of(pieces);
-    switch (columns_of((pieces + team - 1) / team, SHIFT)) {
+    switch ((pieces + team - 1) / team) {
         case 1: return launch_ring<T, 1, NARROW, SHIFT>(p, team, 128, stream);
         case 2: return launch_ring<T, 2, NARROW, SHIFT>(p, team, 128, stream);
+        case 3: return launch_ring<T, 3, NARROW, SHIFT>(p, team, 128, stream);
         case 4: return launch_ring<T, 4, NARROW, SHIFT>(p, team, 128, stream);
+        case 5: return launch_ring<T, 5, NARROW, SHIFT>(p, team, 128, stream);
+        case 6: return launch_ring<T, 6, NARROW, SHIFT>(p, team, 128, stream);
+        case 7: return launch_ring<T, 7, NARROW, SHIFT>(p, team, 128, stream);
         case 8: return launch_ring<T, 8, NARROW, SHIFT>(p, team, 128, stream);
         default: break;
-    }
-    if constexpr (!SHIFT) {
-        switch ((pieces + team - 1) / team) {
-            case 3: return launch_ring<T, 3, NARROW, SHIFT>(p, team, 128, stream);
-            case 5: return launch_ring<T, 5, NARROW, SHIFT>(p, team, 128, stream);
-            case 6: return launch_ring<T, 6, NARROW, SHIFT>(p, team, 128, stream);
-            case 7: return launch_ring<T, 7, NARROW, SHIFT>(p, team, 128, stream);
-            default: break;
-        }
     }
     if (pieces <= 256 * kMost) return launch_ring<T, kMost, WIDE, SHIFT>(p, 32, threads_of(pieces, kMost), stream);
     if (pieces <= 512 * kMost) return launch_ring<T, kMost, BROAD, SHIFT>(p, 32, threads_of(pieces, kMost), stream);

@@ -187,19 +187,21 @@ template <typename T>
 __device__ __forceinline__ uint32_t granule_offset(const T* start) {
     return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(start) & 15);
 }
-// cp.async, to shared address `slot`, of granule k of the `bytes` bytes at start (nothing of it in the row:
-// zeros, and `base` for an address that is not read), and of granule k + 1 into
-// the next slot if `two`.
-template <typename T>
-__device__ __forceinline__ void copy_granules(uint32_t slot, const T* base, const T* start, int k, int bytes, bool two) {
-    const int mis = static_cast<int>(granule_offset(start));
-    const uint8_t* first = reinterpret_cast<const uint8_t*>(start) - mis;
-    const int64_t at = static_cast<int64_t>(k) * 16;
-    // no bytes (a row past the last): nothing, although granule 0 of a shifted row begins before it
-    const bool has = bytes > 0 && at - mis < bytes, has2 = at + 16 - mis < bytes;
-    const uint8_t* none = reinterpret_cast<const uint8_t*>(base) - granule_offset(base);
-    cp_async16_or_zero(slot, has ? first + at : none, has);
-    if (two) cp_async16_or_zero(slot + 16, has2 ? first + at + 16 : none, has2);
+// cp.async, to shared address `slot`, of granule k of a row whose first granule is
+// at `first`, and of granule k + 1 into the next slot if `two`.  INSIDE: both hold
+// elements of the row; otherwise one that begins at or after `end` bytes from
+// `first` is zeros (no byte of it is read).
+template <bool INSIDE>
+__device__ __forceinline__ void copy_granules(uint32_t slot, const uint8_t* first, int k, int end, bool two) {
+    const uint8_t* at = first + static_cast<int64_t>(k) * 16;
+    if constexpr (INSIDE) {
+        cp_async16(slot, at);
+        if (two) cp_async16(slot + 16, at + 16);
+    } else {
+        const bool has = k * 16 < end, has2 = k * 16 + 16 < end;
+        cp_async16_or_zero(slot, has ? at : first, has);
+        if (two) cp_async16_or_zero(slot + 16, has2 ? at + 16 : first, has2);
+    }
 }
 // This lane's piece from the ring: its slot, or cut from its slot and the next.
 template <bool SHIFT>
@@ -239,7 +241,8 @@ __device__ __forceinline__ void store_elements(T* dst, uint4 q, int lo, int hi) 
 // which its piece begins, whose first bytes are the end of the piece before (of
 // lane 0's from the call before); where a warp's part of the row begins (`head`),
 // and what is left of the last piece of it (`tail`), go element by element.
-template <typename T>
+// HEAD, TAIL: whether the call's pieces can be such.
+template <typename T, bool HEAD, bool TAIL>
 __device__ __forceinline__ void store_shifted(uint4 q, uint4& carry, T* start, int k, int valid, bool head, bool tail) {
     constexpr int V = 16 / sizeof(T);
     const int lane = threadIdx.x & 31, from = (lane + 31) & 31;
@@ -255,17 +258,19 @@ __device__ __forceinline__ void store_shifted(uint4 q, uint4& carry, T* start, i
     T* dst = start + static_cast<int64_t>(k) * V;
     const uint32_t mis = granule_offset(start);
     const int lead = (16 - static_cast<int>(mis)) / static_cast<int>(sizeof(T));  // of this piece in its first granule
-    if (mis == 0 && valid >= V) {
-        st_v4(dst, q);
-        return;
+    const bool whole = (!HEAD || !head || mis == 0) && (!TAIL || valid >= lead);
+    if (whole) {
+        const uint4 cut = cut16(prev, q, 16 - mis);
+        st_v4(reinterpret_cast<uint8_t*>(dst) - mis, mis ? cut : q);
     }
-    if (mis != 0 && !head && valid >= lead) {
-        st_v4(reinterpret_cast<uint8_t*>(dst) - mis, cut16(prev, q, 16 - mis));
-    } else {
-        if (mis != 0 && !head) store_elements<T>(dst - V, prev, lead, V);
-        store_elements<T>(dst, q, 0, valid < lead ? valid : lead);
+    if constexpr (HEAD || TAIL) {
+        // (mis = 0: lead = V, and a piece that ends the row early is its first `valid` elements)
+        if (!whole) {
+            if (mis != 0 && !(HEAD && head)) store_elements<T>(dst - V, prev, lead, V);
+            store_elements<T>(dst, q, 0, valid < lead ? valid : lead);
+        }
+        if (TAIL && tail) store_elements<T>(dst, q, lead, valid);
     }
-    if (mis != 0 && tail) store_elements<T>(dst, q, lead, valid);
 }
 
 // ----------------------------------------------------------------- dropout --
@@ -466,13 +471,6 @@ inline bool rows16(const void* p, int64_t ld, size_t es) {
 // Slots that a warp's ring has of one piece index: with SHIFT one more granule a
 // row (33 for one row of 32 pieces, up to 64 where every lane has a row).
 __host__ __device__ constexpr int warp_slots(bool shift, bool rows) { return !shift ? 32 : rows ? 64 : 33; }
-// Pieces a lane of the kernel that takes so many: the number itself on the
-// 16-byte grid, the next power of two off it (half the kernels to build; the
-// surplus pieces are zeros and change no result).
-inline int64_t columns_of(int64_t c, bool shift) {
-    if (!shift) return c;
-    return c <= 2 ? c : c <= 4 ? 4 : c <= 8 ? 8 : c;
-}
 // Lanes of a warp that take a row of so many pieces: a power of two, 32 at most.
 inline int team_of(int64_t pieces) {
     int team = 1;
