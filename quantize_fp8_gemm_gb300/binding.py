@@ -543,6 +543,30 @@ def _rng(t):
     return _vec(t, 2, torch.int64, "rng")
 
 
+def _cell(t, dtype, name: str):
+    """Device pointer of an optional CUDA tensor whose first element a call uses."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.numel() < 1:
+        raise ValueError(f"{name} is empty")
+    return t.data_ptr()
+
+
+def _codes(t, n: int):
+    """Device pointer of an optional packed CUDA tensor of n one-byte codes."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("q_out must be a CUDA tensor")
+    if t.element_size() != 1 or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"q_out must hold {n} packed one-byte codes")
+    return t.data_ptr()
+
+
 def _param_code(x, weight, bias, code: int):
     """(param_dtype, its torch type) of the weight and bias: float32, or x's type."""
     t = weight if weight is not None else bias
@@ -565,13 +589,11 @@ def layer_norm_fwd(x: torch.Tensor, weight, bias, y, *, eps: float = 1e-5, mean=
     pr, ldr = _rows(r_out, M, N, dtype, "r_out")
     py, ldy = _rows(y, M, N, dtype, "y")
     pcode, ptype = _param_code(x, weight, bias, code)
-    if q_out is not None and (q_out.element_size() != 1 or q_out.numel() != M * N):
-        raise ValueError(f"q_out must hold {M * N} one-byte codes")
     a = LayerNormArgs(
         M, N, code, pcode, px, ldx, pres, ldres, pr, ldr, _vec(weight, N, ptype, "weight"), _vec(bias, N, ptype, "bias"),
         py, ldy, _vec(mean, M, torch.float32, "mean"), _vec(rstd, M, torch.float32, "rstd"), p, _rng(rng),
-        _ptr(scale, 4, "scale"), _ptr(q_out, M * N, "q_out"), _ptr(amax_out, 4, "amax_out"),
-        _ptr(sat_count, 8, "sat_count"), eps, fmt, flags)
+        _cell(scale, torch.float32, "scale"), _codes(q_out, M * N), _cell(amax_out, torch.float32, "amax_out"),
+        _cell(sat_count, torch.int64, "sat_count"), eps, fmt, flags)
     _check("layer_norm_fwd", lib().layer_norm_fwd(ctypes.byref(a), _stream(stream)))
 
 

@@ -41,30 +41,31 @@ namespace {
 // copies and reads its own pieces only, so it waits for its own copies and no
 // barrier guards the ring.  SHIFT: rows off the 16-byte grid (norm_ops.cuh); a
 // lane then reads its own granule and the next lane's.
-//   NARROW  `team` lanes (a power of two <= 32) of a warp take a row, up to 32
-//           columns a lane: the row's two sums are shuffles
-//   WIDE    `team` warps take a row, 32 columns a lane, and exchange their sums
-//           at a barrier of their own; a CTA is several such groups
+//   NARROW  `team` lanes (a power of two <= 32) of a warp take a row, up to four
+//           pieces a lane: the row's two sums are shuffles
+//   WIDE    `team` warps take a row, three or four pieces a lane, and exchange
+//           their sums at a barrier of their own; a CTA is several such groups
 //   BROAD   the same, one group of up to 16 warps, whose registers hold no weights
 // A CTA is as many warps as the registers hold, so that few partial rows are
-// written and added: 12, or 8 with the generator or with pieces of four columns.
+// written and added: 16 with up to 16 columns a lane, 12 with up to 32, 8 if the
+// generator is beside those.
 enum BwdMode { NARROW, WIDE, BROAD };
 
-__host__ __device__ constexpr int bwd_warps(int C, BwdMode mode, bool drop) {
-    return mode == BROAD ? 16 : drop || C > 4 ? 8 : 12;
+__host__ __device__ constexpr int bwd_warps(int columns, BwdMode mode, bool drop) {
+    return mode == BROAD || columns <= 16 ? 16 : drop ? 8 : 12;
 }
 // Rows of the ring: what the shared memory of a multiprocessor holds for them (a
 // stage is 1536 C bytes a warp).
-__host__ __device__ constexpr int bwd_ring_rows(int C, BwdMode mode, bool drop) {
-    if (mode == BROAD) return C > 4 ? 1 : 2;
-    return C <= 3 ? 3 : C == 4 ? (bwd_warps(C, mode, drop) == 12 ? 2 : 3) : 2;
+__host__ __device__ constexpr int bwd_ring_rows(int C, int columns, BwdMode mode, bool drop) {
+    const int warps = bwd_warps(columns, mode, drop);
+    return 3 * 1584 * C * warps <= kMaxRing ? 3 : 2 * 1584 * C * warps <= kMaxRing ? 2 : 1;
 }
 
 template <typename T, int C, BwdMode MODE, bool DROP, bool SHIFT>
-__global__ void __launch_bounds__(bwd_warps(C, MODE, DROP) * 32) ln_bwd_ring_kernel(const BwdParams<T> p, int team) {
+__global__ void __launch_bounds__(bwd_warps(C * 16 / sizeof(T), MODE, DROP) * 32) ln_bwd_ring_kernel(const BwdParams<T> p, int team) {
     extern __shared__ uint4 s_ring[];  // [warp][stage][dy, r, dresidual][c][slot]; at the end the groups' column sums
     __shared__ float2 s_sum[2][16];
-    constexpr int V = 16 / sizeof(T), H = V / 2, S = bwd_ring_rows(C, MODE, DROP);
+    constexpr int V = 16 / sizeof(T), H = V / 2, S = bwd_ring_rows(C, C * V, MODE, DROP);
     constexpr bool kHeld = MODE != BROAD, kCta = MODE != NARROW;  // weights in registers; otherwise from L1 in every row
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
     // NARROW: lanes a row, and each warp is a group; otherwise warps a row, and a group
@@ -303,16 +304,17 @@ __global__ void __launch_bounds__(bwd_warps(C, MODE, DROP) * 32) ln_bwd_ring_ker
 
 template <typename T, int C, BwdMode MODE, bool DROP, bool SHIFT>
 cudaError_t launch_ring_as(BwdParams<T>& p, int team, cudaStream_t stream) {
+    constexpr int V = 16 / sizeof(T);
     // groups (rows, or warps of narrow rows) a CTA: as many as fit, fewer where that leaves multiprocessors idle
     const int warps = MODE == NARROW ? 1 : team;
     const int64_t rows = MODE == NARROW ? 32 / (C > 1 ? 32 : team) : 1;
     const int64_t all = (p.M + rows - 1) / rows;
-    const int64_t groups = std::min<int64_t>(std::max(1, bwd_warps(C, MODE, DROP) / warps), (all + sm_count() - 1) / sm_count());
+    const int64_t groups = std::min<int64_t>(std::max(1, bwd_warps(C * V, MODE, DROP) / warps), (all + sm_count() - 1) / sm_count());
     const unsigned block = static_cast<unsigned>(groups) * warps * 32;
     // one wave: as many CTAs as run at a time (the answer is kept by CTA size)
     static std::atomic<int> per_sm[17];
     const auto kern = ln_bwd_ring_kernel<T, C, MODE, DROP, SHIFT>;
-    const size_t smem = size_t(bwd_ring_rows(C, MODE, DROP)) * 3 * C * (block / 32) * warp_slots(SHIFT, MODE == NARROW && C == 1) * 16;
+    const size_t smem = size_t(bwd_ring_rows(C, C * V, MODE, DROP)) * 3 * C * (block / 32) * warp_slots(SHIFT, MODE == NARROW && C == 1) * 16;
     std::atomic<int>& known = per_sm[block / 32];
     int n = known.load(std::memory_order_relaxed);
     if (n == 0) {
@@ -341,25 +343,23 @@ cudaError_t launch_bwd_ring(BwdParams<T>& p, cudaStream_t stream) {
     constexpr int V = 16 / sizeof(T);
     const int64_t pieces = (p.N + V - 1) / V;
     const int team = team_of(pieces);
-    constexpr int kMost = 32 / V;
-    const int64_t c = (pieces + team - 1) / team;
-    if (c <= kMost) {
-        switch (c) {
-            case 1: return launch_ring<T, 1, NARROW, SHIFT>(p, team, stream);
-            case 2: return launch_ring<T, 2, NARROW, SHIFT>(p, team, stream);
-            case 3: return launch_ring<T, 3, NARROW, SHIFT>(p, team, stream);
-            case 4: return launch_ring<T, 4, NARROW, SHIFT>(p, team, stream);
-            default: break;
-        }
-        if constexpr (V == 4) {
-            if (c == 5) return launch_ring<T, 5, NARROW, SHIFT>(p, team, stream);
-            if (c == 6) return launch_ring<T, 6, NARROW, SHIFT>(p, team, stream);
-            if (c == 7) return launch_ring<T, 7, NARROW, SHIFT>(p, team, stream);
-            if (c == 8) return launch_ring<T, 8, NARROW, SHIFT>(p, team, stream);
-        }
+    switch ((pieces + team - 1) / team) {
+        case 1: return launch_ring<T, 1, NARROW, SHIFT>(p, team, stream);
+        case 2: return launch_ring<T, 2, NARROW, SHIFT>(p, team, stream);
+        case 3: return launch_ring<T, 3, NARROW, SHIFT>(p, team, stream);
+        case 4: return launch_ring<T, 4, NARROW, SHIFT>(p, team, stream);
+        default: break;
     }
-    if (pieces <= 256 * kMost) return launch_ring<T, kMost, WIDE, SHIFT>(p, static_cast<int>(threads_of(pieces, kMost) / 32), stream);
-    if (pieces <= 512 * kMost) return launch_ring<T, kMost, BROAD, SHIFT>(p, static_cast<int>(threads_of(pieces, kMost) / 32), stream);
+    const int warps = static_cast<int>((pieces + 127) / 128);  // of a row
+    if (warps <= bwd_warps(4 * V, WIDE, p.drop.on && p.dbranch)) {
+        // (two or three warps may do with three pieces a lane; more need the fourth)
+        if (pieces <= 96 * warps) return launch_ring<T, 3, WIDE, SHIFT>(p, warps, stream);
+        return launch_ring<T, 4, WIDE, SHIFT>(p, warps, stream);
+    }
+    if (warps <= 16) return launch_ring<T, 4, BROAD, SHIFT>(p, warps, stream);
+    if constexpr (V == 4) {
+        if (pieces <= 16 * 256) return launch_ring<T, 8, BROAD, SHIFT>(p, static_cast<int>((pieces + 255) / 256), stream);
+    }
     return cudaErrorNotSupported;
 }
 

@@ -381,7 +381,19 @@ cudaError_t launch_fwd_ring(const FwdParams<T>& p, cudaStream_t stream) {
         case 8: return launch_ring<T, 8, NARROW, SHIFT>(p, team, 128, stream);
         default: break;
     }
-    if (pieces <= 256 * kMost) return launch_ring<T, kMost, WIDE, SHIFT>(p, 32, threads_of(pieces, kMost), stream);
+    if (pieces <= 256 * kMost) {
+        const int64_t warps = (pieces + 32 * kMost - 1) / (32 * kMost);
+        const unsigned block = static_cast<unsigned>(warps) * 32;
+        const int64_t c = (pieces + 32 * warps - 1) / (32 * warps);  // kMost, or less with few warps
+        if constexpr (V == 8) {
+            if (c <= 3) return launch_ring<T, 3, WIDE, SHIFT>(p, 32, block, stream);
+        } else {
+            if (c <= 5) return launch_ring<T, 5, WIDE, SHIFT>(p, 32, block, stream);
+            if (c == 6) return launch_ring<T, 6, WIDE, SHIFT>(p, 32, block, stream);
+            if (c == 7) return launch_ring<T, 7, WIDE, SHIFT>(p, 32, block, stream);
+        }
+        return launch_ring<T, kMost, WIDE, SHIFT>(p, 32, block, stream);
+    }
     if (pieces <= 512 * kMost) return launch_ring<T, kMost, BROAD, SHIFT>(p, 32, threads_of(pieces, kMost), stream);
     return cudaErrorNotSupported;
 }
