@@ -9,6 +9,8 @@ include/fp8q.h).  This package is its Python face:
                    device memory and the current stream.
 * ``downproj``  -- the call order and buffers of one training step with
                    delayed per-tensor (or 1x128 / 128x128 group) scales.
+* ``mlpstack``  -- whole MLP sub-layers, forward and backward: layer norm,
+                   dropout and residual around the FP8 GEMMs.
 * ``workloads`` -- seeded synthetic inputs of the benchmark workloads.
 * ``build``     -- nvcc build of libfp8q.so, in-tree.
 
@@ -20,10 +22,12 @@ from .binding import (ACT_IDENTITY, ACT_RELU, ACT_RELU2, DEV_BAD_AMAX, DEV_TIMEO
                       fp8_quant_fused, fp8q_naive_act, fp8q_naive_amax, fp8q_naive_cast, layer_norm_bwd,
                       layer_norm_bwd_workspace_bytes, layer_norm_fwd)
 from .downproj import DelayedScale, Fp8DownProj
+from .mlpstack import Fp8MlpStack
 
 __all__ = [
     "ACT_IDENTITY", "ACT_RELU", "ACT_RELU2", "DEV_BAD_AMAX", "DEV_TIMEOUT", "E4M3", "E5M2", "GROUP",
     "Fp8qError", "amax_history_update", "dropout_bwd", "dropout_fwd", "fp8_gemm_dgrad", "fp8_gemm_fwd",
     "fp8_quant_fused", "fp8q_naive_act", "fp8q_naive_amax", "fp8q_naive_cast", "layer_norm_bwd",
     "layer_norm_bwd_workspace_bytes", "layer_norm_fwd", "DelayedScale", "Fp8DownProj",
+    "Fp8MlpStack",
 ]

@@ -1,0 +1,149 @@
+"""A stack of GPT-2-style MLP sub-layers in FP8, forward and backward:
+
+    x_{l+1} = x_l + dropout( act( layer_norm(x_l) . W1_l ) . W2_l )
+
+Every product runs on the FP8 GEMMs with delayed per-tensor scales ("FP8 Training
+& Inference", FP8 Training Recipe: weights and activations in E4M3, gradients in
+E5M2), and what stands between them is one pass over the data each:
+
+    layer_norm_fwd   the previous sub-layer's dropout and residual addition, the norm, and
+                     the E4M3 codes that the up-projection reads
+    fp8_upproj_fwd   H = codes . W1, and act(H) quantized in its epilogue
+    fp8_gemm_fwd     the branch act(H) . W2
+    dropout_fwd      dropout and residual of the last sub-layer (no norm follows it)
+
+and back again: dropout_bwd, the gradient's casts, fp8_gemm_dgrad_act, the weight
+gradients, fp8_gemm_dgrad, and layer_norm_bwd, which adds the residual's gradient
+and forms the branch gradient of the sub-layer below.  No dropout mask is stored:
+each sub-layer has its own offset of the generator, and a backward pass forms the
+forward's masks again; ``advance()`` gives the next step new ones.
+
+Like ``Fp8DownProj`` this module owns buffers and the order of the calls; the
+arithmetic is libfp8q's.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import binding as B
+from .downproj import DelayedScale
+
+
+class _Layer:
+    """Buffers and scales of one sub-layer of M tokens, width D, hidden width K."""
+
+    def __init__(self, M: int, D: int, K: int, margin: float, history_len: int, seed: int, index: int, device):
+        bf = lambda *s: torch.empty(*s, dtype=torch.bfloat16, device=device)  # noqa: E731
+        q8 = lambda *s: torch.empty(*s, dtype=torch.uint8, device=device)  # noqa: E731
+        f32 = lambda *s: torch.empty(*s, dtype=torch.float32, device=device)  # noqa: E731
+        scale = lambda fmt: DelayedScale(fmt, margin, history_len, device)  # noqa: E731
+        self.n_s, self.h_s, self.w1_s, self.w2_s = (scale(B.E4M3) for _ in range(4))
+        self.db_s, self.dh_s = scale(B.E5M2), scale(B.E5M2)
+        # (seed, offset): sub-layers of one step differ in the offset's low half, steps in its high half
+        self.rng = torch.tensor([seed, index], dtype=torch.int64, device=device)
+        # forward
+        self.r, self.n, self.n_q = bf(M, D), bf(M, D), q8(M, D)
+        self.mean, self.rstd = f32(M), f32(M)
+        self.h, self.a, self.a_q = bf(M, K), bf(M, K), q8(M, K)
+        self.w1_q, self.w1_q_t = q8(D, K), q8(K, D)
+        self.w2_q, self.w2_q_t = q8(K, D), q8(D, K)
+        self.branch = bf(M, D)
+        # backward
+        self.db, self.db_q, self.db_q_t = bf(M, D), q8(M, D), q8(D, M)
+        self.dh, self.dh_q, self.dh_q_t = bf(M, K), q8(M, K), q8(K, M)
+        self.n_q_t, self.a_q_t = q8(D, M), q8(K, M)
+        self.dn, self.dr = bf(M, D), bf(M, D)
+        self.dw1, self.dw2 = bf(D, K), bf(K, D)
+        self.dweight, self.dbias = f32(D), f32(D)
+
+    def scales(self):
+        return (self.n_s, self.h_s, self.w1_s, self.w2_s)
+
+
+class Fp8MlpStack:
+    """``layers`` sub-layers on [M, D] BF16 activations with hidden width K.
+
+    Parameters of sub-layer l, passed to the calls as ``params[l]``: a tuple
+    (weight [D], bias [D], W1 [D,K] BF16, W2 [K,D] BF16), the layer norm's in
+    float32 or BF16.  M, D and K are multiples of 16 (the FP8 GEMMs' rule)."""
+
+    def __init__(self, M: int, D: int, K: int, layers: int = 1, *, p: float = 0.1, eps: float = 1e-5,
+                 act: int = B.ACT_RELU2, margin: float = 2.0, history_len: int = 1, seed: int = 0, device="cuda"):
+        if layers < 1 or M % 16 or D % 16 or K % 16:
+            raise ValueError("layers >= 1, and M, D, K multiples of 16")
+        self.M, self.D, self.K, self.p, self.eps, self.act = M, D, K, float(p), float(eps), act
+        self.layers = [_Layer(M, D, K, margin, history_len, seed, i, device) for i in range(layers)]
+        self.out = torch.empty(M, D, dtype=torch.bfloat16, device=device)
+        self.workspace = torch.empty(B.layer_norm_bwd_workspace_bytes(M, D), dtype=torch.uint8, device=device)
+        self.gemm_status = torch.zeros(1, dtype=torch.int32, device=device)
+
+    def _cast(self, s: DelayedScale, cast, calibrate: bool) -> None:
+        """cast(scale, amax, sat, flags); with calibrate first once for its amax alone, which seeds the scale."""
+        for _ in range(2 if calibrate else 1):
+            cast(s.scale, s.amax, s.sat, B.ACCUMULATE if s.clean else 0)
+            s.clean = False
+            if calibrate:
+                calibrate = False
+                s.update()
+
+    def forward(self, x: torch.Tensor, params, *, calibrate: bool = False) -> torch.Tensor:
+        """The stack's output [M, D] (a buffer of the stack).  ``calibrate``: take each tensor's scale from
+        its own values (a first step, whose histories are empty)."""
+        before = None
+        for L, (weight, bias, W1, W2) in zip(self.layers, params):
+            for W, s, q, q_t in ((W1, L.w1_s, L.w1_q, L.w1_q_t), (W2, L.w2_s, L.w2_q, L.w2_q_t)):
+                self._cast(s, lambda sc, am, sat, fl: B.fp8_quant_fused_ex(
+                    W, B.ACT_IDENTITY, B.E4M3, sc, q_out=q, q_t_out=q_t, amax_out=am, sat_count=sat, flags=fl), calibrate)
+            if before is None:
+                L.r = x
+                into = dict(x=x)
+            else:  # the dropout and residual of the sub-layer below, in the same pass
+                into = dict(x=before.branch, residual=before.r, r_out=L.r, p=self.p, rng=before.rng)
+            self._cast(L.n_s, lambda sc, am, sat, fl: B.layer_norm_fwd(
+                weight=weight, bias=bias, y=L.n, eps=self.eps, mean=L.mean, rstd=L.rstd, fmt=B.E4M3, scale=sc,
+                q_out=L.n_q, amax_out=am, sat_count=sat, flags=fl, **into), calibrate)
+            self._cast(L.h_s, lambda sc, am, sat, fl: B.fp8_upproj_fwd(
+                L.n_q, L.w1_q_t, L.n_s.scale, L.w1_s.scale, sc, L.a_q, act=self.act, h_out=L.h, act_out=L.a,
+                amax_out=am, sat_count=sat, flags=fl, status=self.gemm_status), calibrate)
+            B.fp8_gemm_fwd(L.a_q, L.w2_q_t, L.h_s.scale, L.w2_s.scale, L.branch, status=self.gemm_status)
+            for s in L.scales():
+                s.update()
+            before = L
+        B.dropout_fwd(before.branch, self.out, self.p, before.rng, residual=before.r)
+        return self.out
+
+    def backward(self, dout: torch.Tensor, params, *, calibrate: bool = False):
+        """(dx, grads) of the last forward(): dx [M, D], and per sub-layer (dweight, dbias, dW1, dW2)."""
+        last = self.layers[-1]
+        B.dropout_bwd(dout, last.db, self.p, last.rng)
+        dres, grads = dout, []
+        for i in range(len(self.layers) - 1, -1, -1):
+            L, below = self.layers[i], self.layers[i - 1] if i else None
+            weight = params[i][0]
+            sn, sh, sw1, sw2 = (s.last_scale for s in L.scales())
+            self._cast(L.db_s, lambda sc, am, sat, fl: B.fp8_quant_fused_ex(
+                L.db, B.ACT_IDENTITY, B.E5M2, sc, q_out=L.db_q, q_t_out=L.db_q_t, amax_out=am, sat_count=sat,
+                flags=fl), calibrate)
+            B.fp8_gemm_dgrad_act(L.db_q, L.w2_q, L.db_s.scale, sw2, L.h, L.dh, act=self.act, status=self.gemm_status)
+            B.fp8_quant_fused(L.a, B.ACT_IDENTITY, B.E4M3, sh, q_t_out=L.a_q_t)
+            B.fp8_gemm_wgrad(L.a_q_t, L.db_q_t, sh, L.db_s.scale, L.dw2, status=self.gemm_status)
+            self._cast(L.dh_s, lambda sc, am, sat, fl: B.fp8_quant_fused_ex(
+                L.dh, B.ACT_IDENTITY, B.E5M2, sc, q_out=L.dh_q, q_t_out=L.dh_q_t, amax_out=am, sat_count=sat,
+                flags=fl), calibrate)
+            B.fp8_gemm_dgrad(L.dh_q, L.w1_q, L.dh_s.scale, sw1, L.dn, status=self.gemm_status)
+            B.fp8_quant_fused(L.n, B.ACT_IDENTITY, B.E4M3, sn, q_t_out=L.n_q_t)
+            B.fp8_gemm_wgrad(L.n_q_t, L.dh_q_t, sn, L.dh_s.scale, L.dw1, status=self.gemm_status)
+            # the norm's gradient, the residual's added; and the branch gradient of the sub-layer below
+            drop = {} if below is None else dict(p=self.p, rng=below.rng, dbranch=below.db)
+            B.layer_norm_bwd(L.dn, L.r, L.mean, L.rstd, weight, L.dr, dresidual=dres, dweight=L.dweight, dbias=L.dbias,
+                             workspace=self.workspace, **drop)
+            L.db_s.update()
+            L.dh_s.update()
+            dres = L.dr
+            grads.append((L.dweight, L.dbias, L.dw1, L.dw2))
+        return dres, grads[::-1]
+
+    def advance(self) -> None:
+        """New dropout masks for the next step (on the device: a captured step may contain it)."""
+        for L in self.layers:
+            L.rng[1:] += 1 << 32
