@@ -139,11 +139,16 @@ int launch_bwd(const fp8q_layer_norm_bwd_args& a, const Dropout& drop, cudaStrea
     p.parts = parts_of(a.M, a.N);
     const bool cols = a.dweight || a.dbias;
     if (!cols) p.part = nullptr;
+    p.dweight = a.dweight;
+    p.dbias = a.dbias;
+    p.accumulate = (a.flags & FP8Q_ACCUMULATE) != 0;
+    bool reduce = cols;
     constexpr int V = 16 / sizeof(T);
     const bool pieces = a.N % V == 0 && rows16(a.dy, a.ld_dy, sizeof(T)) && rows16(a.r, a.ld_r, sizeof(T)) &&
                         rows16(a.dresidual, a.ld_dresidual, sizeof(T)) && rows16(a.dx, a.ld_dx, sizeof(T)) &&
                         rows16(a.dbranch, a.ld_dbranch, sizeof(T)) && aligned16(a.weight);
     cudaError_t e = pieces ? launch_bwd_ring<T, false>(p, stream) : launch_bwd_ring<T, true>(p, stream);
+    if (e == cudaSuccess) reduce = cols && p.parts > 1;
     if (e == cudaErrorNotSupported) {
         e = cudaSuccess;
         if (cols)
@@ -154,10 +159,9 @@ int launch_bwd(const fp8q_layer_norm_bwd_args& a, const Dropout& drop, cudaStrea
                            dim3(static_cast<unsigned>(std::min<int64_t>(a.M, int64_t(sm_count()) * 8))), dim3(256), 0,
                            stream, p);
     }
-    if (cols && e == cudaSuccess)
+    if (reduce && e == cudaSuccess)
         e = launch_pdl(ln_bwd_reduce_kernel, dim3(static_cast<unsigned>((2 * a.N + 31) / 32)), dim3(1024), 0, stream,
-                       static_cast<const float*>(p.part), p.parts, a.N, a.dweight, a.dbias,
-                       (a.flags & FP8Q_ACCUMULATE) != 0);
+                       static_cast<const float*>(p.part), p.parts, a.N, a.dweight, a.dbias, p.accumulate);
     if (e != cudaSuccess) {
         (void)cudaGetLastError();
         return FP8Q_ERR_CUDA;

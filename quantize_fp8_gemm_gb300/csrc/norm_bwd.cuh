@@ -28,8 +28,11 @@ struct BwdParams {
     T* dbranch;
     int64_t ld_db;
     Dropout drop;
-    float* part;  // [parts][2][N]: dweight and dbias sums of a set of rows
+    float* part;  // [parts][2][N]: dweight and dbias sums of a set of rows; NULL: not wanted
     int parts;
+    float* dweight;  // the results, for a call of one part
+    float* dbias;
+    bool accumulate;
 };
 
 namespace {
@@ -298,18 +301,25 @@ __global__ void __launch_bounds__(bwd_warps(C * 16 / sizeof(T), MODE, DROP) * 32
         const float* from = reinterpret_cast<const float*>(s_ring) + j;
         float sum = from[0];
         for (int k = 1; k < groups; ++k) sum += from[k * 2 * N];
-        part[j] = sum;
+        if (gridDim.x > 1) {
+            part[j] = sum;
+        } else if (float* out = j < N ? p.dweight : p.dbias) {  // the one CTA's sums are the result
+            out += j < N ? j : j - N;
+            *out = p.accumulate ? *out + sum : sum;
+        }
     }
 }
 
 template <typename T, int C, BwdMode MODE, bool DROP, bool SHIFT>
 cudaError_t launch_ring_as(BwdParams<T>& p, int team, cudaStream_t stream) {
     constexpr int V = 16 / sizeof(T);
-    // groups (rows, or warps of narrow rows) a CTA: as many as fit, fewer where that leaves multiprocessors idle
+    // groups (rows, or warps of narrow rows) a CTA: as many as fit, fewer where that leaves multiprocessors
+    // idle -- but one CTA for what it takes at a time, whose sums need no second kernel
     const int warps = MODE == NARROW ? 1 : team;
     const int64_t rows = MODE == NARROW ? 32 / (C > 1 ? 32 : team) : 1;
     const int64_t all = (p.M + rows - 1) / rows;
-    const int64_t groups = std::min<int64_t>(std::max(1, bwd_warps(C * V, MODE, DROP) / warps), (all + sm_count() - 1) / sm_count());
+    const int64_t most = std::max(1, bwd_warps(C * V, MODE, DROP) / warps);
+    const int64_t groups = all <= most ? all : std::min<int64_t>(most, (all + sm_count() - 1) / sm_count());
     const unsigned block = static_cast<unsigned>(groups) * warps * 32;
     // one wave: as many CTAs as run at a time (the answer is kept by CTA size)
     static std::atomic<int> per_sm[17];

@@ -48,14 +48,18 @@ namespace {
 enum FwdMode { NARROW, WIDE, BROAD };
 
 // With 40 columns a lane or more the generator's registers beside 128 of weights
-// would leave two warps a scheduler: the CTA's weights are then in shared memory
-// (BROAD: too many for that, they come from L1).
+// would leave two warps a scheduler: the CTA's weights are then in shared memory,
+// as BROAD's are where one input's ring leaves room for them (otherwise they come
+// from L1 and L2 in every row, at twice the row's own bytes).
 __host__ __device__ constexpr bool weights_held(int columns, bool drop, FwdMode mode) {
     return mode != BROAD && !(drop && columns >= 40);
 }
+__host__ __device__ constexpr bool weights_shared(int columns, bool drop, bool res, FwdMode mode) {
+    return !weights_held(columns, drop, mode) && (mode == NARROW || (mode == BROAD && !res));
+}
 // Rows of the ring: what leaves room for three CTAs a multiprocessor, or fits at all.
 __host__ __device__ constexpr int ring_rows(int C, int columns, bool drop, bool res, FwdMode mode) {
-    if (mode == BROAD) return !res ? 3 : C == 8 ? 1 : 2;
+    if (mode == BROAD) return C == 8 ? 1 : 2;
     return drop && res && columns >= 40 ? 2 : 3;
 }
 
@@ -89,9 +93,10 @@ ln_fwd_ring_kernel(const FwdParams<T> p, int team) {
     };
     pdl_wait();
 
-    // [w, b][four columns of a piece][c][lane]: lanes 16 bytes apart
-    constexpr bool kShared = !kHeld && MODE == NARROW;
-    float4* const s_par = reinterpret_cast<float4*>(s_ring + nw * (S * TENSORS * C * warp_slots(SHIFT, !kCta && C == 1))) + lane;
+    // [warp of a CTA's row][w, b][four columns of a piece][c][lane]: lanes 16 bytes apart
+    constexpr bool kShared = weights_shared(C * V, DROP, RES, MODE);
+    float4* const s_par = reinterpret_cast<float4*>(s_ring + nw * (S * TENSORS * C * warp_slots(SHIFT, !kCta && C == 1))) +
+                          (kCta ? warp * (2 * (V / 4) * C * 32) : 0) + lane;
     f32x2 w[kHeld ? C : 1][H], b[kHeld ? C : 1][H];
     int own = 0;  // elements of this thread; of this warp later
 #pragma unroll
@@ -107,7 +112,7 @@ ln_fwd_ring_kernel(const FwdParams<T> p, int team) {
             load_params2<T, V, SHIFT>(p.b, (t + c * 32) * V, N, b[c]);
         }
         if constexpr (kShared) {
-            if (warp == c % 4) {
+            if (kCta || warp == c % 4) {
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     f32x2 f[H];
@@ -338,7 +343,7 @@ cudaError_t launch_ring_as(const FwdParams<T>& p, int team, unsigned block, cuda
     const auto kern = ln_fwd_ring_kernel<T, C, DROP, RES, MODE, SHIFT>;
     size_t smem = size_t(ring_rows(C, C * V, DROP, RES, MODE)) * (RES ? 2 : 1) * C * (block / 32) *
                         warp_slots(SHIFT, MODE == NARROW && C == 1) * 16;
-    if (!weights_held(C * V, DROP, MODE) && MODE == NARROW) smem += size_t(2) * C * 32 * V * sizeof(float);
+    if (weights_shared(C * V, DROP, RES, MODE)) smem += size_t(2) * C * 32 * V * sizeof(float) * (MODE == NARROW ? 1 : block / 32);
     std::atomic<int>& known = per_sm[block / 32];
     int n = known.load(std::memory_order_relaxed);
     if (n == 0) {
