@@ -84,29 +84,33 @@ __global__ void __launch_bounds__(256) ln_bwd_cols_kernel(const BwdParams<T> p) 
 }
 
 // dweight / dbias = the partial rows' sums in a fixed order.  A block takes 32
-// columns; warp k of its 32 adds parts k, k + 32, ..., then the warps' sums are
-// added in order.
-__global__ void __launch_bounds__(1024) ln_bwd_reduce_kernel(const float* part, int parts, int64_t N, float* dweight,
-                                                             float* dbias, bool accumulate) {
-    __shared__ float s[32][33];
-    pdl_wait();
+// columns; warp k of its 16 adds parts k, k + 16, ..., then the warps' sums are
+// added by a tree of fixed shape.
+constexpr int kReduceWarps = 16;
+__global__ void __launch_bounds__(kReduceWarps * 32) ln_bwd_reduce_kernel(const float* part, int parts, int64_t N,
+                                                                          float* dweight, float* dbias, bool accumulate) {
+    __shared__ float s[kReduceWarps][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t j = static_cast<int64_t>(blockIdx.x) * 32 + lane;  // column of [2][N]
+    pdl_wait();
     float sum = 0.0f;
     if (j < 2 * N) {
-#pragma unroll 8
-        for (int k = warp; k < parts; k += 32) sum += part[static_cast<int64_t>(k) * 2 * N + j];
+        const float* from = part + j;
+#pragma unroll 10
+        for (int k = warp; k < parts; k += kReduceWarps) sum += from[static_cast<int64_t>(k) * 2 * N];
     }
     s[warp][lane] = sum;
     __syncthreads();
-    sum = s[lane][warp];  // column `warp` of the block
-#pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + warp;
-    if (lane == 0 && col < 2 * N) {
-        float* out = col < N ? dweight : dbias;
+    if (warp < kReduceWarps / 4 && j < 2 * N) {  // sixteen values of a column by fours
+        sum = (s[4 * warp][lane] + s[4 * warp + 1][lane]) + (s[4 * warp + 2][lane] + s[4 * warp + 3][lane]);
+        s[4 * warp][lane] = sum;
+    }
+    __syncthreads();
+    if (warp == 0 && j < 2 * N) {
+        sum = (s[0][lane] + s[4][lane]) + (s[8][lane] + s[12][lane]);
+        float* out = j < N ? dweight : dbias;
         if (out) {
-            out += col < N ? col : col - N;
+            out += j < N ? j : j - N;
             *out = accumulate ? *out + sum : sum;
         }
     }
@@ -160,7 +164,7 @@ int launch_bwd(const fp8q_layer_norm_bwd_args& a, const Dropout& drop, cudaStrea
                            stream, p);
     }
     if (reduce && e == cudaSuccess)
-        e = launch_pdl(ln_bwd_reduce_kernel, dim3(static_cast<unsigned>((2 * a.N + 31) / 32)), dim3(1024), 0, stream,
+        e = launch_pdl(ln_bwd_reduce_kernel, dim3(static_cast<unsigned>((2 * a.N + 31) / 32)), dim3(kReduceWarps * 32), 0, stream,
                        static_cast<const float*>(p.part), p.parts, a.N, a.dweight, a.dbias, p.accumulate);
     if (e != cudaSuccess) {
         (void)cudaGetLastError();

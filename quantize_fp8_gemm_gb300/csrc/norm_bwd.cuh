@@ -276,12 +276,15 @@ __global__ void __launch_bounds__(bwd_warps(C * 16 / sizeof(T), MODE, DROP) * 32
     cp_async_wait<0>();
     if (p.part == nullptr) return;
 
-    // the groups' sums to shared memory, where the ring was; their sum, in order, is the partial row
+    // The groups' sums to shared memory, where the ring was; their sum, in order, is the partial row.
+    // Column i of a warp's piece (c, lane) is at [c][i][lane], rows kPitch floats apart: the lanes
+    // write 32 banks, and 32 adjacent columns (V columns of 32 / V pieces) are read from 32 banks.
+    constexpr int kPitch = 32 + 32 / V, kWarp = C * V * kPitch;
     __syncthreads();
-    float* s_part = reinterpret_cast<float*>(s_ring) + group * 2 * N;
+    float* const s_part = reinterpret_cast<float*>(s_ring);  // [group][dw, db][warp of the group][c][i][lane]
+    float* const own = s_part + (group * 2 * group_warps + warp - group * group_warps) * kWarp + lane;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-        const int j0 = (t + c * 32) * V;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const float2 pw = split(dw[c][i / 2]), pb = split(db[c][i / 2]);
@@ -290,21 +293,22 @@ __global__ void __launch_bounds__(bwd_warps(C * 16 / sizeof(T), MODE, DROP) * 32
                 a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
                 b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
             }
-            if (lane >= lanes || j0 + i >= N) continue;
-            s_part[j0 + i] = a;
-            s_part[N + j0 + i] = b;
+            own[(c * V + i) * kPitch] = a;
+            own[group_warps * kWarp + (c * V + i) * kPitch] = b;
         }
     }
     __syncthreads();
     float* part = p.part + static_cast<int64_t>(blockIdx.x) * 2 * p.N;
     for (int j = threadIdx.x; j < 2 * N; j += blockDim.x) {
-        const float* from = reinterpret_cast<const float*>(s_ring) + j;
+        const int col = j < N ? j : j - N, piece = col / V;
+        const int run = piece / 32;  // of the row: C runs a warp
+        const float* from = s_part + ((j < N ? 0 : group_warps) + run / C) * kWarp + ((run % C) * V + col % V) * kPitch + piece % 32;
         float sum = from[0];
-        for (int k = 1; k < groups; ++k) sum += from[k * 2 * N];
+        for (int k = 1; k < groups; ++k) sum += from[k * 2 * group_warps * kWarp];
         if (gridDim.x > 1) {
             part[j] = sum;
         } else if (float* out = j < N ? p.dweight : p.dbias) {  // the one CTA's sums are the result
-            out += j < N ? j : j - N;
+            out += col;
             *out = p.accumulate ? *out + sum : sum;
         }
     }
