@@ -126,14 +126,14 @@ __global__ void __launch_bounds__(256, 4) dropout_rows_kernel(const DropParams<T
     constexpr int V = 16 / sizeof(T), H = V / 2, kSlots = warp_slots(true, true), kStage = (RES ? 2 : 1) * kSlots;
     extern __shared__ uint4 s_ring[];  // [warp][stage][x, residual][slot]
     const int lane = threadIdx.x & 31, place = lane & (team - 1);
-    const int64_t warp = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-    const int64_t warps = static_cast<int64_t>(gridDim.x) * blockDim.x >> 5;
-    const int parts = (chunks + deep - 1) / deep;  // warps that a row takes
-    const int first = static_cast<int>(warp % parts) * deep, runs = min(deep, chunks - first);  // this one's runs of it
-    const uint32_t step = static_cast<uint32_t>(warps / parts) * (32 / team);  // rows that all warps take at a time
+    const uint32_t warp = blockIdx.x * 8 + (threadIdx.x >> 5), warps = gridDim.x * 8;
+    const uint32_t parts = static_cast<uint32_t>((chunks + deep - 1) / deep);  // warps that a row takes
+    const uint32_t set = warp / parts, sets = warps / parts;
+    const int first = static_cast<int>(warp - set * parts) * deep, runs = min(deep, chunks - first);  // this one's runs of it
+    const uint32_t step = sets * (32 / team);  // rows that all warps take at a time
     uint4* const ring = s_ring + (threadIdx.x >> 5) * (kRing * kStage) + lane + lane / team;
     pdl_wait();
-    if (warp / parts >= warps / parts) return;  // the warps that make no full set
+    if (set >= sets) return;  // the warps that make no full set
 
     const int64_t left = p.N - (static_cast<int64_t>(first) * 32 + place) * V;  // columns from this thread's first
     Philox g;
@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(256, 4) dropout_rows_kernel(const DropParams<T
         first_m0 = kPhiloxM0 * ((static_cast<uint32_t>(first) * 32 + place) * (V / 4));
     }
     const uint32_t M = static_cast<uint32_t>(p.M);
-    uint32_t base = static_cast<uint32_t>(warp / parts) * (32 / team), row = base + lane / team;
+    uint32_t base = set * (32 / team), row = base + lane / team;
     const int64_t column = static_cast<int64_t>(first) * 32 * V;
     const T *x_at = p.x + static_cast<int64_t>(row) * p.ldx + column, *r_at = p.res + static_cast<int64_t>(row) * p.ld_res + column;
     T* y_at = p.y + static_cast<int64_t>(row) * p.ldy + column;

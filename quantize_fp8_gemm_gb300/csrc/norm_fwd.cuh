@@ -141,15 +141,19 @@ ln_fwd_ring_kernel(const FwdParams<T> p, int team) {
     uint32_t amax = 0, amax2 = 0, nsat = 0;
 
     const int rows_warp = kCta ? 1 : 32 / team, rows_cta = kCta ? 1 : rows_warp * nw;
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * rows_cta;
-    const int64_t base0 = static_cast<int64_t>(blockIdx.x) * rows_cta;
-    const int64_t sub = kCta ? 0 : warp * rows_warp + lane / team;
+    // (M is below 2^31, and so few rows ahead of it below 2^32)
+    const uint32_t M = static_cast<uint32_t>(p.M), stride = gridDim.x * rows_cta, base0 = blockIdx.x * rows_cta;
+    const uint32_t sub = kCta ? 0 : warp * rows_warp + lane / team;
+    constexpr bool kRun = C <= 2;
+    RowWalk<const T, kRun> x_in(p.x, p.ldx, base0 + sub, stride), res_in(p.res, p.ld_res, base0 + sub, stride);
+    RowWalk<const T, kRun> x_at = x_in, res_at = res_in;
+    RowWalk<T, kRun> r_at(p.r_out, p.ld_r, base0 + sub, stride), y_at(p.y, p.ldy, base0 + sub, stride);
+    RowWalk<uint8_t, kRun> q_at(p.quant.q, p.N, base0 + sub, stride);
     constexpr int kSlots = warp_slots(SHIFT, !kCta && C == 1), kStage = TENSORS * C * kSlots;
     uint4* const ring = s_ring + warp * (S * kStage) + lane + (SHIFT ? lane / team : 0);  // [stage][tensor][c][slot]
     const bool team_end = SHIFT && (kCta ? lane == 31 : t == team - 1);
     const uint32_t ring_at = smem_u32(ring);
-    auto fill_tensor = [&](uint32_t to, const T* x, int64_t ld, int64_t row) {
-        const T* start = x + row * ld;
+    auto fill_tensor = [&](uint32_t to, const T* start) {
         const uint32_t mis = SHIFT ? granule_offset(start) : 0;
         const uint8_t* first = reinterpret_cast<const uint8_t*>(start) - mis;
         const int end = N * static_cast<int>(sizeof(T)) + static_cast<int>(mis);
@@ -164,13 +168,15 @@ ln_fwd_ring_kernel(const FwdParams<T> p, int team) {
         }
     };
     // the pieces of a row; nothing for a row past the last, whose results are not used
-    auto fill = [&](int stage, int64_t row) {
-        if (row < p.M) {
+    auto fill = [&](int stage, uint32_t row) {
+        if (row < M) {
             const uint32_t to = ring_at + stage * kStage * 16;
-            fill_tensor(to, p.x, p.ldx, row);
-            if constexpr (RES) fill_tensor(to + C * kSlots * 16, p.res, p.ld_res, row);
+            fill_tensor(to, x_in.at(row));
+            if constexpr (RES) fill_tensor(to + C * kSlots * 16, res_in.at(row));
         }
         cp_async_commit();
+        x_in.next();
+        if constexpr (RES) res_in.next();
     };
     if constexpr (!SHIFT) {  // pieces past the row are zeros in every stage, and stay so
 #pragma unroll
@@ -186,18 +192,18 @@ ln_fwd_ring_kernel(const FwdParams<T> p, int team) {
     // where a warp takes one row, it is done at its own last; where it shares a barrier or
     // its lanes take several, at the CTA's
     constexpr bool kOwnEnd = MODE == NARROW && C > 1;
-    for (int64_t base = base0; (kOwnEnd ? base + sub : base) < p.M; base += stride) {
-        const int64_t row = base + sub;
-        const bool in = kOwnEnd || kCta || row < p.M;
+    for (uint32_t base = base0; (kOwnEnd ? base + sub : base) < M; base += stride) {
+        const uint32_t row = base + sub;
+        const bool in = kOwnEnd || kCta || row < M;
         fill(stage == 0 ? S - 1 : stage - 1, row + (S - 1) * stride);
         cp_async_wait<S - 1>();
         const uint4* at = ring + stage * kStage;
         if constexpr (SHIFT) __syncwarp();
         uint64_t row_m0 = 0;
-        if constexpr (DROP) row_m0 = g.row(static_cast<uint32_t>(row));
-        const uint32_t mis_x = SHIFT ? granule_offset(p.x + row * p.ldx) : 0;
-        const uint32_t mis_r = SHIFT && RES ? granule_offset(p.res + row * p.ld_res) : 0;
-        T* r_row = p.r_out + row * p.ld_r;
+        if constexpr (DROP) row_m0 = g.row(row);
+        const uint32_t mis_x = SHIFT ? granule_offset(x_at.at(row)) : 0;
+        const uint32_t mis_r = SHIFT && RES ? granule_offset(res_at.at(row)) : 0;
+        T* r_row = r_at.at(row);
         f32x2 v[C][H], sum2 = zero2;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
@@ -233,10 +239,9 @@ ln_fwd_ring_kernel(const FwdParams<T> p, int team) {
             if constexpr (H == 4) part = add2(part, add2(v[c][2], v[c][3]));
             sum2 = add2(sum2, part);
         }
-        const int width = kCta ? 32 : team;
         const float2 halves = split(sum2);
         float sum = halves.x + halves.y;
-        for (int o = width / 2; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        sum = team_sum<C == 1 && !kCta>(sum, team);
         float mean = sum * inv_own;
         f32x2 shift = pair_of(-mean, -mean), dev2[2] = {zero2, zero2};
 #pragma unroll
@@ -254,7 +259,7 @@ ln_fwd_ring_kernel(const FwdParams<T> p, int team) {
         }
         const float2 devs = split(add2(dev2[0], dev2[1]));
         float dev = devs.x + devs.y;
-        for (int o = width / 2; o; o >>= 1) dev += __shfl_xor_sync(0xFFFFFFFFu, dev, o);
+        dev = team_sum<C == 1 && !kCta>(dev, team);
         if constexpr (kCta) {
             // two buffers: a warp that runs ahead writes the other one, and cannot reach this one
             // again before every warp has passed the next row's barrier
@@ -277,8 +282,8 @@ ln_fwd_ring_kernel(const FwdParams<T> p, int team) {
         }
         const float rstd = 1.0f / sqrtf(__fmaf_rn(dev, inv_n, p.eps));
         const f32x2 scale = pair_of(rstd, rstd);
-        T* y_row = p.y + row * p.ldy;
-        uint8_t* q_row = p.quant.q + row * p.N;
+        T* y_row = y_at.at(row);
+        uint8_t* q_row = q_at.at(row);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int valid = in && has(c) ? count(c) : 0;
@@ -328,6 +333,11 @@ ln_fwd_ring_kernel(const FwdParams<T> p, int team) {
             if (p.rstd) p.rstd[row] = rstd;
         }
         stage = stage == S - 1 ? 0 : stage + 1;
+        x_at.next();
+        res_at.next();
+        r_at.next();
+        y_at.next();
+        q_at.next();
         if constexpr (SHIFT) __syncwarp();  // the granules that a neighbour read may be overwritten now
     }
     pdl_launch_dependents();

@@ -482,6 +482,33 @@ inline unsigned threads_of(int64_t pieces, int c) { return static_cast<unsigned>
 constexpr int kMaxRing = 208 * 1024;  // dynamic shared memory that a ring may take
 inline bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+// The rows that a thread comes to, `stride` apart.  RUN: the address is carried
+// from row to row (two registers more, and no 64-bit product a row: worth it
+// where a row is few pieces a lane).
+template <typename T, bool RUN>
+struct RowWalk {
+    T* p;
+    int64_t step;
+    __device__ __forceinline__ RowWalk(T* base, int64_t ld, uint32_t row0, uint32_t stride)
+        : p(RUN ? base + row0 * ld : base), step(RUN ? stride * ld : ld) {}
+    __device__ __forceinline__ T* at(uint32_t row) const { return RUN ? p : p + row * step; }
+    __device__ __forceinline__ void next() {
+        if constexpr (RUN) p += step;
+    }
+};
+
+// Sum over the lanes of a warp, or (PART) of each team of `team` of them (a power
+// of two), in every lane; the order of the additions depends on the team alone.
+template <bool PART>
+__device__ __forceinline__ float team_sum(float v, int team) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        const float other = __shfl_xor_sync(0xFFFFFFFFu, v, o);
+        v += !PART || o < team ? other : 0.0f;
+    }
+    return v;
+}
+
 // Sum over the CTA's threads of two values, in every thread; the order of the
 // additions depends on blockDim.x alone.  `s` holds 2 * 32 + 2 floats.
 __device__ __forceinline__ float2 block_sum2(float a, float b, float* s) {
