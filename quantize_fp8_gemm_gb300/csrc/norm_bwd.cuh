@@ -279,30 +279,7 @@ __global__ void __launch_bounds__(bwd_warps(C * 16 / sizeof(T), MODE, DROP) * 32
     // The groups' sums to shared memory, where the ring was; their sum, in order, is the partial row.
     // Column i of a warp's piece (c, lane) is at [c][i][lane], rows kPitch floats apart: the lanes
     // write 32 banks, and 32 adjacent columns (V columns of 32 / V pieces) are read from 32 banks.
-    // (A CTA of one group writes them at once: few rows, where the kernel's length counts.)
     constexpr int kPitch = 32 + 32 / V, kWarp = C * V * kPitch;
-    float* part = p.part + static_cast<int64_t>(blockIdx.x) * 2 * p.N;
-    auto put_sum = [&](int j, float sum, bool bias) {
-        if (gridDim.x > 1) {
-            part[bias ? N + j : j] = sum;
-        } else if (float* out = bias ? p.dbias : p.dweight) {  // the one CTA's sums are the result
-            out[j] = p.accumulate ? out[j] + sum : sum;
-        }
-    };
-    if (MODE == WIDE && groups == 1) {
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float2 pw = split(dw[c][i / 2]), pb = split(db[c][i / 2]);
-                const int j = (t + c * 32) * V + i;
-                if (j >= N) continue;
-                put_sum(j, i & 1 ? pw.y : pw.x, false);
-                put_sum(j, i & 1 ? pb.y : pb.x, true);
-            }
-        }
-        return;
-    }
     __syncthreads();
     float* const s_part = reinterpret_cast<float*>(s_ring);  // [group][dw, db][warp of the group][c][i][lane]
     float* const own = s_part + (group * 2 * group_warps + warp - group * group_warps) * kWarp + lane;
@@ -321,13 +298,19 @@ __global__ void __launch_bounds__(bwd_warps(C * 16 / sizeof(T), MODE, DROP) * 32
         }
     }
     __syncthreads();
+    float* part = p.part + static_cast<int64_t>(blockIdx.x) * 2 * p.N;
     for (int j = threadIdx.x; j < 2 * N; j += blockDim.x) {
         const int col = j < N ? j : j - N, piece = col / V;
         const int run = piece / 32;  // of the row: C runs a warp
         const float* from = s_part + ((j < N ? 0 : group_warps) + run / C) * kWarp + ((run % C) * V + col % V) * kPitch + piece % 32;
         float sum = from[0];
         for (int k = 1; k < groups; ++k) sum += from[k * 2 * group_warps * kWarp];
-        put_sum(col, sum, j >= N);
+        if (gridDim.x > 1) {
+            part[j] = sum;
+        } else if (float* out = j < N ? p.dweight : p.dbias) {  // the one CTA's sums are the result
+            out += col;
+            *out = p.accumulate ? *out + sum : sum;
+        }
     }
 }
 

@@ -305,8 +305,6 @@ struct Philox {
         for (int i = 0; i < 9; ++i) {
             a[i] = k0 + (i + 1) * 0x9E3779B9u;
             b[i] = k1 + (i + 1) * 0xBB67AE85u;
-            // kept in registers: formed anew they are two additions a round of every block
-            asm volatile("" : "+r"(a[i]), "+r"(b[i]));
         }
     }
     // Round 2's product of the row: a row's blocks share it.
