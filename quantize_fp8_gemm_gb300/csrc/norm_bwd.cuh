@@ -167,16 +167,16 @@ __global__ void __launch_bounds__(bwd_warps(C * 16 / sizeof(T), MODE, DROP) * 32
         const uint32_t mis_r = SHIFT ? granule_offset(p.r + row * p.ld_r) : 0;
         const uint32_t mis_dres = SHIFT && p.dres ? granule_offset(p.dres + row * p.ld_dres) : 0;
         const f32x2 shift = pair_of(-mean, -mean), scale = pair_of(rstd, rstd);
-        // dy, xhat and g = dy * w of piece c
-        auto inputs = [&](int c, f32x2 (&dy)[H], f32x2 (&xhat)[H], f32x2 (&gw)[H]) {
+        // dy, r and g = dy * w of piece c
+        auto inputs = [&](int c, f32x2 (&dy)[H], f32x2 (&r)[H], f32x2 (&gw)[H]) {
             Piece<T, V> a;
             a.raw = read_piece<SHIFT>(at + c * kSlots, mis_dy);
             unpack2(a, dy);
             a.raw = read_piece<SHIFT>(at + (C + c) * kSlots, mis_r);
-            unpack2(a, xhat);
+            unpack2(a, r);
             if (SHIFT && count(c) < V) {  // the row's end: what follows in the granule is not its own
                 zero_from<V>(dy, count(c));
-                zero_from<V>(xhat, count(c));
+                zero_from<V>(r, count(c));
             }
             f32x2 wl[H];
             if constexpr (!kHeld) {
@@ -186,7 +186,6 @@ __global__ void __launch_bounds__(bwd_warps(C * 16 / sizeof(T), MODE, DROP) * 32
             }
 #pragma unroll
             for (int i = 0; i < H; ++i) {
-                xhat[i] = mul2(add2(xhat[i], shift), scale);
                 gw[i] = mul2(dy[i], kHeld ? w[kHeld ? c : 0][i] : wl[i]);
             }
         };
@@ -198,6 +197,7 @@ __global__ void __launch_bounds__(bwd_warps(C * 16 / sizeof(T), MODE, DROP) * 32
             inputs(c, dy, xhat, gw);
 #pragma unroll
             for (int i = 0; i < H; ++i) {
+                xhat[i] = mul2(add2(xhat[i], shift), scale);
                 c1v = add2(c1v, gw[i]);
                 c2v = fma2(gw[i], xhat[i], c2v);
                 dw[c][i] = fma2(dy[i], xhat[i], dw[c][i]);
@@ -228,30 +228,31 @@ __global__ void __launch_bounds__(bwd_warps(C * 16 / sizeof(T), MODE, DROP) * 32
         // (also keeps the compiler from carrying the first pass's values into the second, in more
         // registers than there are; where warps meet, their barrier does)
         if constexpr (!kCta) __syncwarp();
-        c1 *= -inv_n;
-        c2 *= -inv_n;
+        // dr = rstd (g - c1 - xhat c2) + dres = rstd g + r a + (b + dres) with the row's
+        // a = -rstd^2 c2, b = -rstd c1 - mean a: three operations a column after g
+        const float slope = -rstd * rstd * (c2 * inv_n), offset = __fmaf_rn(-mean, slope, -rstd * (c1 * inv_n));
         T* dx_row = p.dx + row * p.ld_dx;
         T* db_row = p.dbranch + row * p.ld_db;
-        const f32x2 c1n = pair_of(c1, c1), c2n = pair_of(c2, c2);
+        const f32x2 slope2 = pair_of(slope, slope), offset2 = pair_of(offset, offset);
         uint64_t row_m0 = 0;
         if constexpr (DROP) row_m0 = g.row(static_cast<uint32_t>(row));
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int valid = in && has(c) ? count(c) : 0;
-            f32x2 dy[H], xhat[H], d[H];
+            f32x2 dy[H], r[H], d[H], rest[H];
             Piece<T, V> out;
-            inputs(c, dy, xhat, d);
-#pragma unroll
-            for (int i = 0; i < H; ++i) d[i] = fma2(xhat[i], c2n, add2(d[i], c1n));
+            inputs(c, dy, r, d);
             if (p.dres) {
                 out.raw = read_piece<SHIFT>(at + (2 * C + c) * kSlots, mis_dres);
-                unpack2(out, xhat);
+                unpack2(out, rest);
 #pragma unroll
-                for (int i = 0; i < H; ++i) d[i] = fma2(d[i], scale, xhat[i]);
+                for (int i = 0; i < H; ++i) rest[i] = add2(rest[i], offset2);
             } else {
 #pragma unroll
-                for (int i = 0; i < H; ++i) d[i] = mul2(d[i], scale);
+                for (int i = 0; i < H; ++i) rest[i] = offset2;
             }
+#pragma unroll
+            for (int i = 0; i < H; ++i) d[i] = fma2(d[i], scale, fma2(r[i], slope2, rest[i]));
             pack2(out, d);
             if constexpr (SHIFT) put(out.raw, carry, dx_row, c, valid);
             else if (valid > 0) out.store(dx_row + t * V + c * 32 * V);
