@@ -636,9 +636,12 @@ int amax_history_update_ex(float* history, int L, int* head, const float* amax_n
  * are aligned to the element.  0 <= M <= FP8Q_NORM_MAX, 1 <= N <=
  * FP8Q_NORM_MAX.  An [M,N] output may be one of the [M,N] inputs (the same
  * pointer and row stride: each element is read before it is written); apart
- * from that the tensors must not overlap.  Rows whose pointers and row strides
- * (in bytes) are multiples of 16 are moved in 16-byte pieces, others element
- * by element.
+ * from that the tensors must not overlap.  Results do not depend on where the
+ * rows lie (dweight and dbias: below); rows whose pointers and row strides (in
+ * bytes) are multiples of 16, and whose N fills 16-byte pieces, move fastest.
+ * Of a row that does not start on a 16-byte boundary the calls read whole
+ * 16-byte granules that hold elements of it, and use those elements alone;
+ * they write the row's elements alone.
  *
  * Dropout masks are never stored.  rng points to 16 bytes of device memory:
  * a 64-bit seed and a 64-bit offset.  Element (i, j) is dropped when word
@@ -720,7 +723,8 @@ int layer_norm_fwd(const fp8q_layer_norm_args* args, cudaStream_t stream);
  *     dbranch = keep ? T(float32(dr * inv)) : 0     gradient of x
  *     dweight = sum_i dy * xhat,  dbias = sum_i dy  float32
  * dweight and dbias are summed in a fixed order (which depends on M, N, the
- * tensors' alignment and the device): the same call gives the same bits.
+ * types, dropout, the tensors' alignment and the device): the same call gives
+ * the same bits.
  *   dresidual      gradient that reaches r on its other way, or NULL.
  *   dbranch        NULL: not wanted.  With p = 0 it is T(dr).
  *   weight         NULL: 1.

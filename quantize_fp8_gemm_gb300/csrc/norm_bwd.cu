@@ -24,7 +24,7 @@ extern template cudaError_t launch_bwd_ring<float, true>(BwdParams<float>&, cuda
 
 namespace {
 
-// Any width: one CTA per row, two passes over it.
+// Wider than the one-pass kernels' 16384 columns: one CTA per row, two passes over it.
 template <typename T>
 __global__ void __launch_bounds__(256) ln_bwd_loop_kernel(const BwdParams<T> p) {
     __shared__ float s_sum[66];

@@ -11,7 +11,8 @@
 // reads that r, so its gradient is the gradient of what was computed, and the
 // fused call equals dropout_fwd followed by a plain layer_norm_fwd bit for bit.
 // Statistics are float32 sums of the deviations, not of squares, so a mean far
-// above the deviation costs no digits.
+// above the deviation costs no digits.  The kernels are in norm_fwd.cuh, the one for
+// any width here.
 #include "norm_fwd.cuh"
 
 #include <algorithm>
@@ -36,7 +37,7 @@ extern template cudaError_t launch_fwd_ring<float, true>(const FwdParams<float>&
 
 namespace {
 
-// Any width: one CTA per row, three passes over the row (the second and third
+// Wider than the one-pass kernels' 16384 columns: one CTA per row, three passes over the row (the second and third
 // from L1 / L2), each thread taking quads of columns (one generator block).
 // The row is formed again from its inputs in every pass and r_out is written
 // in the last, so r_out and y may replace an input.

@@ -45,19 +45,37 @@ namespace {
 // SHIFT: rows off the 16-byte grid (norm_ops.cuh).  A thread copies its own
 // granule, the last lane of a team one more; a lane reads its own and the next.
 // Without SHIFT a thread reads what it copied, and waits for its own copies only.
+//
+// What bounds it: memory from about 1000 columns and 10^4 rows on, as the ring
+// keeps 40 KB or more of loads in flight a multiprocessor whatever the registers
+// hold.  A warp a row costs the fewest instructions (statistics are ten shuffles a
+// row, weights stay in registers); a CTA a row pays a barrier.  Packed float32
+// pairs (f32x2) halve the arithmetic.  With dropout it is the issue slots: a piece
+// of eight columns takes about 250 instructions, 70 of them the generator's.
+// Measured on GB300 (share of the measured copy rate, 6785 GB/s): bf16 131072 x
+// 1600 148 us (0.84), with residual 273 us (0.91), with dropout, residual and
+// E4M3 codes 308 us (0.90); 32768 x 4096 83 us (0.95); 8192 x 16384 107 us (0.74);
+// 131072 x 128 15.7 us (0.64: two rows a warp, instruction-bound); off the grid
+// float32 65536 x 1001 95 us (0.81), bf16 16384 x 1001 20 us (0.48: cutting and
+// joining the granules is half the instructions).  The register-only form before
+// the ring (loads in registers, weights from L1) took 272 us at 131072 x 1600.
 enum FwdMode { NARROW, WIDE, BROAD };
 
 // With 40 columns a lane or more the generator's registers beside 128 of weights
-// would leave two warps a scheduler: the CTA's weights are then in shared memory,
-// as BROAD's are where one input's ring leaves room for them (otherwise they come
-// from L1 and L2 in every row, at twice the row's own bytes).
+// would leave two warps a scheduler: the CTA's weights are then in shared memory
+// (131072 x 1600 with dropout: 429 us with them from L1, 317 from shared memory;
+// at 24 columns registers are better, 65536 x 768 66 against 72 us), as BROAD's
+// are where one input's ring leaves room for them (8192 x 16384: 151 us with the
+// weights from L2, twice the row's own bytes in every row, 107 from shared memory).
 __host__ __device__ constexpr bool weights_held(int columns, bool drop, FwdMode mode) {
     return mode != BROAD && !(drop && columns >= 40);
 }
 __host__ __device__ constexpr bool weights_shared(int columns, bool drop, bool res, FwdMode mode) {
     return !weights_held(columns, drop, mode) && (mode == NARROW || (mode == BROAD && !res));
 }
-// Rows of the ring: what leaves room for three CTAs a multiprocessor, or fits at all.
+// Rows of the ring: what leaves room for three CTAs a multiprocessor (131072 x 1600
+// with dropout and residual: 308 us with two rows, 372 with three and two CTAs), or
+// fits at all.
 __host__ __device__ constexpr int ring_rows(int C, int columns, bool drop, bool res, FwdMode mode) {
     if (mode == BROAD) return C == 8 ? 1 : 2;
     return drop && res && columns >= 40 ? 2 : 3;
@@ -226,10 +244,10 @@ ln_fwd_ring_kernel(const FwdParams<T> p, int team) {
                     for (int i = 0; i < H; ++i) v[c][i] = add2(f[i], v[c][i]);
                 }
                 pack2(a, v[c]);
-                if (p.r_out) {
-                    if constexpr (SHIFT) put(a.raw, carry, r_row, c, in && has(c) ? count(c) : 0);
-                    else if (in && has(c)) a.store(r_row + t * V + c * 32 * V);
-                }
+            }
+            if (p.r_out) {
+                if constexpr (SHIFT) put(a.raw, carry, r_row, c, in && has(c) ? count(c) : 0);
+                else if (in && has(c)) a.store(r_row + t * V + c * 32 * V);
             }
             unpack2(a, v[c]);
             if constexpr (SHIFT) {

@@ -175,6 +175,25 @@ def test_fwd_codes_bit_exact(M, N, fmt):
     assert amax.item() == 1e9
 
 
+@pytest.mark.parametrize("T", [BF, HF, SF], ids=ids.get)
+@pytest.mark.parametrize("N", [5, 64, 200, 1000, 1600, 2048, 3000, 6400, 16384, 20000])
+def test_results_do_not_depend_on_where_rows_lie(N, T):
+    """Rows on and off the 16-byte grid give the same bits (the column sums may differ in order)."""
+    M = 21
+    w, b = params(N, SF, 1)
+    rng = rng_of(3, 4)
+    seen = []
+    for pad, shift in ((0, 0), (3, 0), (1, 5), (8, 16)):
+        x, res, dy, dres = (rows(M, N, T, s, pad=pad, shift=shift) for s in (1, 2, 3, 4))
+        r, y, dx, db = (out_like(M, N, T, pad=pad, shift=shift) for _ in range(4))
+        mean, rstd = torch.empty(M, device="cuda"), torch.empty(M, device="cuda")
+        B.layer_norm_fwd(x, w, b, y, mean=mean, rstd=rstd, residual=res, r_out=r, p=0.2, rng=rng)
+        run_bwd(dy, r, mean, rstd, w, dres=dres, p=0.2, rng=rng, dx=dx, db=db)
+        seen.append([t.clone() for t in (r, y, mean, rstd, dx, db)])
+    for other in seen[1:]:
+        assert all(torch.equal(a, c) for a, c in zip(seen[0], other))
+
+
 def test_fwd_amax_of_a_nan():
     x = rows(4, 64, BF, 1)
     x[2, 5] = float("nan")
@@ -261,6 +280,17 @@ def test_fused_forward_equals_the_separate_calls(M, N, pad, T):
         y3 = out_like(M, N, T)  # r not kept
         B.layer_norm_fwd(x, w, b, y3, residual=residual, p=p, rng=rng)
         assert_within(f64(y3), f64(y), 2 * R.fwd_tolerances(f64(r), f64(w), f64(b), 1e-5, T)[0], "y without r_out")
+
+
+@pytest.mark.parametrize("N", [64, 1600, 1001, 2056, 16384, 33000])
+@pytest.mark.parametrize("p", [0.0, 1e-11])
+def test_r_out_of_a_call_without_residual_or_dropout(N, p):
+    """r is x then, and r_out gets it; so also where p is too small to drop anything."""
+    x = rows(6, N, BF, 55)
+    r, y, y2 = (out_like(6, N, BF) for _ in range(3))
+    B.layer_norm_fwd(x, None, None, y, r_out=r, p=p)
+    B.layer_norm_fwd(x, None, None, y2)
+    assert torch.equal(r, x) and torch.equal(y, y2)
 
 
 @pytest.mark.parametrize("N", [64, 1600, 1001, 2056, 33000])
