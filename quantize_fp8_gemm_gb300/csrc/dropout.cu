@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(256, 4) dropout_rows_kernel(const DropParams<T
         __syncwarp();
         const uint4* at = ring + stage * kStage;
         Piece<T, V> x;
-        x.raw = read_piece<true>(at, granule_offset(x_at));
+        x.raw = read_piece<T, true>(at, granule_offset(x_at));
         f32x2 v[H];
         unpack2(x, v);
         if (p.drop.on) {
@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(256, 4) dropout_rows_kernel(const DropParams<T
         }
         if constexpr (RES) {
             Piece<T, V> r;
-            r.raw = read_piece<true>(at + kSlots, granule_offset(r_at));
+            r.raw = read_piece<T, true>(at + kSlots, granule_offset(r_at));
             f32x2 f[H];
             unpack2(r, f);
 #pragma unroll

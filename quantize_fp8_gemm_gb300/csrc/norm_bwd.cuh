@@ -176,23 +176,35 @@ __global__ void __launch_bounds__(bwd_warps(C * 16 / sizeof(T), MODE, DROP) * 32
         const float mean_next = ahead < p.M ? p.mean[ahead] : 0.0f, rstd_next = ahead < p.M ? p.rstd[ahead] : 0.0f;
         fill(stage == 0 ? S - 1 : stage - 1, row + (S - 1) * stride);
         cp_async_wait<S - 1>();
-        const uint4* at = ring + stage * kStage;
+        uint4* const at = ring + stage * kStage;
         if constexpr (SHIFT) __syncwarp();
         const uint32_t mis_dy = SHIFT ? granule_offset(p.dy + row * p.ld_dy) : 0;
         const uint32_t mis_r = SHIFT ? granule_offset(p.r + row * p.ld_r) : 0;
         const uint32_t mis_dres = SHIFT && p.dres ? granule_offset(p.dres + row * p.ld_dres) : 0;
         const f32x2 shift = pair_of(-mean, -mean), scale = pair_of(rstd, rstd);
-        // dy, r and g = dy * w of piece c
-        auto inputs = [&](int c, f32x2 (&dy)[H], f32x2 (&r)[H], f32x2 (&gw)[H]) {
-            Piece<T, V> a;
-            a.raw = read_piece<SHIFT>(at + c * kSlots, mis_dy);
-            unpack2(a, dy);
-            a.raw = read_piece<SHIFT>(at + (C + c) * kSlots, mis_r);
-            unpack2(a, r);
-            if (SHIFT && count(c) < V) {  // the row's end: what follows in the granule is not its own
-                zero_from<V>(dy, count(c));
-                zero_from<V>(r, count(c));
+        // dy, r and g = dy * w of piece c.  SHIFT: the first pass cuts the pieces from the granules,
+        // without what is not the row's, and leaves them where its own granules were for the second
+        auto inputs = [&](int c, bool first, f32x2 (&dy)[H], f32x2 (&r)[H], f32x2 (&gw)[H]) {
+            Piece<T, V> a, b;
+            uint4* const dy_slot = at + c * kSlots;
+            uint4* const r_slot = at + (C + c) * kSlots;
+            if (SHIFT && first) {
+                a.raw = read_piece<T, true>(dy_slot, mis_dy);
+                b.raw = read_piece<T, true>(r_slot, mis_r);
+                __syncwarp();  // every lane has read its neighbour's granule
+                const int valid = in ? count(c) : 0;
+                if (valid < V) {
+                    clear_from(a, valid);
+                    clear_from(b, valid);
+                }
+                *dy_slot = a.raw;
+                *r_slot = b.raw;
+            } else {
+                a.raw = *dy_slot;
+                b.raw = *r_slot;
             }
+            unpack2(a, dy);
+            unpack2(b, r);
             f32x2 wl[H];
             if constexpr (!kHeld) {
 #pragma unroll
@@ -207,9 +219,9 @@ __global__ void __launch_bounds__(bwd_warps(C * 16 / sizeof(T), MODE, DROP) * 32
         f32x2 c1v = zero2, c2v = zero2;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            if (C == 1 && !kCta && !in) continue;
+            if (!SHIFT && C == 1 && !kCta && !in) continue;
             f32x2 dy[H], xhat[H], gw[H];  // pieces past the row: dy = 0, which adds nothing
-            inputs(c, dy, xhat, gw);
+            inputs(c, true, dy, xhat, gw);
 #pragma unroll
             for (int i = 0; i < H; ++i) {
                 xhat[i] = mul2(add2(xhat[i], shift), scale);
@@ -256,9 +268,9 @@ __global__ void __launch_bounds__(bwd_warps(C * 16 / sizeof(T), MODE, DROP) * 32
             const int valid = in && has(c) ? count(c) : 0;
             f32x2 dy[H], r[H], d[H], rest[H];
             Piece<T, V> out;
-            inputs(c, dy, r, d);
+            inputs(c, false, dy, r, d);
             if (p.dres) {
-                out.raw = read_piece<SHIFT>(at + (2 * C + c) * kSlots, mis_dres);
+                out.raw = read_piece<T, SHIFT>(at + (2 * C + c) * kSlots, mis_dres);
                 unpack2(out, rest);
 #pragma unroll
                 for (int i = 0; i < H; ++i) rest[i] = add2(rest[i], offset2);

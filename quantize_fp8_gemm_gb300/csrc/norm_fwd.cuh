@@ -226,7 +226,7 @@ ln_fwd_ring_kernel(const FwdParams<T> p, int team) {
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             Piece<T, V> a;
-            a.raw = read_piece<SHIFT>(at + c * kSlots, mis_x);
+            a.raw = read_piece<T, SHIFT>(at + c * kSlots, mis_x);
             if constexpr (DROP || RES) {
                 unpack2(a, v[c]);
                 if constexpr (DROP) {
@@ -237,7 +237,7 @@ ln_fwd_ring_kernel(const FwdParams<T> p, int team) {
                 }
                 if constexpr (RES) {
                     Piece<T, V> r;
-                    r.raw = read_piece<SHIFT>(at + (C + c) * kSlots, mis_r);
+                    r.raw = read_piece<T, SHIFT>(at + (C + c) * kSlots, mis_r);
                     f32x2 f[H];
                     unpack2(r, f);
 #pragma unroll

@@ -166,7 +166,8 @@ __device__ __forceinline__ void load_params2(const Params<T>& w, int j, int n, f
 // rows lie.  A granule that holds an element of the row is read whole; its other
 // bytes are not used.  Writes touch the row's own elements only.
 
-// Bytes mis .. mis + 15 of a:b (0 <= mis < 16; whole elements of 2 or 4 bytes).
+// Bytes mis .. mis + 15 of a:b (0 <= mis < 16; whole elements of ES = 2 or 4 bytes).
+template <int ES>
 __device__ __forceinline__ uint4 cut16(uint4 a, uint4 b, uint32_t mis) {
     uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     if (mis & 8) {
@@ -177,6 +178,7 @@ __device__ __forceinline__ uint4 cut16(uint4 a, uint4 b, uint32_t mis) {
 #pragma unroll
         for (int i = 0; i < 5; ++i) u[i] = u[i + 1];
     }
+    if constexpr (ES == 4) return make_uint4(u[0], u[1], u[2], u[3]);
     const uint32_t bits = (mis & 3) * 8;
     return make_uint4(__funnelshift_r(u[0], u[1], bits), __funnelshift_r(u[1], u[2], bits),
                       __funnelshift_r(u[2], u[3], bits), __funnelshift_r(u[3], u[4], bits));
@@ -204,9 +206,9 @@ __device__ __forceinline__ void copy_granules(uint32_t slot, const uint8_t* firs
     }
 }
 // This lane's piece from the ring: its slot, or cut from its slot and the next.
-template <bool SHIFT>
+template <typename T, bool SHIFT>
 __device__ __forceinline__ uint4 read_piece(const uint4* slot, uint32_t mis) {
-    if constexpr (SHIFT) return cut16(slot[0], slot[1], mis);
+    if constexpr (SHIFT) return cut16<sizeof(T)>(slot[0], slot[1], mis);
     return slot[0];
 }
 // Zero the columns from `valid` on.
@@ -217,6 +219,16 @@ __device__ __forceinline__ void zero_from(f32x2 (&v)[V / 2], int valid) {
         const float2 f = split(v[i]);
         v[i] = pair_of(2 * i < valid ? f.x : 0.0f, 2 * i + 1 < valid ? f.y : 0.0f);
     }
+}
+
+// The same of a packed piece.
+template <typename T, int V>
+__device__ __forceinline__ void clear_from(Piece<T, V>& q, int valid) {
+    float f[V];
+    q.unpack(f);
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = i < valid ? f[i] : 0.0f;
+    q.pack(f);
 }
 
 // Elements lo .. hi - 1 of a piece, one by one, to dst + their index.
@@ -260,7 +272,7 @@ __device__ __forceinline__ void store_shifted(uint4 q, uint4& carry, T* start, i
     const int lead = (16 - static_cast<int>(mis)) / static_cast<int>(sizeof(T));  // of this piece in its first granule
     const bool whole = (!HEAD || !head || mis == 0) && (!TAIL || valid >= lead);
     if (whole) {
-        const uint4 cut = cut16(prev, q, 16 - mis);
+        const uint4 cut = cut16<sizeof(T)>(prev, q, 16 - mis);
         st_v4(reinterpret_cast<uint8_t*>(dst) - mis, mis ? cut : q);
     }
     if constexpr (HEAD || TAIL) {
