@@ -95,9 +95,18 @@ __global__ void __launch_bounds__(kReduceWarps * 32) ln_bwd_reduce_kernel(const 
     pdl_wait();
     float sum = 0.0f;
     if (j < 2 * N) {
-        const float* from = part + j;
-#pragma unroll 10
-        for (int k = warp; k < parts; k += kReduceWarps) sum += from[static_cast<int64_t>(k) * 2 * N];
+        // ten loads in flight: 160 parts a round (152 CTAs write one each)
+        constexpr int kAtOnce = 10;
+        for (int k0 = warp; k0 < parts; k0 += kAtOnce * kReduceWarps) {
+            float v[kAtOnce];
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+                const int k = k0 + u * kReduceWarps;
+                v[u] = k < parts ? part[static_cast<int64_t>(k) * 2 * N + j] : 0.0f;
+            }
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) sum += v[u];
+        }
     }
     s[warp][lane] = sum;
     __syncthreads();
