@@ -10,12 +10,15 @@
 // which it is full beside the other instructions.  Measured on GB300: bf16 131072 x
 // 1600 160 us (0.77 of the measured copy rate), with residual 205 us (0.90);
 // 65536 x 768 with residual 52 us (0.85); float32 65536 x 1600 129 us (0.96).  Off
-// the 16-byte grid 65536 x 1601 with residual 229 us (0.40).
+// the 16-byte grid the instructions of single elements come on top (116 for 128
+// elements, the integer pipe at 65 %): 65536 x 1601 with residual 167 us (0.55),
+// float32 65536 x 1001 with residual 122 us (0.95), without 103 us (0.75).
 #include "common.cuh"
 #include "norm_ops.cuh"
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 namespace fp8q {
 
@@ -120,148 +123,128 @@ cudaError_t launch_pieces(const DropParams<T>& p, cudaStream_t stream) {
     return launch_pdl(kern, grid, dim3(256), 0, stream, p, total, per_row, div);
 }
 
-// Rows off the 16-byte grid (norm_ops.cuh), or too many pieces for 31 bits.  A warp
-// takes `deep` runs of 32 adjacent pieces of a row (or, where a row has
-// fewer than 32, 32 / team rows), the same columns of every row that it comes to.
-// The next runs are in flight in a ring of kRing in shared memory (norm_fwd.cuh);
-// the generator is what bounds this kernel beside the memory, so no register holds
-// a load in flight.
-constexpr int kRing = 4;
+// Rows off the 16-byte grid, or too many pieces for 31 bits.  A warp takes 128 columns
+// (or, where rows have at most 64, 32 / team rows), the same of each row that it
+// comes to, U of them at a time, loads first.  A lane forms the block of one column
+// quad, but loads and stores single elements, 32 adjacent ones a warp: a tensor may
+// begin anywhere, and each access is of whole sectors but at its ends.  The mask goes
+// from the quads to the elements by four votes: bit q of vote i is element 4q + i.
+// (Pieces of eight elements, cut from aligned granules in shared memory and joined
+// into such, took 230 us at 65536 x 1601 with residual, 155 us at float32 65536 x
+// 1001, 7.2 us at fp16 4097 x 333; this takes 167, 103 and 3.6.)
+//
+// Rows at a time, where rows are wide: with residual 65536 x 1601 takes 203 us at 2 and
+// three CTAs a multiprocessor, 166 at 3, 162 to 167 at 4, 178 at 6.  Narrow ones hold
+// four addresses a tensor: what fits the registers (131072 x 63: 14 us at 2, 19 at 4).
+template <bool RES, bool NARROW>
+constexpr int kRows = NARROW ? (RES ? 1 : 2) : 4;
 
-template <typename T, bool RES>
-__global__ void __launch_bounds__(256, 4) dropout_rows_kernel(const DropParams<T> p, int team, int chunks, int deep) {
-    constexpr int V = 16 / sizeof(T), H = V / 2, kSlots = warp_slots(true, true), kStage = (RES ? 2 : 1) * kSlots;
-    extern __shared__ uint4 s_ring[];  // [warp][stage][x, residual][slot]
-    const int lane = threadIdx.x & 31, place = lane & (team - 1);
+template <typename T, bool RES, bool NARROW>
+__global__ void __launch_bounds__(256, 2) dropout_elems_kernel(const DropParams<T> p, int team, uint32_t spans) {
+    constexpr uint32_t U = kRows<RES, NARROW>;
+    const int lane = threadIdx.x & 31;
     const uint32_t warp = blockIdx.x * 8 + (threadIdx.x >> 5), warps = gridDim.x * 8;
-    const uint32_t parts = static_cast<uint32_t>((chunks + deep - 1) / deep);  // warps that a row takes
-    const uint32_t set = warp / parts, sets = warps / parts;
-    const int first = static_cast<int>(warp - set * parts) * deep, runs = min(deep, chunks - first);  // this one's runs of it
-    const uint32_t step = sets * (32 / team);  // rows that all warps take at a time
-    uint4* const ring = s_ring + (threadIdx.x >> 5) * (kRing * kStage) + lane + lane / team;
+    const uint32_t set = warp / spans, sets = warps / spans, span = warp - set * spans;
     pdl_wait();
     if (set >= sets) return;  // the warps that make no full set
-
-    const int64_t left = p.N - (static_cast<int64_t>(first) * 32 + place) * V;  // columns from this thread's first
+    const uint32_t per = NARROW ? 32 / team : 1;  // rows a warp at a time
+    const uint32_t M = static_cast<uint32_t>(p.M), step = sets * per;
+    const int64_t first = static_cast<int64_t>(span) * 128, columns = p.N - first;
+    uint32_t row = set * per;
+    bool in[4];
+    uint32_t sub[4];
+    int64_t xo[4], ro[4], yo[4];  // of an element from its warp's first; past the row's end the last one's
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+        const int q = 8 * s + (lane >> 2);  // the quad of element s
+        sub[s] = NARROW ? q / team : 0;
+        int c = NARROW ? 4 * (q & (team - 1)) + (lane & 3) : 32 * s + lane;
+        in[s] = c < columns;
+        if (!in[s]) c = static_cast<int>(columns) - 1;
+        xo[s] = sub[s] * p.ldx + c;
+        ro[s] = sub[s] * p.ld_res + c;
+        yo[s] = sub[s] * p.ldy + c;
+    }
+    const T* x = p.x + row * p.ldx + first;
+    const T* res = RES ? p.res + row * p.ld_res + first : nullptr;
+    T* y = p.y + row * p.ldy + first;
+    const int64_t x_step = step * p.ldx, r_step = step * p.ld_res, y_step = step * p.ldy;
+    const uint32_t own = NARROW ? lane / team : 0;  // the row of this lane's quad among the warp's
     Philox g;
-    uint64_t first_m0 = 0;
+    uint64_t quad_m0 = 0;
     if (p.drop.on) {
         g = Philox(p.drop.rng);
-        first_m0 = kPhiloxM0 * ((static_cast<uint32_t>(first) * 32 + place) * (V / 4));
+        quad_m0 = kPhiloxM0 * (span * 32 + (NARROW ? lane & (team - 1) : lane));
     }
-    const uint32_t M = static_cast<uint32_t>(p.M);
-    uint32_t base = set * (32 / team), row = base + lane / team;
-    const int64_t column = static_cast<int64_t>(first) * 32 * V;
-    const T *x_at = p.x + static_cast<int64_t>(row) * p.ldx + column, *r_at = p.res + static_cast<int64_t>(row) * p.ld_res + column;
-    T* y_at = p.y + static_cast<int64_t>(row) * p.ldy + column;
-    const int64_t x_step = step * p.ldx, r_step = step * p.ld_res, y_step = step * p.ldy;
-    const uint32_t ring_at = smem_u32(ring);
-
-    // what is put in flight next: run `run_in` of row `row_in`
-    const T *x_in = x_at, *r_in = r_at;
-    uint32_t row_in = row;
-    int run_in = 0;
-    auto fill_tensor = [&](uint32_t to, const T* start) {
-        const int64_t rest = left - static_cast<int64_t>(run_in) * 32 * V;
-        const uint32_t mis = granule_offset(start);
-        const int64_t bytes = (rest + place * V) * static_cast<int64_t>(sizeof(T)) + mis;  // from the run's first granule on
-        copy_granules<false>(to, reinterpret_cast<const uint8_t*>(start + run_in * 32 * V) - mis, place,
-                             static_cast<int>(bytes < 1024 ? bytes : 1024), place == team - 1);
+    // n: rows (of this warp, `step` apart) that the batch has, 1 .. U
+    auto batch = [&](auto full, uint32_t n) {
+        constexpr bool FULL = decltype(full)::value;
+        T v[U][4], f[U][4];
+#pragma unroll
+        for (uint32_t u = 0; u < U; ++u) {
+            const uint32_t at = FULL ? u : min(u, n - 1);
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                if (NARROW && sub[s] >= M - row - at * step)
+                    v[u][s] = f[u][s] = from_f32<T>(0.0f);
+                else {
+                    v[u][s] = x[at * x_step + xo[s]];
+                    if constexpr (RES) f[u][s] = res[at * r_step + ro[s]];
+                }
+            }
+        }
+#pragma unroll
+        for (uint32_t u = 0; u < U; ++u) {
+            if (!FULL && u == n) break;
+            uint32_t keep = ~0u;
+            if (p.drop.on) {
+                const uint4 w = g.block(quad_m0, g.row(row + u * step + own));
+                const uint32_t k0 = __ballot_sync(~0u, w.x > p.drop.last), k1 = __ballot_sync(~0u, w.y > p.drop.last),
+                               k2 = __ballot_sync(~0u, w.z > p.drop.last), k3 = __ballot_sync(~0u, w.w > p.drop.last);
+                const uint32_t even = lane & 2 ? k2 : k0, odd = lane & 2 ? k3 : k1;
+                keep = (lane & 1 ? odd : even) >> (lane >> 2);
+            }
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                float o = to_f32(v[u][s]) * p.drop.inv;
+                o = keep & (1u << (8 * s)) ? o : 0.0f;
+                if constexpr (RES) o = to_f32(f[u][s]) + o;
+                if (in[s] && (!NARROW || sub[s] < M - row - u * step)) y[u * y_step + yo[s]] = from_f32<T>(o);
+            }
+        }
+        row += U * step;
+        x += U * x_step;
+        if constexpr (RES) res += U * r_step;
+        y += U * y_step;
     };
-    auto fill = [&](int stage) {
-        if (row_in < M) {
-            fill_tensor(ring_at + stage * kStage * 16, x_in);
-            if constexpr (RES) fill_tensor(ring_at + (stage * kStage + kSlots) * 16, r_in);
-        }
-        cp_async_commit();
-        if (++run_in == runs) {
-            run_in = 0;
-            row_in += step;
-            x_in += x_step;
-            if constexpr (RES) r_in += r_step;
-        }
-    };
-#pragma unroll
-    for (int k = 0; k < kRing - 1; ++k) fill(k);
-    const f32x2 inv2 = pair_of(p.drop.inv, p.drop.inv);
-    uint4 carry = make_uint4(0, 0, 0, 0);
-    int stage = 0, run = 0;
-    uint64_t row_m0 = p.drop.on ? g.row(row) : 0, quad_m0 = first_m0;
-    while (base < M) {
-        fill(stage == 0 ? kRing - 1 : stage - 1);
-        cp_async_wait<kRing - 1>();
-        __syncwarp();
-        const uint4* at = ring + stage * kStage;
-        Piece<T, V> x;
-        x.raw = read_piece<T, true>(at, granule_offset(x_at));
-        f32x2 v[H];
-        unpack2(x, v);
-        if (p.drop.on) {
-            uint32_t w[V];
-            words_at<V>(g, quad_m0, row_m0, w);
-#pragma unroll
-            for (int i = 0; i < H; ++i) v[i] = dropped2(mul2(v[i], inv2), w[2 * i], w[2 * i + 1], p.drop);
-        }
-        if constexpr (RES) {
-            Piece<T, V> r;
-            r.raw = read_piece<T, true>(at + kSlots, granule_offset(r_at));
-            f32x2 f[H];
-            unpack2(r, f);
-#pragma unroll
-            for (int i = 0; i < H; ++i) v[i] = add2(f[i], v[i]);
-        }
-        pack2(x, v);
-        const int64_t rest = row < M ? left - static_cast<int64_t>(run) * 32 * V : 0;
-        const int valid = rest <= 0 ? 0 : rest < V ? static_cast<int>(rest) : V;
-        if (run > 0 && run < runs - 1)
-            store_shifted<T, false, false>(x.raw, carry, y_at, run * 32 + place, valid, false, false);
-        else
-            store_shifted<T, true, true>(x.raw, carry, y_at, run * 32 + place, valid, run == 0 && place == 0,
-                                         rest <= V || (run == runs - 1 && place == 31));
-        __syncwarp();  // the granules that a neighbour read may be overwritten now
-        stage = stage == kRing - 1 ? 0 : stage + 1;
-        quad_m0 += kPhiloxM0 * (32 * (V / 4));
-        if (++run == runs) {
-            run = 0;
-            base += step;
-            row += step;
-            x_at += x_step;
-            if constexpr (RES) r_at += r_step;
-            y_at += y_step;
-            quad_m0 = first_m0;
-            if (p.drop.on) row_m0 = g.row(row);
-        }
-    }
+    uint32_t n = row < M ? (M - row + step - 1) / step : 0;
+    for (; n >= U; n -= U) batch(std::true_type(), U);
+    if (n != 0) batch(std::false_type(), n);
     pdl_launch_dependents();
-    cp_async_wait<0>();
 }
 
-template <typename T, bool RES>
-cudaError_t launch_rows(const DropParams<T>& p, cudaStream_t stream) {
-    constexpr int V = 16 / sizeof(T);
+template <typename T, bool RES, bool NARROW>
+cudaError_t launch_elems(const DropParams<T>& p, int team, cudaStream_t stream) {
     static std::atomic<int> per_sm;  // CTAs that run at a time
-    const auto kern = dropout_rows_kernel<T, RES>;
-    const size_t smem = size_t(8) * kRing * (RES ? 2 : 1) * warp_slots(true, true) * 16;
+    const auto kern = dropout_elems_kernel<T, RES, NARROW>;
     int n = per_sm.load(std::memory_order_relaxed);
     if (n == 0) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxRing);
-        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, 256, smem);
+        const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, 256, 0);
         if (e != cudaSuccess) return e;
         n = std::max(n, 1);
         per_sm.store(n, std::memory_order_relaxed);
     }
-    const int64_t pieces = (p.N + V - 1) / V, chunks = (pieces + 31) / 32;
-    const int team = team_of(pieces);
-    const int64_t rows = (p.M + 32 / team - 1) / (32 / team);
-    // a warp's part of a row has ends that go element by element: up to 8 runs a part,
-    // where that leaves two rows a warp
-    int64_t deep = 1;
-    while (deep < 8 && deep < chunks && rows * ((chunks + 2 * deep - 1) / (2 * deep)) >= int64_t(n) * sm_count() * 16) deep *= 2;
-    const int64_t parts = (chunks + deep - 1) / deep;
-    const int64_t want = (rows * parts + 7) / 8, least = (parts + 7) / 8;  // least: one full set of a row's warps
+    const int64_t spans = (p.N + 127) / 128, rows = (p.M + 32 / team - 1) / (32 / team);
+    const int64_t want = (rows * spans + 7) / 8, least = (spans + 7) / 8;  // least: one full set of a row's warps
     const int64_t grid = std::max(least, std::min<int64_t>(want, int64_t(n) * sm_count()));
-    return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(256), smem, stream, p, team, static_cast<int>(chunks),
-                      static_cast<int>(deep));
+    return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(256), 0, stream, p, team,
+                      static_cast<uint32_t>(spans));
+}
+
+template <typename T, bool RES>
+cudaError_t launch_rows(const DropParams<T>& p, cudaStream_t stream) {
+    const int team = team_of((p.N + 3) / 4);
+    return team < 32 ? launch_elems<T, RES, true>(p, team, stream) : launch_elems<T, RES, false>(p, team, stream);
 }
 
 template <typename T>
