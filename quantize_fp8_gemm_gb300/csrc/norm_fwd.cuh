@@ -56,7 +56,7 @@ namespace {
 // 1600 148 us (0.84), with residual 273 us (0.91), with dropout, residual and
 // E4M3 codes 308 us (0.90); 32768 x 4096 83 us (0.95); 8192 x 16384 107 us (0.74);
 // 131072 x 128 15.7 us (0.64: two rows a warp, instruction-bound); off the grid
-// float32 65536 x 1001 95 us (0.81), bf16 16384 x 1001 20 us (0.48: cutting and
+// float32 65536 x 1001 93 us (0.83), bf16 16384 x 1001 21 us (0.46: cutting and
 // joining the granules is half the instructions).  The register-only form before
 // the ring (loads in registers, weights from L1) took 272 us at 131072 x 1600.
 enum FwdMode { NARROW, WIDE, BROAD };
