@@ -84,6 +84,7 @@ __global__ void __launch_bounds__(bwd_warps(C * 16 / sizeof(T), MODE, DROP) * 32
     extern __shared__ uint4 s_ring[];  // [warp][stage][dy, r, dresidual][c][slot]; at the end the groups' column sums
     __shared__ float2 s_sum[2][16];
     constexpr int V = 16 / sizeof(T), H = V / 2, S = bwd_ring_rows(C, C * V, MODE, DROP);
+    constexpr bool kKeepDev = SHIFT && sizeof(T) == 4;
     constexpr bool kHeld = MODE != BROAD, kCta = MODE != NARROW;  // weights in registers; otherwise from L1 in every row
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
     // NARROW: lanes a row, and each warp is a group; otherwise warps a row, and a group
@@ -182,9 +183,11 @@ __global__ void __launch_bounds__(bwd_warps(C * 16 / sizeof(T), MODE, DROP) * 32
         const uint32_t mis_r = SHIFT ? granule_offset(p.r + row * p.ld_r) : 0;
         const uint32_t mis_dres = SHIFT && p.dres ? granule_offset(p.dres + row * p.ld_dres) : 0;
         const f32x2 shift = pair_of(-mean, -mean), scale = pair_of(rstd, rstd);
-        // dy, r and g = dy * w of piece c.  SHIFT: the first pass cuts the pieces from the granules,
-        // without what is not the row's, and leaves them where its own granules were for the second
-        auto inputs = [&](int c, bool first, f32x2 (&dy)[H], f32x2 (&r)[H], f32x2 (&gw)[H]) {
+        // dy, the deviations r - mean, and g = dy * w (first pass) or g + less (second) of piece c.
+        // SHIFT: the first pass cuts the pieces from the granules, without what is not the row's, and
+        // leaves them (of float32 r the deviations: the second pass's own subtraction would cost 2999 x
+        // 1237 18.6 us against 17.1) where its own granules were for the second
+        auto inputs = [&](int c, bool first, f32x2 less, f32x2 (&dy)[H], f32x2 (&dev)[H], f32x2 (&gw)[H]) {
             Piece<T, V> a, b;
             uint4* const dy_slot = at + c * kSlots;
             uint4* const r_slot = at + (C + c) * kSlots;
@@ -197,6 +200,12 @@ __global__ void __launch_bounds__(bwd_warps(C * 16 / sizeof(T), MODE, DROP) * 32
                     clear_from(a, valid);
                     clear_from(b, valid);
                 }
+                if constexpr (kKeepDev) {
+                    unpack2(b, dev);
+#pragma unroll
+                    for (int i = 0; i < H; ++i) dev[i] = add2(dev[i], shift);
+                    pack2(b, dev);
+                }
                 *dy_slot = a.raw;
                 *r_slot = b.raw;
             } else {
@@ -204,7 +213,7 @@ __global__ void __launch_bounds__(bwd_warps(C * 16 / sizeof(T), MODE, DROP) * 32
                 b.raw = *r_slot;
             }
             unpack2(a, dy);
-            unpack2(b, r);
+            unpack2(b, dev);
             f32x2 wl[H];
             if constexpr (!kHeld) {
 #pragma unroll
@@ -213,7 +222,9 @@ __global__ void __launch_bounds__(bwd_warps(C * 16 / sizeof(T), MODE, DROP) * 32
             }
 #pragma unroll
             for (int i = 0; i < H; ++i) {
-                gw[i] = mul2(dy[i], kHeld ? w[kHeld ? c : 0][i] : wl[i]);
+                const f32x2 weight = kHeld ? w[kHeld ? c : 0][i] : wl[i];
+                if constexpr (!kKeepDev) dev[i] = add2(dev[i], shift);
+                gw[i] = first ? mul2(dy[i], weight) : fma2(dy[i], weight, less);
             }
         };
         f32x2 c1v = zero2, c2v = zero2;
@@ -221,10 +232,10 @@ __global__ void __launch_bounds__(bwd_warps(C * 16 / sizeof(T), MODE, DROP) * 32
         for (int c = 0; c < C; ++c) {
             if (!SHIFT && C == 1 && !kCta && !in) continue;
             f32x2 dy[H], xhat[H], gw[H];  // pieces past the row: dy = 0, which adds nothing
-            inputs(c, true, dy, xhat, gw);
+            inputs(c, true, zero2, dy, xhat, gw);
 #pragma unroll
             for (int i = 0; i < H; ++i) {
-                xhat[i] = mul2(add2(xhat[i], shift), scale);
+                xhat[i] = mul2(xhat[i], scale);
                 c1v = add2(c1v, gw[i]);
                 c2v = fma2(gw[i], xhat[i], c2v);
                 dw[c][i] = fma2(dy[i], xhat[i], dw[c][i]);
@@ -255,31 +266,30 @@ __global__ void __launch_bounds__(bwd_warps(C * 16 / sizeof(T), MODE, DROP) * 32
         // (also keeps the compiler from carrying the first pass's values into the second, in more
         // registers than there are; where warps meet, their barrier does)
         if constexpr (!kCta) __syncwarp();
-        // dr = rstd (g - c1 - xhat c2) + dres = rstd g + r a + (b + dres) with the row's
-        // a = -rstd^2 c2, b = -rstd c1 - mean a: three operations a column after g
-        const float slope = -rstd * rstd * (c2 * inv_n), offset = __fmaf_rn(-mean, slope, -rstd * (c1 * inv_n));
+        // dr = rstd ((g - c1) + (r - mean) (-rstd c2)) + dres: four operations a column from dy on.
+        // The deviation is formed before anything is multiplied by it, so a mean far above it costs no
+        // digits, and rstd, which may be finite where its square is not (eps = 0), is never squared.
+        const float slope = -rstd * (c2 * inv_n), less = -(c1 * inv_n);
         T* dx_row = p.dx + row * p.ld_dx;
         T* db_row = p.dbranch + row * p.ld_db;
-        const f32x2 slope2 = pair_of(slope, slope), offset2 = pair_of(offset, offset);
+        const f32x2 slope2 = pair_of(slope, slope), less2 = pair_of(less, less);
         uint64_t row_m0 = 0;
         if constexpr (DROP) row_m0 = g.row(static_cast<uint32_t>(row));
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int valid = in && has(c) ? count(c) : 0;
-            f32x2 dy[H], r[H], d[H], rest[H];
+            f32x2 dy[H], dev[H], d[H], rest[H];
             Piece<T, V> out;
-            inputs(c, false, dy, r, d);
+            inputs(c, false, less2, dy, dev, d);
             if (p.dres) {
                 out.raw = read_piece<T, SHIFT>(at + (2 * C + c) * kSlots, mis_dres);
                 unpack2(out, rest);
-#pragma unroll
-                for (int i = 0; i < H; ++i) rest[i] = add2(rest[i], offset2);
             } else {
 #pragma unroll
-                for (int i = 0; i < H; ++i) rest[i] = offset2;
+                for (int i = 0; i < H; ++i) rest[i] = zero2;
             }
 #pragma unroll
-            for (int i = 0; i < H; ++i) d[i] = fma2(d[i], scale, fma2(r[i], slope2, rest[i]));
+            for (int i = 0; i < H; ++i) d[i] = fma2(fma2(dev[i], slope2, d[i]), scale, rest[i]);
             pack2(out, d);
             if constexpr (SHIFT) put(out.raw, carry, dx_row, c, valid);
             else if (valid > 0) out.store(dx_row + t * V + c * 32 * V);
