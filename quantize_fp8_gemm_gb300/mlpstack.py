@@ -87,16 +87,16 @@ class Fp8MlpStack:
                 s.update()
 
     def forward(self, x: torch.Tensor, params, *, calibrate: bool = False) -> torch.Tensor:
-        """The stack's output [M, D] (a buffer of the stack).  ``calibrate``: take each tensor's scale from
-        its own values (a first step, whose histories are empty)."""
+        """The stack's output [M, D], a buffer of the stack that the next forward() writes; x may be that
+        buffer, and may change as soon as the call's work on the stream is done.  ``calibrate``: take each
+        tensor's scale from its own values (a first step, whose histories are empty)."""
         before = None
         for L, (weight, bias, W1, W2) in zip(self.layers, params):
             for W, s, q, q_t in ((W1, L.w1_s, L.w1_q, L.w1_q_t), (W2, L.w2_s, L.w2_q, L.w2_q_t)):
                 self._cast(s, lambda sc, am, sat, fl: B.fp8_quant_fused_ex(
                     W, B.ACT_IDENTITY, B.E4M3, sc, q_out=q, q_t_out=q_t, amax_out=am, sat_count=sat, flags=fl), calibrate)
-            if before is None:
-                L.r = x
-                into = dict(x=x)
+            if before is None:  # r = x, kept for backward in the same pass: the caller may change x
+                into = dict(x=x, r_out=L.r)
             else:  # the dropout and residual of the sub-layer below, in the same pass
                 into = dict(x=before.branch, residual=before.r, r_out=L.r, p=self.p, rng=before.rng)
             self._cast(L.n_s, lambda sc, am, sat, fl: B.layer_norm_fwd(
@@ -113,7 +113,8 @@ class Fp8MlpStack:
         return self.out
 
     def backward(self, dout: torch.Tensor, params, *, calibrate: bool = False):
-        """(dx, grads) of the last forward(): dx [M, D], and per sub-layer (dweight, dbias, dW1, dW2)."""
+        """(dx, grads) of the last forward(): dx [M, D], and per sub-layer (dweight, dbias, dW1, dW2); buffers
+        of the stack, which the next backward() writes."""
         last = self.layers[-1]
         B.dropout_bwd(dout, last.db, self.p, last.rng)
         dres, grads = dout, []
