@@ -77,6 +77,13 @@ class Fp8MlpStack:
         self.workspace = torch.empty(B.layer_norm_bwd_workspace_bytes(M, D), dtype=torch.uint8, device=device)
         self.gemm_status = torch.zeros(1, dtype=torch.int32, device=device)
 
+    def _checked(self, params) -> list:
+        """The sub-layers' parameters, one tuple each."""
+        params = list(params)
+        if len(params) != len(self.layers):
+            raise ValueError(f"{len(params)} tuples of parameters for {len(self.layers)} sub-layers")
+        return params
+
     def _cast(self, s: DelayedScale, cast, calibrate: bool) -> None:
         """cast(scale, amax, sat, flags); with calibrate first once for its amax alone, which seeds the scale."""
         for _ in range(2 if calibrate else 1):
@@ -90,6 +97,7 @@ class Fp8MlpStack:
         """The stack's output [M, D], a buffer of the stack that the next forward() writes; x may be that
         buffer, and may change as soon as the call's work on the stream is done.  ``calibrate``: take each
         tensor's scale from its own values (a first step, whose histories are empty)."""
+        params = self._checked(params)
         before = None
         for L, (weight, bias, W1, W2) in zip(self.layers, params):
             for W, s, q, q_t in ((W1, L.w1_s, L.w1_q, L.w1_q_t), (W2, L.w2_s, L.w2_q, L.w2_q_t)):
@@ -115,6 +123,7 @@ class Fp8MlpStack:
     def backward(self, dout: torch.Tensor, params, *, calibrate: bool = False):
         """(dx, grads) of the last forward(): dx [M, D], and per sub-layer (dweight, dbias, dW1, dW2); buffers
         of the stack, which the next backward() writes."""
+        params = self._checked(params)
         last = self.layers[-1]
         B.dropout_bwd(dout, last.db, self.p, last.rng)
         dres, grads = dout, []
