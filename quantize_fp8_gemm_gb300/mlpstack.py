@@ -78,10 +78,17 @@ class Fp8MlpStack:
         self.gemm_status = torch.zeros(1, dtype=torch.int32, device=device)
 
     def _checked(self, params) -> list:
-        """The sub-layers' parameters, one tuple each."""
+        """The sub-layers' parameters, one tuple each.  (The quantize takes a matrix as raw BF16 of any
+        shape that fits its outputs, and the layer norm checks its own vectors.)"""
         params = list(params)
         if len(params) != len(self.layers):
             raise ValueError(f"{len(params)} tuples of parameters for {len(self.layers)} sub-layers")
+        for _, _, W1, W2 in params:
+            for W, shape, name in ((W1, (self.D, self.K), "W1"), (W2, (self.K, self.D), "W2")):
+                if W.dtype != torch.bfloat16:
+                    raise TypeError(f"{name} must be torch.bfloat16, not {W.dtype}")
+                if W.shape != shape:
+                    raise ValueError(f"{name} is {list(W.shape)}, the stack needs {list(shape)}")
         return params
 
     def _cast(self, s: DelayedScale, cast, calibrate: bool) -> None:
