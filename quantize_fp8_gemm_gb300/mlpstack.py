@@ -16,7 +16,9 @@ and back again: dropout_bwd, the gradient's casts, fp8_gemm_dgrad_act, the weigh
 gradients, fp8_gemm_dgrad, and layer_norm_bwd, which adds the residual's gradient
 and forms the branch gradient of the sub-layer below.  No dropout mask is stored:
 each sub-layer has its own offset of the generator, and a backward pass forms the
-forward's masks again; ``advance()`` gives the next step new ones.
+forward's masks again; ``advance()`` gives the next step new ones.  Nothing of a step's
+state is on the host: a CUDA graph may hold any number of steps, and its replays may
+mix with eager ones.
 
 Like ``Fp8DownProj`` this module owns buffers and the order of the calls; the
 arithmetic is libfp8q's.
@@ -29,16 +31,56 @@ from . import binding as B
 from .downproj import DelayedScale
 
 
-class _Layer:
-    """Buffers and scales of one sub-layer of M tokens, width D, hidden width K."""
+class _Scale(DelayedScale):
+    """A DelayedScale whose state between two steps is always in slot 1.
 
-    def __init__(self, M: int, D: int, K: int, margin: float, history_len: int, seed: int, index: int, device):
+    DelayedScale alternates its slots by a switch on the host, which a CUDA graph would freeze.
+    Here begin() moves the state to slot 0, a step casts with slot 0, and update() writes slot 1:
+    so a captured step starts where the step before it, eager or replayed, ended."""
+
+    def __init__(self, fmt: int, margin: float, history_len: int, device, record: torch.Tensor):
+        super().__init__(fmt, margin, history_len, device)
+        self.record = record  # int64 [slot][(scale, amax), count]
+        words = record.view(torch.float32)
+        self.scales, self.amaxes, self.sats = words[:, 0], words[:, 1], record[:, 1]
+        self.scales.fill_(1.0)
+        self.slot = 1
+
+    def begun(self) -> None:
+        self.slot, self.clean = 0, True
+
+    def begin(self) -> None:
+        self.record[0].copy_(self.record[1])
+        self.begun()
+
+    def seed(self, amax: float) -> None:
+        self.begin()
+        super().seed(amax)
+
+
+class _Scales:
+    """The scales that one pass over the stack casts with, begun by one copy."""
+
+    def __init__(self, fmt: int, count: int, margin: float, history_len: int, device):
+        self.records = torch.zeros(count, 2, 2, dtype=torch.int64, device=device)
+        self.scales = [_Scale(fmt, margin, history_len, device, r) for r in self.records]
+
+    def begin(self) -> None:
+        self.records[:, 0].copy_(self.records[:, 1])
+        for s in self.scales:
+            s.begun()
+
+
+class _Layer:
+    """Buffers of one sub-layer of M tokens, width D, hidden width K, and its scales: of the norm's output, the
+    activation, W1 and W2 in the forward pass, of the branch's and the activation's gradient in the backward."""
+
+    def __init__(self, M: int, D: int, K: int, forward_scales, backward_scales, seed: int, index: int, device):
         bf = lambda *s: torch.empty(*s, dtype=torch.bfloat16, device=device)  # noqa: E731
         q8 = lambda *s: torch.empty(*s, dtype=torch.uint8, device=device)  # noqa: E731
         f32 = lambda *s: torch.empty(*s, dtype=torch.float32, device=device)  # noqa: E731
-        scale = lambda fmt: DelayedScale(fmt, margin, history_len, device)  # noqa: E731
-        self.n_s, self.h_s, self.w1_s, self.w2_s = (scale(B.E4M3) for _ in range(4))
-        self.db_s, self.dh_s = scale(B.E5M2), scale(B.E5M2)
+        self.n_s, self.h_s, self.w1_s, self.w2_s = forward_scales
+        self.db_s, self.dh_s = backward_scales
         # (seed, offset): sub-layers of one step differ in the offset's low half, steps in its high half
         self.rng = torch.tensor([seed, index], dtype=torch.int64, device=device)
         # forward
@@ -72,7 +114,10 @@ class Fp8MlpStack:
         if layers < 1 or M % 16 or D % 16 or K % 16:
             raise ValueError("layers >= 1, and M, D, K multiples of 16")
         self.M, self.D, self.K, self.p, self.eps, self.act = M, D, K, float(p), float(eps), act
-        self.layers = [_Layer(M, D, K, margin, history_len, seed, i, device) for i in range(layers)]
+        self.forward_scales = _Scales(B.E4M3, 4 * layers, margin, history_len, device)
+        self.backward_scales = _Scales(B.E5M2, 2 * layers, margin, history_len, device)
+        self.layers = [_Layer(M, D, K, self.forward_scales.scales[4 * i:4 * i + 4],
+                              self.backward_scales.scales[2 * i:2 * i + 2], seed, i, device) for i in range(layers)]
         self.out = torch.empty(M, D, dtype=torch.bfloat16, device=device)
         self.workspace = torch.empty(B.layer_norm_bwd_workspace_bytes(M, D), dtype=torch.uint8, device=device)
         self.gemm_status = torch.zeros(1, dtype=torch.int32, device=device)
@@ -99,12 +144,14 @@ class Fp8MlpStack:
             if calibrate:
                 calibrate = False
                 s.update()
+                s.begin()
 
     def forward(self, x: torch.Tensor, params, *, calibrate: bool = False) -> torch.Tensor:
         """The stack's output [M, D], a buffer of the stack that the next forward() writes; x may be that
         buffer, and may change as soon as the call's work on the stream is done.  ``calibrate``: take each
         tensor's scale from its own values (a first step, whose histories are empty)."""
         params = self._checked(params)
+        self.forward_scales.begin()
         before = None
         for L, (weight, bias, W1, W2) in zip(self.layers, params):
             for W, s, q, q_t in ((W1, L.w1_s, L.w1_q, L.w1_q_t), (W2, L.w2_s, L.w2_q, L.w2_q_t)):
@@ -131,6 +178,7 @@ class Fp8MlpStack:
         """(dx, grads) of the last forward(): dx [M, D], and per sub-layer (dweight, dbias, dW1, dW2); buffers
         of the stack, which the next backward() writes."""
         params = self._checked(params)
+        self.backward_scales.begin()
         last = self.layers[-1]
         B.dropout_bwd(dout, last.db, self.p, last.rng)
         dres, grads = dout, []
