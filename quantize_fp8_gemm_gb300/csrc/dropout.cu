@@ -17,7 +17,6 @@
 #include "norm_ops.cuh"
 
 #include <algorithm>
-#include <atomic>
 #include <type_traits>
 
 namespace fp8q {
@@ -225,15 +224,11 @@ __global__ void __launch_bounds__(256, 2) dropout_elems_kernel(const DropParams<
 
 template <typename T, bool RES, bool NARROW>
 cudaError_t launch_elems(const DropParams<T>& p, int team, cudaStream_t stream) {
-    static std::atomic<int> per_sm;  // CTAs that run at a time
+    static DeviceTable<17> table;  // CTAs that run at a time
     const auto kern = dropout_elems_kernel<T, RES, NARROW>;
-    int n = per_sm.load(std::memory_order_relaxed);
-    if (n == 0) {
-        const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, 256, 0);
-        if (e != cudaSuccess) return e;
-        n = std::max(n, 1);
-        per_sm.store(n, std::memory_order_relaxed);
-    }
+    int n = 0;
+    const cudaError_t e = resident_ctas(table, kern, 256, 0, 0, &n);
+    if (e != cudaSuccess) return e;
     const int64_t spans = (p.N + 127) / 128, rows = (p.M + 32 / team - 1) / (32 / team);
     const int64_t want = (rows * spans + 7) / 8, least = (spans + 7) / 8;  // least: one full set of a row's warps
     const int64_t grid = std::max(least, std::min<int64_t>(want, int64_t(n) * sm_count()));

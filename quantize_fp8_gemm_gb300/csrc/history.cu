@@ -16,14 +16,13 @@
 // can zero the accumulators the next step's cast folds into.
 #include "common.cuh"
 #include "history_ops.cuh"
+#include "launch_table.cuh"
 
 #include <mutex>
 
 namespace fp8q {
 
 namespace {
-
-constexpr int kMaxDevices = 64;
 
 __global__ void __launch_bounds__(32)
 amax_history_kernel(float* __restrict__ history, int L, int* __restrict__ head,

@@ -7,7 +7,6 @@
 #include "norm_ops.cuh"
 
 #include <algorithm>
-#include <atomic>
 
 namespace fp8q {
 
@@ -363,19 +362,13 @@ cudaError_t launch_ring_as(BwdParams<T>& p, int team, cudaStream_t stream) {
     const int64_t most = std::max(1, bwd_warps(C * V, MODE, DROP) / warps);
     const int64_t groups = all <= most ? all : std::min<int64_t>(most, (all + sm_count() - 1) / sm_count());
     const unsigned block = static_cast<unsigned>(groups) * warps * 32;
-    // one wave: as many CTAs as run at a time (the answer is kept by CTA size)
-    static std::atomic<int> per_sm[17];
+    // one wave: as many CTAs as run at a time (kept by device and CTA size)
+    static DeviceTable<17> table;
     const auto kern = ln_bwd_ring_kernel<T, C, MODE, DROP, SHIFT>;
     const size_t smem = size_t(bwd_ring_rows(C, C * V, MODE, DROP)) * 3 * C * (block / 32) * warp_slots(SHIFT, MODE == NARROW && C == 1) * 16;
-    std::atomic<int>& known = per_sm[block / 32];
-    int n = known.load(std::memory_order_relaxed);
-    if (n == 0) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxRing);
-        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, static_cast<int>(block), smem);
-        if (e != cudaSuccess) return e;
-        n = std::max(n, 1);
-        known.store(n, std::memory_order_relaxed);
-    }
+    int n = 0;
+    const cudaError_t e = resident_ctas(table, kern, block, smem, kMaxRing, &n);
+    if (e != cudaSuccess) return e;
     p.parts = static_cast<int>(std::min<int64_t>({p.parts, int64_t(n) * sm_count(), (all + groups - 1) / groups}));
     return launch_pdl(kern, dim3(p.parts), dim3(block), smem, stream, p, team);
 }

@@ -7,7 +7,6 @@
 #include "norm_ops.cuh"
 
 #include <algorithm>
-#include <atomic>
 
 namespace fp8q {
 
@@ -366,21 +365,15 @@ ln_fwd_ring_kernel(const FwdParams<T> p, int team) {
 template <typename T, int C, bool DROP, bool RES, FwdMode MODE, bool SHIFT>
 cudaError_t launch_ring_as(const FwdParams<T>& p, int team, unsigned block, cudaStream_t stream) {
     constexpr int V = 16 / sizeof(T);
-    // one wave: as many CTAs as run at a time (the answer is kept by CTA size)
-    static std::atomic<int> per_sm[17];
+    // one wave: as many CTAs as run at a time (kept by device and CTA size)
+    static DeviceTable<17> table;
     const auto kern = ln_fwd_ring_kernel<T, C, DROP, RES, MODE, SHIFT>;
     size_t smem = size_t(ring_rows(C, C * V, DROP, RES, MODE)) * (RES ? 2 : 1) * C * (block / 32) *
                         warp_slots(SHIFT, MODE == NARROW && C == 1) * 16;
     if (weights_shared(C * V, DROP, RES, MODE)) smem += size_t(2) * C * 32 * V * sizeof(float) * (MODE == NARROW ? 1 : block / 32);
-    std::atomic<int>& known = per_sm[block / 32];
-    int n = known.load(std::memory_order_relaxed);
-    if (n == 0) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxRing);
-        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, static_cast<int>(block), smem);
-        if (e != cudaSuccess) return e;
-        n = std::max(n, 1);
-        known.store(n, std::memory_order_relaxed);
-    }
+    int n = 0;
+    const cudaError_t e = resident_ctas(table, kern, block, smem, kMaxRing, &n);
+    if (e != cudaSuccess) return e;
     const int64_t rows = MODE == NARROW ? 128 / team : 1;
     const int64_t grid = std::min<int64_t>((p.M + rows - 1) / rows, int64_t(n) * sm_count());
     return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(block), smem, stream, p, team);

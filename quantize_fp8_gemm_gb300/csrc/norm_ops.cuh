@@ -4,8 +4,10 @@
 #pragma once
 
 #include "common.cuh"
+#include "launch_table.cuh"
 #include "quant_ops.cuh"
 
+#include <algorithm>
 #include <type_traits>
 
 namespace fp8q {
@@ -491,6 +493,22 @@ inline int team_of(int64_t pieces) {
 inline unsigned threads_of(int64_t pieces, int c) { return static_cast<unsigned>((pieces + 32 * c - 1) / (32 * c)) * 32; }
 constexpr int kMaxRing = 208 * 1024;  // dynamic shared memory that a ring may take
 inline bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// *n = CTAs of `kern`, of `block` threads with `smem` bytes, that run at a time on a
+// multiprocessor of the current device; on the first call there the kernel is
+// allowed `most` bytes.
+template <typename Kern>
+inline cudaError_t resident_ctas(DeviceTable<17>& table, Kern kern, unsigned block, size_t smem, int most, int* n) {
+    int device = 0;
+    const cudaError_t got = cudaGetDevice(&device);
+    if (got != cudaSuccess) return got;
+    return table.get(device, static_cast<int>(block / 32), n, [&](int* ctas) {
+        cudaError_t e = most ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most) : cudaSuccess;
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas, kern, static_cast<int>(block), smem);
+        *ctas = std::max(*ctas, 1);
+        return e;
+    });
+}
 
 // The rows that a thread comes to, `stride` apart.  RUN: the address is carried
 // from row to row (two registers more, and no 64-bit product a row: worth it
