@@ -49,7 +49,7 @@ template <typename T, int V>
 struct Piece {
     static_assert(V * sizeof(T) == 16, "16-byte pieces");
     uint4 raw;
-    __device__ __forceinline__ void load(const T* p) { raw = ld_stream_v4(p); }
+    __device__ __forceinline__ void load(const T* p) { raw = ld_once_v4(p); }  // an output may replace an input
     __device__ __forceinline__ void store(T* p) const { st_v4(p, raw); }
     __device__ __forceinline__ void zero() { raw = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ void unpack(float (&v)[V]) const {
