@@ -354,6 +354,8 @@ __global__ void __launch_bounds__(bwd_warps(C * 16 / sizeof(T), MODE, DROP) * 32
 template <typename T, int C, BwdMode MODE, bool DROP, bool SHIFT>
 cudaError_t launch_ring_as(BwdParams<T>& p, int team, cudaStream_t stream) {
     constexpr int V = 16 / sizeof(T);
+    // a row that fits WIDE's warps at these columns a lane goes there
+    static_assert(MODE != BROAD || bwd_warps(C * V, WIDE, DROP) < 16, "no call reaches this variant");
     // groups (rows, or warps of narrow rows) a CTA: as many as fit, fewer where that leaves multiprocessors
     // idle -- but one CTA for what it takes at a time, whose sums need no second kernel
     const int warps = MODE == NARROW ? 1 : team;
@@ -401,8 +403,9 @@ cudaError_t launch_bwd_ring(BwdParams<T>& p, cudaStream_t stream) {
         if (pieces <= 96 * warps) return launch_ring<T, 3, WIDE, SHIFT>(p, warps, stream);
         return launch_ring<T, 4, WIDE, SHIFT>(p, warps, stream);
     }
-    if (warps <= 16) return launch_ring<T, 4, BROAD, SHIFT>(p, warps, stream);
-    if constexpr (V == 4) {
+    if constexpr (V == 8) {
+        if (warps <= 16) return launch_ring<T, 4, BROAD, SHIFT>(p, warps, stream);
+    } else {  // (at four columns a piece WIDE takes 16 warps of four pieces; BROAD begins past it)
         if (pieces <= 16 * 256) return launch_ring<T, 8, BROAD, SHIFT>(p, static_cast<int>((pieces + 255) / 256), stream);
     }
     return cudaErrorNotSupported;
