@@ -639,8 +639,8 @@ int amax_history_update_ex(float* history, int L, int* head, const float* amax_n
  * from that the tensors must not overlap.  Results do not depend on where the
  * rows lie (dweight and dbias: below); rows whose pointers and row strides (in
  * bytes) are multiples of 16, and whose N fills 16-byte pieces, move fastest.
- * Of a row that does not start on a 16-byte boundary the calls read whole
- * 16-byte granules that hold elements of it, and use those elements alone;
+ * Of a row that does not start and end on 16-byte boundaries the calls read
+ * whole 16-byte granules that hold elements of it, and use those elements alone;
  * they write the row's elements alone.
  *
  * Dropout masks are never stored.  rng points to 16 bytes of device memory:
@@ -672,8 +672,11 @@ typedef enum { FP8Q_BF16 = 0, FP8Q_FP16 = 1, FP8Q_FP32 = 2 } fp8q_dtype;
  *     amax_out = max |y|;  sat_count = #{ |v| > format max }
  *
  * The norm is that of the stored r (rounded to T; r = x without residual and
- * dropout).  Sums are float32.  An infinity or NaN in a row gives NaNs in that
- * row alone (and a NaN amax, which the history update reports).
+ * dropout).  Sums are float32: a row whose squared deviations add up past its
+ * largest value (3.4e38) gets rstd = 0, and with eps = 0 one whose variance is
+ * below its normal range (1.2e-38) loses digits of rstd.  An infinity or NaN in
+ * a row gives NaNs in that row alone (and a NaN amax, which the history update
+ * reports).
  *   dtype, param_dtype  x, residual, r_out, y;  weight and bias: FP8Q_FP32 or
  *                       dtype, [N] each, NULL for 1 and 0.
  *   x                   required unless M == 0.

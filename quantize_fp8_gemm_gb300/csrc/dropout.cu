@@ -8,11 +8,12 @@
 // What bounds it: memory beside the generator's multiplications.  The 17 products
 // of a block (norm_ops.cuh) keep the multiply pipe at 60 to 70 % of its cycles, at
 // which it is full beside the other instructions.  Measured on GB300: bf16 131072 x
-// 1600 160 us (0.77 of the measured copy rate), with residual 205 us (0.90);
+// 1600 159 us (0.78 of the measured copy rate), with residual 205 us (0.90);
 // 65536 x 768 with residual 52 us (0.85); float32 65536 x 1600 129 us (0.96).  Off
-// the 16-byte grid the instructions of single elements come on top (116 for 128
-// elements, the integer pipe at 65 %): 65536 x 1601 with residual 167 us (0.55),
-// float32 65536 x 1001 with residual 122 us (0.95), without 103 us (0.75).
+// the 16-byte grid the instructions of single elements come on top (112 for 128
+// elements, 138 with residual; the integer pipe at 57 and 62 % of its cycles):
+// 65536 x 1601 with residual 167 us (0.55), float32 65536 x 1001 with residual 122 us
+// (0.95), without 103 us (0.75).
 #include "common.cuh"
 #include "norm_ops.cuh"
 
@@ -52,7 +53,7 @@ struct FastDiv {
 };
 
 // Pieces a thread: 131072 x 1600 bf16 without residual takes 193 us at 1, 169 at 2,
-// 160 at 4 (the generator's chains hide each other); float32 65536 x 1600 156, 131, 135.
+// 159 at 4 (the generator's chains hide each other); float32 65536 x 1600 156, 131, 135.
 template <typename T>
 constexpr int kUnroll = sizeof(T) == 2 ? 4 : 2;
 

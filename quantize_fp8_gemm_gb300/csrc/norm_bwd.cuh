@@ -53,19 +53,22 @@ namespace {
 // generator is beside those.
 //
 // What bounds it: memory, where rows are long and many: bf16 with residual 131072 x
-// 1600 240 us (1.03 of the measured copy rate: four fifths of the bytes are reads),
-// 32768 x 4096 125 us (0.95), 65536 x 768 64 us (0.93), float32 16384 x 4096 133 us
+// 1600 241 us (1.03 of the measured copy rate: four fifths of the bytes are reads),
+// 32768 x 4096 125 us (0.95), 65536 x 768 64 us (0.93), float32 16384 x 4096 134 us
 // (0.89).  The split: up to 32 columns a lane keep the row's fixed costs (two sums,
 // addresses) below a third of the instructions, and the column sums of them (64
 // registers) still leave 12 warps; with one piece a lane and seven warps a row
 // 131072 x 1600 took 420 us, with one warp and seven pieces 558.  With dropout it is
-// the issue slots: about 280 instructions a piece, 86 of them the generator's and the
-// selection's: 131072 x 1600 415 us (0.74); drawing the mask as bits before the row,
-// which would free registers for 12 warps, took 475.  Calls of a few thousand rows
-// are bound by the column sums' way out: 8192 x 768 takes 8 us without them and 12
-// with them (the sums through shared memory, a partial row a CTA, and a second
-// kernel).  BROAD is short of registers (its 128 hold 64 of sums): 8192 x 16384
-// 245 us (0.49).  Off the grid, 65536 x 1001 93 us (0.63).
+// latency: 131072 x 1600 414 us (0.75).  A piece takes about 260 instructions, a third
+// of them the generator's and the selection's, in 238 registers; so 8 warps are on a
+// multiprocessor, two a scheduler, each in its own chains of ten dependent rounds.
+// Nothing is full: they issue in 49 % of the cycles, the multiply pipe is busy in 55 %,
+// the memory gives 55 % of its peak.  Drawing the mask as bits before the row, by the
+// same warp, which frees registers for 12 warps, took 475.  Calls of a few thousand rows
+// are bound by the column sums' way out (through shared memory, a partial row a CTA, and
+// a second kernel): 8192 x 768 takes 14.5 us from memory; with its data in L2 11.6,
+// and 7.7 of them without the sums.  BROAD is short of registers (its 128 hold 64 of
+// sums): 8192 x 16384 245 us (0.49).  Off the grid, 65536 x 1001 95 us (0.61).
 enum BwdMode { NARROW, WIDE, BROAD };
 
 __host__ __device__ constexpr int bwd_warps(int columns, BwdMode mode, bool drop) {

@@ -10,8 +10,9 @@
 // The norm is that of the r which is stored, rounded to T: layer_norm_bwd
 // reads that r, so its gradient is the gradient of what was computed, and the
 // fused call equals dropout_fwd followed by a plain layer_norm_fwd bit for bit.
-// Statistics are float32 sums of the deviations, not of squares, so a mean far
-// above the deviation costs no digits.  The kernels are in norm_fwd.cuh, the one for
+// Statistics are float32 sums: the mean's, then the squared deviations' from it (not
+// of squares), so a mean far above the deviation costs the variance no digits beyond
+// the mean's own rounding.  The kernels are in norm_fwd.cuh, the one for
 // any width here.
 #include "norm_fwd.cuh"
 

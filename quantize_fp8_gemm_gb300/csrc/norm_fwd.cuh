@@ -49,14 +49,17 @@ namespace {
 // keeps 40 KB or more of loads in flight a multiprocessor whatever the registers
 // hold.  A warp a row costs the fewest instructions (statistics are ten shuffles a
 // row, weights stay in registers); a CTA a row pays a barrier.  Packed float32
-// pairs (f32x2) halve the arithmetic.  With dropout it is the issue slots: a piece
-// of eight columns takes about 250 instructions, 70 of them the generator's.
+// pairs (f32x2) halve the arithmetic.  With dropout it is memory and latency together:
+// a piece of eight columns takes about 235 instructions, 70 of them the generator's, in
+// 168 registers, and the 11 warps of a multiprocessor issue in 52 % of the cycles
+// (32768 x 1600 with codes: multiply pipe 53 %, memory 62 % of its peak).
 // Measured on GB300 (share of the measured copy rate, 6785 GB/s): bf16 131072 x
-// 1600 148 us (0.84), with residual 273 us (0.91), with dropout, residual and
-// E4M3 codes 308 us (0.90); 32768 x 4096 83 us (0.95); 8192 x 16384 107 us (0.74);
-// 131072 x 128 15.7 us (0.64: two rows a warp, instruction-bound); off the grid
-// float32 65536 x 1001 93 us (0.83), bf16 16384 x 1001 21 us (0.46: cutting and
-// joining the granules is half the instructions).  The register-only form before
+// 1600 148 us (0.83), with residual 273 us (0.91), with dropout, residual and
+// E4M3 codes 309 us (0.90); 32768 x 4096 84 us (0.95); 8192 x 16384 109 us (0.72);
+// 131072 x 128 16.6 us (0.60: two rows a warp, instruction-bound); off the grid
+// float32 65536 x 1001 92 us (0.84), bf16 16384 x 1001 21 us (0.46: cutting and
+// joining the granules makes 8 instructions an element 26, which 11 warps issue in
+// 46 % of the cycles, the memory at 18 % of its peak).  The register-only form before
 // the ring (loads in registers, weights from L1) took 272 us at 131072 x 1600.
 enum FwdMode { NARROW, WIDE, BROAD };
 
