@@ -1,6 +1,6 @@
-"""Layer norm and dropout over more rows than the persistent kernels take in one round, so that
-ring slots, double buffers, carried addresses and prefetched statistics are all used again, with
-a ragged last round; each also in place, on and off the 16-byte grid.
+"""Layer norm and dropout over many more rows than the persistent kernels hold at a time, so that
+ring slots, double buffers, carried addresses and prefetched statistics are all used again, and the
+last rows are too few for every CTA; each also in place, on and off the 16-byte grid.
 
 The reference is float64 (in torch, by blocks of rows).  r, masks and codes are exact.  The
 gradient's column sums are taken from small integers and powers of two, where float32 sums of any
@@ -78,7 +78,7 @@ def check_norm(y, mean, rstd, r, w, b, eps, T):
         within(rstd[s], rs, t_rstd, "rstd")
 
 
-# rows: past three rounds of as many CTAs as the threads of 152 multiprocessors allow, and a ragged last one
+# rows: more than three times what as many CTAs take at a time as the threads of 152 multiprocessors allow
 CASES = [(1000003, 7, BF), (250007, 63, BF), (250001, 64, SF), (30011, 768, BF), (30011, 1001, BF), (30011, 1001, SF),
          (20011, 1001, HF), (20011, 1600, BF), (15013, 1601, SF), (8009, 2056, BF), (6007, 4096, SF), (6007, 4099, BF),
          (3001, 4099, SF), (1531, 12345, BF), (1531, 16384, BF), (1021, 12347, SF), (2503, 20000, BF)]
