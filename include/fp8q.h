@@ -20,6 +20,8 @@
  *    layer_norm_bwd,         the norm with the up-projection's quantize in its
  *    dropout_fwd,            epilogue and the dropout + residual before it, and
  *    dropout_bwd             the gradients)
+ *   (fp8_glu_fwd,           the gated block (act(x Wg) * (x Wu)) W2: both projections,
+ *    fp8_gemm_dgrad_glu      the product and the quantize in one GEMM; its gradient)
  *
  * Conventions shared by every call:
  *  - All tensor pointers are DEVICE pointers to caller-owned memory; the
@@ -82,7 +84,8 @@ typedef enum {
 #define FP8Q_DEV_BAD_AMAX 2 /* history update kept the previous scale (amax 0/inf/NaN) */
 
 typedef enum { FP8Q_E4M3 = 0, FP8Q_E5M2 = 1 } fp8q_format;
-typedef enum { FP8Q_ACT_IDENTITY = 0, FP8Q_ACT_RELU = 1, FP8Q_ACT_RELU2 = 2 } fp8q_act;
+typedef enum { FP8Q_ACT_IDENTITY = 0, FP8Q_ACT_RELU = 1, FP8Q_ACT_RELU2 = 2,
+               FP8Q_ACT_SILU = 3, FP8Q_ACT_GELU = 4 /* of the gated calls alone */ } fp8q_act;
 
 /* Width of one scale group along the contraction dimension. */
 #define FP8Q_GROUP 128
@@ -774,6 +777,75 @@ int dropout_fwd(const void* x, int64_t ldx, const void* residual, int64_t ld_res
  * dropout_fwd's x (the residual's is dy itself). */
 int dropout_bwd(const void* dy, int64_t ld_dy, void* dx, int64_t ld_dx, int64_t M, int64_t N, int dtype, double p,
                 const uint64_t* rng, cudaStream_t stream);
+
+/*
+ * The gated feed-forward block  y = (act(x Wg) * (x Wu)) W2
+ *
+ * Both projections are one weight W1 [K,2F], the gate's F columns first, cast
+ * to E4M3 under one scale; its gradient and the input's are then those of a
+ * single linear layer (fp8_gemm_wgrad, fp8_gemm_dgrad on the [M,2F] gradient).
+ * act is an fp8q_act:  SiLU g / (1 + exp(-g));  GELU in its tanh form,
+ * g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2;  the others as above, with
+ * the derivative 0 of ReLU and ReLU^2 at 0.
+ */
+
+/*
+ * fp8_glu_fwd -- both projections, the activation, the product and its quantize
+ *
+ *     [g | u] = X . W1 / (s_x s_w)                   float32 sums, not rounded
+ *     h_out   = BF16([g | u])
+ *     a       = BF16(act(g) * u)                     -> act_out
+ *     v       = float32(a * s_a);  q = E4M3(v)       -> a_q, a_q_t
+ *     amax_out = max |a|;  sat_count = #{ |v| > 448 }
+ *
+ *   x_q      device [M,K] E4M3.
+ *   w1t_q    device [2F,K] E4M3: W1's transposed copy (q_t_out of fp8_quant_fused
+ *            run on W1): the gate's F rows, then the up-projection's.
+ *   scale_x, scale_w  device, 1 float each.
+ *   h_out    device [M,2F] BF16 or NULL (fp8_gemm_dgrad_glu needs it).
+ *   act_out  device [M,F] BF16 or NULL.
+ *   scale_a  device float: a's scale; required with a_q, a_q_t or sat_count.
+ *   a_q      device [M,F] E4M3 or NULL: the down-projection's operand.
+ *   a_q_t    device [F,M] E4M3 or NULL: its transpose, the weight gradient's
+ *            operand.  Needs M % 16 == 0.
+ *            At least one of act_out, a_q and a_q_t.
+ *   amax_out, sat_count  device float / uint64 or NULL; zeroed by the call unless
+ *            flags has FP8Q_ACCUMULATE.  A NaN among the a gives a NaN amax.
+ *   M, F, K  M >= 0 (0: only amax_out and sat_count are zeroed); F >= 16,
+ *            F % 16 == 0; K >= 16, K % 16 == 0.
+ *   status   as for fp8_gemm_fwd.
+ * Tensors are packed and 16-byte aligned, and must not overlap.
+ */
+int fp8_glu_fwd(const void* x_q, const void* w1t_q, const float* scale_x, const float* scale_w, int act,
+                void* h_out, void* act_out, const float* scale_a, void* a_q, void* a_q_t,
+                float* amax_out, unsigned long long* sat_count, int64_t M, int64_t F, int64_t K,
+                unsigned flags, int* status, cudaStream_t stream);
+
+/*
+ * fp8_gemm_dgrad_glu -- the gated block's gradient in the down-projection's dgrad
+ *
+ *     dA = dY . W2^T / (s_dy s_w)                    float32 sums, not rounded
+ *     dh = BF16([dA * u * act'(g) | dA * act(g)])    -> dh      (g, u: h's halves)
+ *     v  = float32(dh * s_dh);  q = E5M2(v)          -> dh_q, dh_q_t
+ *     amax_out = max |dh|;  sat_count = #{ |v| > 57344 }
+ *
+ *   dy_q     device [M,N] E5M2.
+ *   w2_q     device [F,N] E4M3: W2 in its own layout (q_out of fp8_quant_fused).
+ *   scale_dy, scale_w  device, 1 float each.
+ *   h        device [M,2F] BF16: h_out of fp8_glu_fwd.
+ *   dh       device [M,2F] BF16 or NULL; may be h itself.
+ *   scale_dh device float; required with dh_q, dh_q_t or sat_count.
+ *   dh_q     device [M,2F] E5M2 or NULL: fp8_gemm_dgrad's operand.
+ *   dh_q_t   device [2F,M] E5M2 or NULL: fp8_gemm_wgrad's.  Needs M % 16 == 0.
+ *            At least one of dh, dh_q and dh_q_t.
+ *   amax_out, sat_count, flags, status  as for fp8_glu_fwd.
+ *   M, N, F  M >= 0; N >= 16, N % 16 == 0 (the contraction); F as for fp8_glu_fwd.
+ * Apart from dh over h the tensors must not overlap; packed, 16-byte aligned.
+ */
+int fp8_gemm_dgrad_glu(const void* dy_q, const void* w2_q, const float* scale_dy, const float* scale_w,
+                       const void* h, int act, void* dh, const float* scale_dh, void* dh_q, void* dh_q_t,
+                       float* amax_out, unsigned long long* sat_count, int64_t M, int64_t N, int64_t F,
+                       unsigned flags, int* status, cudaStream_t stream);
 
 /* Human-readable name of an fp8q_status value (static string). */
 const char* fp8q_status_string(int status);

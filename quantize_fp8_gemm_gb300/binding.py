@@ -20,6 +20,7 @@ NAIVE_LIB_PATH = os.path.join(PKG, "libfp8q_naive.so")  # the unfused comparator
 
 E4M3, E5M2 = 0, 1
 ACT_IDENTITY, ACT_RELU, ACT_RELU2 = 0, 1, 2
+ACT_SILU, ACT_GELU = 3, 4  # of the gated calls alone
 DEV_TIMEOUT, DEV_BAD_AMAX = 1, 2
 ACCUMULATE = 1  # fp8_quant_fused_ex flag
 BATCH_MAX = 4  # FP8Q_BATCH_MAX
@@ -89,6 +90,8 @@ def lib() -> ctypes.CDLL:
         L.fp8_gemm_mx.argtypes = [P, P, P, P, P, i64, i64, i64, i32, i32, P, P]
         L.fp8_mx_scale_bytes.argtypes = [i64, i64]
         L.fp8_mx_scale_bytes.restype = i64
+        L.fp8_glu_fwd.argtypes = [P, P, P, P, i32, P, P, P, P, P, P, P, i64, i64, i64, ctypes.c_uint, P, P]
+        L.fp8_gemm_dgrad_glu.argtypes = [P, P, P, P, P, i32, P, P, P, P, P, P, i64, i64, i64, ctypes.c_uint, P, P]
         L.layer_norm_fwd.argtypes = [P, P]
         L.layer_norm_bwd.argtypes = [P, P]
         L.layer_norm_bwd_workspace_bytes.argtypes = [i64, i64]
@@ -98,7 +101,7 @@ def lib() -> ctypes.CDLL:
         for fn in ("fp8_quant_fused", "fp8_quant_fused_ex", "fp8_quant_fused_batch", "fp8_downproj_fwd",
                    "fp8_downproj_fwd_noalloc", "fp8_downproj_fwd_ex", "fp8_gemm_fwd", "fp8_gemm_fwd_update", "fp8_gemm_dgrad", "fp8_gemm_wgrad", "fp8_gemm_dgrad_act", "fp8_gemm_dgrad_act_q", "fp8_upproj_fwd", "amax_history_update",
                    "amax_history_update_ex", "fp8_quant_mx", "fp8_gemm_mx", "layer_norm_fwd", "layer_norm_bwd",
-                   "dropout_fwd", "dropout_bwd"):
+                   "dropout_fwd", "dropout_bwd", "fp8_glu_fwd", "fp8_gemm_dgrad_glu"):
             getattr(L, fn).restype = i32
         _lib = L
     return _lib
@@ -567,6 +570,25 @@ def _codes(t, n: int):
     return t.data_ptr()
 
 
+def _packed(t, rows: int, cols: int, dtype, name: str):
+    """Device pointer of an optional packed [rows, cols] CUDA tensor of a type (None: one-byte codes)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.element_size() != 1 if dtype is None else t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype or 'one-byte codes'}, not {t.dtype}")
+    if t.shape != (rows, cols) or not t.is_contiguous():
+        raise ValueError(f"{name} must be packed {[rows, cols]}, not {list(t.shape)} with strides {t.stride()}")
+    return t.data_ptr()
+
+
+def _here(t, name: str) -> None:
+    """The call runs on the current device: its tensors have to be there."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch._C._cuda_getDevice()}")
+
+
 def _param_code(x, weight, bias, code: int):
     """(param_dtype, its torch type) of the weight and bias: float32, or x's type."""
     t = weight if weight is not None else bias
@@ -644,6 +666,52 @@ def dropout_bwd(dy: torch.Tensor, dx: torch.Tensor, p: float, rng, *, stream=Non
 
 
 # -- the unfused three-pass comparator (include/fp8q_naive.h, libfp8q_naive.so) --
+# -- the gated feed-forward block --
+def fp8_glu_fwd(x_q: torch.Tensor, w1t_q: torch.Tensor, scale_x: torch.Tensor, scale_w: torch.Tensor, *,
+                act: int = ACT_SILU, h_out=None, act_out=None, scale_a=None, a_q=None, a_q_t=None, amax_out=None,
+                sat_count=None, flags: int = 0, status=None, stream=None) -> None:
+    """[g | u] = x_q[M,K] . w1t_q[2F,K]^T / (s_x s_w) and a = BF16(act(g) * u) in one GEMM; optionally
+    h_out[M,2F] = BF16([g | u]), act_out[M,F] = a, its E4M3 codes under scale_a (a_q[M,F], transposed
+    a_q_t[F,M]), max |a| and the saturations."""
+    if getattr(x_q, "ndim", 0) != 2 or getattr(w1t_q, "ndim", 0) != 2:
+        raise TypeError("x_q and w1t_q must be 2-dimensional CUDA tensors")
+    M, K = x_q.shape
+    rows = w1t_q.shape[0]
+    F = rows // 2
+    if rows != 2 * F:
+        raise ValueError(f"w1t_q has {rows} rows: the gate's and as many of the up-projection")
+    _here(x_q, "x_q")
+    bf, f32 = torch.bfloat16, torch.float32
+    st = lib().fp8_glu_fwd(
+        _packed(x_q, M, K, None, "x_q"), _packed(w1t_q, rows, K, None, "w1t_q"), _cell(scale_x, f32, "scale_x"),
+        _cell(scale_w, f32, "scale_w"), act, _packed(h_out, M, rows, bf, "h_out"), _packed(act_out, M, F, bf, "act_out"),
+        _cell(scale_a, f32, "scale_a"), _packed(a_q, M, F, None, "a_q"), _packed(a_q_t, F, M, None, "a_q_t"),
+        _cell(amax_out, f32, "amax_out"), _cell(sat_count, torch.int64, "sat_count"), M, F, K, flags,
+        _cell(status, torch.int32, "status"), _stream(stream))
+    _check("fp8_glu_fwd", st)
+
+
+def fp8_gemm_dgrad_glu(dy_q: torch.Tensor, w2_q: torch.Tensor, scale_dy: torch.Tensor, scale_w: torch.Tensor,
+                       h: torch.Tensor, *, act: int = ACT_SILU, dh=None, scale_dh=None, dh_q=None, dh_q_t=None,
+                       amax_out=None, sat_count=None, flags: int = 0, status=None, stream=None) -> None:
+    """dA = dy_q[M,N] . w2_q[F,N]^T / (s_dy s_w) and, from fp8_glu_fwd's h = [g | u] [M,2F], the gradient
+    dh = BF16([dA u act'(g) | dA act(g)]) in the GEMM's epilogue: dh[M,2F] (may be h), its E5M2 codes
+    under scale_dh (dh_q[M,2F], transposed dh_q_t[2F,M]), max |dh| and the saturations."""
+    if getattr(dy_q, "ndim", 0) != 2 or getattr(w2_q, "ndim", 0) != 2:
+        raise TypeError("dy_q and w2_q must be 2-dimensional CUDA tensors")
+    M, N = dy_q.shape
+    F = w2_q.shape[0]
+    _here(dy_q, "dy_q")
+    bf, f32 = torch.bfloat16, torch.float32
+    st = lib().fp8_gemm_dgrad_glu(
+        _packed(dy_q, M, N, None, "dy_q"), _packed(w2_q, F, N, None, "w2_q"), _cell(scale_dy, f32, "scale_dy"),
+        _cell(scale_w, f32, "scale_w"), _packed(h, M, 2 * F, bf, "h"), act, _packed(dh, M, 2 * F, bf, "dh"),
+        _cell(scale_dh, f32, "scale_dh"), _packed(dh_q, M, 2 * F, None, "dh_q"),
+        _packed(dh_q_t, 2 * F, M, None, "dh_q_t"), _cell(amax_out, f32, "amax_out"),
+        _cell(sat_count, torch.int64, "sat_count"), M, N, F, flags, _cell(status, torch.int32, "status"), _stream(stream))
+    _check("fp8_gemm_dgrad_glu", st)
+
+
 def fp8q_naive_act(h, act: int, act_out, *, stream=None) -> None:
     M, K = h.shape
     _check("fp8q_naive_act", naive_lib().fp8q_naive_act(
