@@ -22,6 +22,8 @@
  *    dropout_bwd             the gradients)
  *   (fp8_glu_fwd,           the gated block (act(x Wg) * (x Wu)) W2: both projections,
  *    fp8_gemm_dgrad_glu      the product and the quantize in one GEMM; its gradient)
+ *   (block_norm_fwd,        around it, r' = alpha r + gate norm(block(norm(r))): both
+ *    block_norm_bwd          norms, gate and residual in one pass; their gradient)
  *
  * Conventions shared by every call:
  *  - All tensor pointers are DEVICE pointers to caller-owned memory; the
@@ -846,6 +848,125 @@ int fp8_gemm_dgrad_glu(const void* dy_q, const void* w2_q, const float* scale_dy
                        const void* h, int act, void* dh, const float* scale_dh, void* dh_q, void* dh_q_t,
                        float* amax_out, unsigned long long* sat_count, int64_t M, int64_t N, int64_t F,
                        unsigned flags, int* status, cudaStream_t stream);
+
+/*
+ * Norms before and after a block
+ *
+ * A sub-layer of this form is  r' = alpha r + gate norm(block(norm(r))).  Norms are
+ * root-mean-square ones; element types, row strides, alignment, sizes and outputs
+ * over inputs are those of the layer norm calls.
+ */
+
+/*
+ * block_norm_fwd -- [norm after a block, weight, gate, scaled residual +] norm
+ * before the next block [+ FP8 cast]
+ *
+ *     xhat = post_norm ? x * rstd_post : x,  rstd_post[i] = 1 / sqrt(sum_j x^2 / N + eps)
+ *     r    = T(alpha * residual + gate[i] * (xhat * post_weight))       -> r_out
+ *     rstd[i] = 1 / sqrt(sum_j r^2 / N + eps)
+ *     y    = T(r * rstd * weight)                                       -> y
+ *     v    = float32(y * *scale);  q = FP8(v)                           -> q_out
+ *     amax_out = max |y|;  sat_count = #{ |v| > format max }
+ *
+ * The norm before the next block is that of the stored r (rounded to T).  Without
+ * residual, gate, post_weight and post_norm r is x itself: the norm before the
+ * first block; without y, q_out, rstd, amax_out and sat_count only r is formed:
+ * the end of the last.  Sums are float32: a row whose squares add up past its
+ * largest value (3.4e38) gets a statistic of 0; with eps = 0 a row of zeros gives
+ * NaNs.  An infinity or NaN stays in its row (and makes amax a NaN or infinite).
+ *   dtype, param_dtype   x, residual, r_out, y; weight and post_weight: FP8Q_FP32 or
+ *                        dtype, [N] each, NULL for 1.
+ *   x                    required unless M == 0.  One of r_out, y and q_out is too.
+ *   residual, alpha      NULL: none; alpha device float, NULL for 1 (without a
+ *                        residual it is not used).
+ *   gate                 device [M] float, NULL for 1.
+ *   rstd, rstd_post      device [M] float or NULL (rstd_post only with post_norm).
+ *   q_out, fmt, scale, amax_out, sat_count, flags, eps   as for layer_norm_fwd.
+ * Zero the struct and set what the call needs.
+ */
+typedef struct {
+    int64_t M, N;
+    int dtype, param_dtype;
+    const void* x;        int64_t ldx;
+    const void* residual; int64_t ld_residual;
+    void* r_out;          int64_t ld_r;
+    void* y;              int64_t ldy;
+    const void* weight;
+    const void* post_weight;
+    const float* gate;
+    const float* alpha;
+    float* rstd;
+    float* rstd_post;
+    const float* scale;
+    void* q_out;
+    float* amax_out;
+    unsigned long long* sat_count;
+    float eps;
+    int fmt;
+    int post_norm;
+    unsigned flags;
+} fp8q_block_norm_args;
+
+int block_norm_fwd(const fp8q_block_norm_args* args, cudaStream_t stream);
+
+/*
+ * block_norm_bwd -- gradient of block_norm_fwd
+ *
+ * With rhat = r * rstd, g = dy * weight, xhat as above, all in float32:
+ *     dr'       = dr + rstd * (g - rhat * sum_j (g * rhat) / N)
+ *     dresidual = T(alpha * dr')
+ *     e_i       = sum_j dr' * post_weight * xhat
+ *     dx        = T(gate[i] * (post_norm ? rstd_post * (dr' * post_weight - xhat * e_i / N)
+ *                                        : dr' * post_weight))
+ *     dgate     = e_i,  dalpha = sum_ij dr' * residual
+ *     dweight   = sum_i dy * rhat,  dpost_weight = sum_i gate[i] * dr' * xhat
+ * dalpha, dweight and dpost_weight are summed in a fixed order (which depends on M,
+ * N, the types, the tensors' alignment and the device).
+ *   dy, r, rstd     the gradient of y, and what the forward call kept.  dy NULL: the
+ *                   call had no norm before a next block (r, rstd, weight are not read).
+ *   dr              gradient that reaches r on its other way, or NULL (not both).
+ *   x, rstd_post, gate, post_weight, post_norm   as in the forward call; x and (with
+ *                   post_norm) rstd_post are required with dx, dpost_weight or dgate.
+ *   residual        required with dalpha alone.
+ *   dresidual, dx   device [M,N], or NULL: not wanted.
+ *   dgate [M], dweight [N], dpost_weight [N], dalpha [1]   device float, or NULL.
+ *   flags           FP8Q_ACCUMULATE adds to dweight, dpost_weight and dalpha.  M == 0
+ *                   without it zeroes them.
+ *   workspace       device, 16-byte aligned, block_norm_bwd_workspace_bytes(M, N) bytes;
+ *                   its contents need no preparation.  Required with dweight,
+ *                   dpost_weight or dalpha (unless M == 0).
+ */
+typedef struct {
+    int64_t M, N;
+    int dtype, param_dtype;
+    const void* dy;       int64_t ld_dy;
+    const void* r;        int64_t ld_r;
+    const void* dr;       int64_t ld_dr;
+    const void* x;        int64_t ldx;
+    const void* residual; int64_t ld_residual;
+    void* dresidual;      int64_t ld_dresidual;
+    void* dx;             int64_t ld_dx;
+    const void* weight;
+    const void* post_weight;
+    const float* gate;
+    const float* alpha;
+    const float* rstd;
+    const float* rstd_post;
+    float* dweight;
+    float* dpost_weight;
+    float* dgate;
+    float* dalpha;
+    void* workspace;
+    size_t workspace_bytes;
+    int post_norm;
+    unsigned flags;
+} fp8q_block_norm_bwd_args;
+
+int block_norm_bwd(const fp8q_block_norm_bwd_args* args, cudaStream_t stream);
+
+/* Bytes of block_norm_bwd's workspace: at most 1024 partial rows of 2 N + 1 floats.
+ * 0 for sizes that the call refuses and for M == 0. */
+size_t block_norm_bwd_workspace_bytes(int64_t M, int64_t N);
 
 /* Human-readable name of an fp8q_status value (static string). */
 const char* fp8q_status_string(int status);

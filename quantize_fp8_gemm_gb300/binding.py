@@ -92,6 +92,10 @@ def lib() -> ctypes.CDLL:
         L.fp8_mx_scale_bytes.restype = i64
         L.fp8_glu_fwd.argtypes = [P, P, P, P, i32, P, P, P, P, P, P, P, i64, i64, i64, ctypes.c_uint, P, P]
         L.fp8_gemm_dgrad_glu.argtypes = [P, P, P, P, P, i32, P, P, P, P, P, P, i64, i64, i64, ctypes.c_uint, P, P]
+        L.block_norm_fwd.argtypes = [P, P]
+        L.block_norm_bwd.argtypes = [P, P]
+        L.block_norm_bwd_workspace_bytes.argtypes = [i64, i64]
+        L.block_norm_bwd_workspace_bytes.restype = ctypes.c_size_t
         L.layer_norm_fwd.argtypes = [P, P]
         L.layer_norm_bwd.argtypes = [P, P]
         L.layer_norm_bwd_workspace_bytes.argtypes = [i64, i64]
@@ -101,7 +105,7 @@ def lib() -> ctypes.CDLL:
         for fn in ("fp8_quant_fused", "fp8_quant_fused_ex", "fp8_quant_fused_batch", "fp8_downproj_fwd",
                    "fp8_downproj_fwd_noalloc", "fp8_downproj_fwd_ex", "fp8_gemm_fwd", "fp8_gemm_fwd_update", "fp8_gemm_dgrad", "fp8_gemm_wgrad", "fp8_gemm_dgrad_act", "fp8_gemm_dgrad_act_q", "fp8_upproj_fwd", "amax_history_update",
                    "amax_history_update_ex", "fp8_quant_mx", "fp8_gemm_mx", "layer_norm_fwd", "layer_norm_bwd",
-                   "dropout_fwd", "dropout_bwd", "fp8_glu_fwd", "fp8_gemm_dgrad_glu"):
+                   "dropout_fwd", "dropout_bwd", "fp8_glu_fwd", "fp8_gemm_dgrad_glu", "block_norm_fwd", "block_norm_bwd"):
             getattr(L, fn).restype = i32
         _lib = L
     return _lib
@@ -666,6 +670,93 @@ def dropout_bwd(dy: torch.Tensor, dx: torch.Tensor, p: float, rng, *, stream=Non
 
 
 # -- the unfused three-pass comparator (include/fp8q_naive.h, libfp8q_naive.so) --
+# -- norms before and after a block --
+class BlockNormArgs(ctypes.Structure):
+    """fp8q_block_norm_args."""
+    _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int64), ("dtype", ctypes.c_int), ("param_dtype", ctypes.c_int),
+                ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("residual", ctypes.c_void_p),
+                ("ld_residual", ctypes.c_int64), ("r_out", ctypes.c_void_p), ("ld_r", ctypes.c_int64),
+                ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64), ("weight", ctypes.c_void_p),
+                ("post_weight", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("alpha", ctypes.c_void_p),
+                ("rstd", ctypes.c_void_p), ("rstd_post", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("q_out", ctypes.c_void_p), ("amax_out", ctypes.c_void_p), ("sat_count", ctypes.c_void_p),
+                ("eps", ctypes.c_float), ("fmt", ctypes.c_int), ("post_norm", ctypes.c_int), ("flags", ctypes.c_uint)]
+
+
+class BlockNormBwdArgs(ctypes.Structure):
+    """fp8q_block_norm_bwd_args."""
+    _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int64), ("dtype", ctypes.c_int), ("param_dtype", ctypes.c_int),
+                ("dy", ctypes.c_void_p), ("ld_dy", ctypes.c_int64), ("r", ctypes.c_void_p), ("ld_r", ctypes.c_int64),
+                ("dr", ctypes.c_void_p), ("ld_dr", ctypes.c_int64), ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64),
+                ("residual", ctypes.c_void_p), ("ld_residual", ctypes.c_int64), ("dresidual", ctypes.c_void_p),
+                ("ld_dresidual", ctypes.c_int64), ("dx", ctypes.c_void_p), ("ld_dx", ctypes.c_int64),
+                ("weight", ctypes.c_void_p), ("post_weight", ctypes.c_void_p), ("gate", ctypes.c_void_p),
+                ("alpha", ctypes.c_void_p), ("rstd", ctypes.c_void_p), ("rstd_post", ctypes.c_void_p),
+                ("dweight", ctypes.c_void_p), ("dpost_weight", ctypes.c_void_p), ("dgate", ctypes.c_void_p),
+                ("dalpha", ctypes.c_void_p), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+                ("post_norm", ctypes.c_int), ("flags", ctypes.c_uint)]
+
+
+def block_norm_fwd(x: torch.Tensor, weight, y, *, eps: float = 1e-5, rstd=None, residual=None, alpha=None, gate=None,
+                   post_weight=None, post_norm: bool = False, rstd_post=None, r_out=None, fmt: int = E4M3, scale=None,
+                   q_out=None, amax_out=None, sat_count=None, flags: int = 0, stream=None) -> None:
+    """r = alpha * residual + gate * (xhat * post_weight), xhat the rows of x, normed to root mean square 1
+    with post_norm; y = the rows of r normed, times weight; optionally r_out, the float32 statistics [M], and
+    the FP8 codes q_out [M,N] of y under `scale` with amax_out and sat_count.  x, residual, r_out, y: [M,N]
+    bfloat16, float16 or float32 with any row stride; weight, post_weight: [N] float32 or x's type, or None;
+    gate [M] and alpha [1]: float32, or None.  y None without codes: r_out alone."""
+    code, dtype = _dtype_code(x, "x"), x.dtype
+    M, N = x.shape
+    _here(x, "x")
+    px, ldx = _rows(x, M, N, dtype, "x")
+    pres, ldres = _rows(residual, M, N, dtype, "residual")
+    pr, ldr = _rows(r_out, M, N, dtype, "r_out")
+    py, ldy = _rows(y, M, N, dtype, "y")
+    pcode, ptype = _param_code(x, weight, post_weight, code)
+    f32 = torch.float32
+    a = BlockNormArgs(
+        M, N, code, pcode, px, ldx, pres, ldres, pr, ldr, py, ldy, _vec(weight, N, ptype, "weight"),
+        _vec(post_weight, N, ptype, "post_weight"), _vec(gate, M, f32, "gate"), _cell(alpha, f32, "alpha"),
+        _vec(rstd, M, f32, "rstd"), _vec(rstd_post, M, f32, "rstd_post"), _cell(scale, f32, "scale"),
+        _codes(q_out, M * N), _cell(amax_out, f32, "amax_out"), _cell(sat_count, torch.int64, "sat_count"), eps, fmt,
+        bool(post_norm), flags)
+    _check("block_norm_fwd", lib().block_norm_fwd(ctypes.byref(a), _stream(stream)))
+
+
+def block_norm_bwd_workspace_bytes(M: int, N: int) -> int:
+    return int(lib().block_norm_bwd_workspace_bytes(int(M), int(N)))
+
+
+def block_norm_bwd(dy, r, rstd, weight, *, dr=None, x=None, residual=None, alpha=None, gate=None, post_weight=None,
+                   post_norm: bool = False, rstd_post=None, dresidual=None, dx=None, dweight=None, dpost_weight=None,
+                   dgate=None, dalpha=None, workspace=None, flags: int = 0, stream=None) -> None:
+    """Gradient of block_norm_fwd from dy (None: no norm before a next block), the stored r and rstd, and dr,
+    r's gradient on its other way: dresidual, dx (the block's output's), and the float32 dgate [M], dweight,
+    dpost_weight [N] and dalpha [1], the last three through a workspace of
+    block_norm_bwd_workspace_bytes(M, N) bytes."""
+    first, name = (dy, "dy") if dy is not None else (dr, "dr")
+    code, dtype = _dtype_code(first, name), first.dtype
+    M, N = first.shape
+    _here(first, name)
+    pdy, lddy = _rows(dy, M, N, dtype, "dy")
+    pr, ldr = _rows(r, M, N, dtype, "r")
+    pdr, lddr = _rows(dr, M, N, dtype, "dr")
+    px, ldx = _rows(x, M, N, dtype, "x")
+    pres, ldres = _rows(residual, M, N, dtype, "residual")
+    pdres, lddres = _rows(dresidual, M, N, dtype, "dresidual")
+    pdx, lddx = _rows(dx, M, N, dtype, "dx")
+    pcode, ptype = _param_code(first, weight, post_weight, code)
+    f32 = torch.float32
+    a = BlockNormBwdArgs(
+        M, N, code, pcode, pdy, lddy, pr, ldr, pdr, lddr, px, ldx, pres, ldres, pdres, lddres, pdx, lddx,
+        _vec(weight, N, ptype, "weight"), _vec(post_weight, N, ptype, "post_weight"), _vec(gate, M, f32, "gate"),
+        _cell(alpha, f32, "alpha"), _vec(rstd, M, f32, "rstd"), _vec(rstd_post, M, f32, "rstd_post"),
+        _vec(dweight, N, f32, "dweight"), _vec(dpost_weight, N, f32, "dpost_weight"), _vec(dgate, M, f32, "dgate"),
+        _cell(dalpha, f32, "dalpha"), _ptr(workspace, None, "workspace"),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), bool(post_norm), flags)
+    _check("block_norm_bwd", lib().block_norm_bwd(ctypes.byref(a), _stream(stream)))
+
+
 # -- the gated feed-forward block --
 def fp8_glu_fwd(x_q: torch.Tensor, w1t_q: torch.Tensor, scale_x: torch.Tensor, scale_w: torch.Tensor, *,
                 act: int = ACT_SILU, h_out=None, act_out=None, scale_a=None, a_q=None, a_q_t=None, amax_out=None,

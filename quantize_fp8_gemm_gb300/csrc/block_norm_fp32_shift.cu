@@ -1,0 +1,6 @@
+// block_norm_fp32_shift.cu -- the one-pass kernels of block_norm_fwd and block_norm_bwd for fp32, rows off the 16-byte grid.
+#include "block_norm.cuh"
+
+template cudaError_t fp8q::launch_bn_fwd<float, true>(const BnFwd<float>&, cudaStream_t);
+template cudaError_t fp8q::launch_bn_bwd<float, false, true>(const BnBwd<float>&, int, int*, cudaStream_t);
+template cudaError_t fp8q::launch_bn_bwd<float, true, true>(const BnBwd<float>&, int, int*, cudaStream_t);
