@@ -5,7 +5,7 @@ import itertools
 import pytest
 import torch
 
-import block_norm_reference as R
+from tests import block_norm_reference as R
 
 pytestmark = pytest.mark.gpu
 

@@ -5,7 +5,7 @@ values (codes, their transposes, maximum, saturations) exactly against the BF16 
 import pytest
 import torch
 
-import glu_reference as R
+from tests import glu_reference as R
 
 pytestmark = pytest.mark.gpu
 
