@@ -84,30 +84,43 @@ struct GluCfg {
 };
 
 // The codes of one chunk (32 columns of this lane's row, packed BF16) into `codes` (32 x 32
-// bytes, lane r's row at 32 r) and, transposed, into `turned` (column j at 32 j): a byte
-// store a code, whose 32 lanes fill 32 adjacent bytes.
+// bytes, lane r's row at 32 r) and, transposed, into `turned` (column j at 32 j).  Four lanes
+// turn 4 x 4 bytes by two exchanges: first neighbouring lanes swap odd for even bytes, then
+// pairs of lanes high for low halves; lane 4 k + i then holds rows 4 k .. 4 k + 3 of column
+// 4 w + i, and a warp's stores of a word fill all banks.  (A byte store a code and the shifts
+// before it, 56 instructions for 32 codes against 40.)
 template <int FMT>
 __device__ __forceinline__ void glu_codes(const uint32_t (&v)[16], float s, uint8_t* codes, uint8_t* turned, int lane,
                                           bool want_codes, bool want_turned, uint32_t& amax2, uint32_t& nsat) {
-    uint32_t q[8];
+    uint32_t q[8], all = 0;
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
         const uint4 p = make_uint4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
-        const uint32_t m2 = __vmaxu2(__vmaxu2(p.x & 0x7FFF7FFFu, p.y & 0x7FFF7FFFu),
-                                     __vmaxu2(p.z & 0x7FFF7FFFu, p.w & 0x7FFF7FFFu));
-        amax2 = __vmaxu2(amax2, m2);
-        if (may_saturate<FMT>(m2, s)) nsat += sat_count8<FMT>(p, s);
+        all = __vmaxu2(all, __vmaxu2(__vmaxu2(p.x & 0x7FFF7FFFu, p.y & 0x7FFF7FFFu),
+                                     __vmaxu2(p.z & 0x7FFF7FFFu, p.w & 0x7FFF7FFFu)));
         const uint2 c = cast8_codes<FMT>(p, s);
         q[2 * g] = c.x;
         q[2 * g + 1] = c.y;
+    }
+    amax2 = __vmaxu2(amax2, all);
+    if (!(__fmul_rn(__uint_as_float(max16x2(all) << 16), s) <= fp8_max_value(FMT))) {  // (a NaN counts the others too)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+            nsat += sat_count8<FMT>(make_uint4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]), s);
     }
     if (want_codes) {
         *reinterpret_cast<uint4*>(codes + lane * 32) = make_uint4(q[0], q[1], q[2], q[3]);
         *reinterpret_cast<uint4*>(codes + lane * 32 + 16) = make_uint4(q[4], q[5], q[6], q[7]);
     }
     if (want_turned) {
+        const uint32_t sel1 = lane & 1 ? 0x3715u : 0x6240u, sel2 = lane & 2 ? 0x3276u : 0x5410u;
+        uint8_t* to = turned + (lane & 3) * 32 + (lane >> 2) * 4;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) turned[j * 32 + lane] = static_cast<uint8_t>(q[j / 4] >> (8 * (j & 3)));
+        for (int w = 0; w < 8; ++w) {
+            uint32_t x = __byte_perm(q[w], __shfl_xor_sync(0xFFFFFFFFu, q[w], 1), sel1);
+            x = __byte_perm(x, __shfl_xor_sync(0xFFFFFFFFu, x, 2), sel2);
+            *reinterpret_cast<uint32_t*>(to + w * 128) = x;
+        }
     }
 }
 
@@ -126,17 +139,23 @@ __device__ __forceinline__ void put_box(uint8_t* box, int lane, const uint32_t (
             make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
 }
 
+__device__ __forceinline__ f32x2 acc_pair(uint32_t a, uint32_t b) { return pair_of(__uint_as_float(a), __uint_as_float(b)); }
+
 template <int ACT>
 __device__ __forceinline__ void glu_products(const uint32_t (&g)[32], const uint32_t (&u)[32], float inv,
                                              uint32_t (&a)[16]) {
+    const f32x2 inv2 = twice(inv);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-        float v[2];
+    for (int j = 0; j < 16; ++j)
+        a[j] = bf16x2_of(mul2(glu_act<ACT>(mul2(acc_pair(g[2 * j], g[2 * j + 1]), inv2)),
+                              mul2(acc_pair(u[2 * j], u[2 * j + 1]), inv2)));
+}
+
+// The accumulator's 32 columns of this lane's row as packed BF16.
+__device__ __forceinline__ void glu_stored(const uint32_t (&r)[32], float inv, uint32_t (&h)[16]) {
+    const f32x2 inv2 = twice(inv);
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            v[i] = glu_act<ACT>(__uint_as_float(g[2 * j + i]) * inv) * (__uint_as_float(u[2 * j + i]) * inv);
-        a[j] = cvt_bf16x2(v[0], v[1]);
-    }
+    for (int j = 0; j < 16; ++j) h[j] = bf16x2_of(mul2(acc_pair(r[2 * j], r[2 * j + 1]), inv2));
 }
 
 // dA of this lane's row (32 columns), its g and u from the boxes -> packed BF16 dg and du.
@@ -144,6 +163,7 @@ template <int ACT>
 __device__ __forceinline__ void glu_gradients(const uint32_t (&r)[32], float inv, const uint8_t* gbox,
                                               const uint8_t* ubox, int lane, uint32_t (&dg)[16], uint32_t (&du)[16]) {
     const int sw = (lane >> 1) & 3;
+    const f32x2 inv2 = twice(inv);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         const int at = lane * 64 + ((k ^ sw) << 4);
@@ -151,10 +171,11 @@ __device__ __forceinline__ void glu_gradients(const uint32_t (&r)[32], float inv
         const uint32_t gw[4] = {g4.x, g4.y, g4.z, g4.w}, uw[4] = {u4.x, u4.y, u4.z, u4.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const float d0 = __uint_as_float(r[8 * k + 2 * j]) * inv, d1 = __uint_as_float(r[8 * k + 2 * j + 1]) * inv;
-            const float2 f0 = glu_act_grad<ACT>(bf16lo_to_f32(gw[j])), f1 = glu_act_grad<ACT>(bf16hi_to_f32(gw[j]));
-            dg[4 * k + j] = cvt_bf16x2(d0 * bf16lo_to_f32(uw[j]) * f0.y, d1 * bf16hi_to_f32(uw[j]) * f1.y);
-            du[4 * k + j] = cvt_bf16x2(d0 * f0.x, d1 * f1.x);
+            const f32x2 d = mul2(acc_pair(r[8 * k + 2 * j], r[8 * k + 2 * j + 1]), inv2);
+            f32x2 f, slope;
+            glu_act_grad<ACT>(f32x2_of(gw[j]), f, slope);
+            dg[4 * k + j] = bf16x2_of(mul2(mul2(d, f32x2_of(uw[j])), slope));
+            du[4 * k + j] = bf16x2_of(mul2(d, f));
         }
     }
 }
@@ -363,13 +384,9 @@ glu_kernel(const __grid_constant__ GluMaps maps, const GluArgs p) {
                     }
                     if (p.has_o) {
                         uint32_t hv[16];
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            hv[j] = cvt_bf16x2(__uint_as_float(g[2 * j]) * inv, __uint_as_float(g[2 * j + 1]) * inv);
+                        glu_stored(g, inv, hv);
                         put_box(buf, lane, hv);
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            hv[j] = cvt_bf16x2(__uint_as_float(u[2 * j]) * inv, __uint_as_float(u[2 * j + 1]) * inv);
+                        glu_stored(u, inv, hv);
                         put_box(buf + 2 * kBox, lane, hv);
                     }
                     if (p.has_d) put_box(buf + 4 * kBox, lane, a);
