@@ -6,10 +6,10 @@
 //   backward  dA = dY W2^T (E5M2 x E4M3, FP32 sums); dg = dA u act'(g), du = dA act(g)
 //
 // Both are the tcgen05 GEMM D[M, .] = A[M,K] . B[., K]^T of gemm_parts.cuh's pieces with
-// an epilogue of their own.  A CTA is 10 warps, persistent over output tiles:
+// an epilogue of their own.  A CTA is 10 warps (backward 18), persistent over output tiles:
 //   warp 0     TMA producer: k-blocks of 128 bytes a row into a ring of stages
 //   warp 1     MMA issuer: kind::f8f6f4 into one of two TMEM accumulators
-//   warps 2-9  epilogue: two warps a TMEM lane quarter, alternate 32-column chunks
+//   the others epilogue: two (backward four) warps a TMEM lane quarter, 32-column chunks in turn
 // PAIR: a cluster of two CTAs, 256 rows a tile, cta_group::2.
 //
 // The forward tile of BN accumulator columns is BN / 2 columns of the gate and the same
@@ -18,9 +18,12 @@
 // its half of B: the MMA reads B's first half from the leader's shared memory (the gate's
 // rows of W1^T) and its second from the peer's (the up-projection's).
 //
-// The backward tile is BN columns of dA; the chunks of g and u that it needs come by TMA
-// into two buffers a warp, asked for one chunk ahead (the first before the accumulator is
-// ready), and the gradients are written over them.
+// The epilogue is a thread a row, 32 columns (a chunk) at a time, and stores without shared
+// memory: 32 bytes of a thread's own row, a whole sector each, and the transposed codes after
+// exchanges between lanes.  No fence or copy engine stands between the accumulator and memory,
+// and the operands' ring has the shared memory that staging would take.  The backward's chunks
+// of g and u come by TMA into a buffer a warp, the next one asked for as soon as this one is in
+// registers (32-byte loads straight into registers, 32 sectors an instruction, took 680 us).
 //
 // Every wait is bounded as in gemm.cu: on time-out the CTA sets FP8Q_DEV_TIMEOUT, lets its
 // copies and MMAs land (bounded), frees TMEM and exits.
@@ -36,18 +39,24 @@ namespace fp8q {
 
 namespace {
 
-constexpr int kGluWarps = 8;                      // epilogue warps
-constexpr int kGluThreads = 64 + 32 * kGluWarps;
-constexpr int kBox = 32 * 32;                     // elements of a box: 32 rows x 32 columns
+constexpr int kBoxBytes = 32 * 32 * 2;  // 32 rows x 32 BF16 columns, in the 64-byte swizzle
 
-// Tensor maps of a call; one that a call has no tensor for is a copy of `a`, never used.
-// h (read), o (h_out or dh), q, t: the halves (gate, up) of a [M,2F] or [2F,M] tensor, each
-// a tensor of its own width, so that a box at a half's ragged end is clipped there.
+// Operands; h0 / h1 (backward): the halves of h, each a tensor of its own width, so that a box
+// at a half's ragged end is clipped there.
 struct GluMaps {
-    CUtensorMap a, b, h0, h1, o0, o1, d, q0, q1, t0, t1;
+    CUtensorMap a, b, h0, h1;
 };
 
+// The tensors of a call.  Forward: x [M,K], w [2F,K], o = h_out [M,2F], d = act_out [M,F], q [M,F], t [F,M].
+// Backward: x = dY [M,K], w = W2 [F,K], h [M,2F], o = dh [M,2F], q [M,2F], t [2F,M].
 struct GluArgs {
+    const void* x;
+    const void* w;
+    const uint16_t* h;
+    uint16_t* o;
+    uint16_t* d;
+    uint8_t* q;
+    uint8_t* t;
     const float* scale_a;
     const float* scale_b;
     const float* scale_q;
@@ -57,7 +66,7 @@ struct GluArgs {
     int64_t M, F, K;
     uint32_t idesc;
     int act;
-    bool has_o, has_d, has_q, has_t;  // h_out or dh; act_out; codes; transposed codes
+    bool wide_bf, wide_q;  // every 16 columns of h, o and d (32 of q) of a row are one 32-byte sector
 };
 
 template <int BN, bool PAIR, bool BWD>
@@ -69,132 +78,171 @@ struct GluCfg {
     static constexpr int STAGE_BYTES = A_BYTES + B_ROWS * BK;
     static constexpr int TX_BYTES = STAGE_BYTES * (PAIR ? 2 : 1);
     static constexpr int ACCS = 2;
-    // forward: g, u and a (BF16 boxes), codes and their transpose; backward: two buffers of
-    // g and u, and both halves' codes and transposes
-    static constexpr int WARP_BYTES = BWD ? 2 * 4 * kBox + 4 * kBox : 6 * kBox + 2 * kBox;
+    // epilogue warps: the backward's instructions, twice the forward's, want all that 96 registers a
+    // thread allow (32768 x 1600 -> 6400: 385 us with 16, 400 with 12, 453 with 8; forward 476, 483, 483)
+    static constexpr int WARPS = BWD ? 16 : 8;
+    static constexpr int THREADS = 64 + 32 * WARPS;
+    static constexpr int LOADS = BWD ? 1 : 0;           // backward: a warp's buffers for a chunk of g and u
+    static constexpr int LOAD_BYTES = WARPS * LOADS * 2 * kBoxBytes;
     static constexpr int BAR_BYTES = 512;
-    static constexpr int RING = 232448 - 512 - BAR_BYTES - 1024 - kGluWarps * WARP_BYTES;
+    static constexpr int RING = 232448 - 512 - BAR_BYTES - 1024 - LOAD_BYTES;
     static constexpr int STAGES = RING / STAGE_BYTES < 8 ? RING / STAGE_BYTES : 8;
-    static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + kGluWarps * WARP_BYTES + BAR_BYTES + 1024;
+    static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + LOAD_BYTES + BAR_BYTES + 1024;
     static constexpr int TMEM_COLS = 2 * BN <= 64 ? 64 : 2 * BN <= 128 ? 128 : 2 * BN <= 256 ? 256 : 512;
     static constexpr int TILE_M = PAIR ? 2 * BM : BM;
     static constexpr int CHUNKS = OUT / 32;
     static_assert(OUT % 32 == 0 && BN <= 256 && STAGES >= 2 && (B_ROWS * BK) % 1024 == 0, "tile shape");
-    static_assert((2 * STAGES + 2 * ACCS + 1 + 2 * kGluWarps) * 8 + 16 <= BAR_BYTES, "barrier area");
+    static_assert((2 * STAGES + 2 * ACCS + 1 + LOADS * WARPS) * 8 + 16 <= BAR_BYTES, "barrier area");
 };
 
-// The codes of one chunk (32 columns of this lane's row, packed BF16) into `codes` (32 x 32
-// bytes, lane r's row at 32 r) and, transposed, into `turned` (column j at 32 j).  Four lanes
-// turn 4 x 4 bytes by two exchanges: first neighbouring lanes swap odd for even bytes, then
-// pairs of lanes high for low halves; lane 4 k + i then holds rows 4 k .. 4 k + 3 of column
-// 4 w + i, and a warp's stores of a word fill all banks.  (A byte store a code and the shifts
-// before it, 56 instructions for 32 codes against 40.)
+// 32 bytes of a thread's row: one access where the row's sectors allow it, else two of 16.
+__device__ __forceinline__ void st_32(void* to, const uint32_t (&v)[8], bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                     :: "l"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]) : "memory");
+    } else {
+        st_v4(to, make_uint4(v[0], v[1], v[2], v[3]));
+        st_v4(static_cast<uint8_t*>(to) + 16, make_uint4(v[4], v[5], v[6], v[7]));
+    }
+}
+// The larger magnitudes of two pairs of BF16 values; a NaN stays one.
+__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("{\n\t.reg .b32 t;\n\tabs.bf16x2 t, %2;\n\tmax.NaN.bf16x2 %0, %1, t;\n\t}" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// 16 columns of this lane's row (packed BF16): their codes in four words, the magnitudes and
+// saturations counted.
 template <int FMT>
-__device__ __forceinline__ void glu_codes(const uint32_t (&v)[16], float s, uint8_t* codes, uint8_t* turned, int lane,
-                                          bool want_codes, bool want_turned, uint32_t& amax2, uint32_t& nsat) {
-    uint32_t q[8], all = 0;
+__device__ __forceinline__ void glu_codes(const uint32_t (&v)[8], float s, uint32_t* q, uint32_t& amax2, uint32_t& nsat) {
+    uint32_t all = 0;
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-        const uint4 p = make_uint4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
-        all = __vmaxu2(all, __vmaxu2(__vmaxu2(p.x & 0x7FFF7FFFu, p.y & 0x7FFF7FFFu),
-                                     __vmaxu2(p.z & 0x7FFF7FFFu, p.w & 0x7FFF7FFFu)));
-        const uint2 c = cast8_codes<FMT>(p, s);
+    for (int j = 0; j < 8; ++j) all = max_abs_bf16x2(all, v[j]);
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+        const uint2 c = cast8_codes<FMT>(make_uint4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]), s);
         q[2 * g] = c.x;
         q[2 * g + 1] = c.y;
     }
-    amax2 = __vmaxu2(amax2, all);
+    amax2 = max_abs_bf16x2(amax2, all);
     if (!(__fmul_rn(__uint_as_float(max16x2(all) << 16), s) <= fp8_max_value(FMT))) {  // (a NaN counts the others too)
 #pragma unroll
-        for (int g = 0; g < 4; ++g)
+        for (int g = 0; g < 2; ++g)
             nsat += sat_count8<FMT>(make_uint4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]), s);
-    }
-    if (want_codes) {
-        *reinterpret_cast<uint4*>(codes + lane * 32) = make_uint4(q[0], q[1], q[2], q[3]);
-        *reinterpret_cast<uint4*>(codes + lane * 32 + 16) = make_uint4(q[4], q[5], q[6], q[7]);
-    }
-    if (want_turned) {
-        const uint32_t sel1 = lane & 1 ? 0x3715u : 0x6240u, sel2 = lane & 2 ? 0x3276u : 0x5410u;
-        uint8_t* to = turned + (lane & 3) * 32 + (lane >> 2) * 4;
-#pragma unroll
-        for (int w = 0; w < 8; ++w) {
-            uint32_t x = __byte_perm(q[w], __shfl_xor_sync(0xFFFFFFFFu, q[w], 1), sel1);
-            x = __byte_perm(x, __shfl_xor_sync(0xFFFFFFFFu, x, 2), sel2);
-            *reinterpret_cast<uint32_t*>(to + w * 128) = x;
-        }
     }
 }
 
 // The magnitudes alone (a call that wants a maximum but no codes).
-__device__ __forceinline__ void glu_amax(const uint32_t (&v)[16], uint32_t& amax2) {
+__device__ __forceinline__ void glu_amax(const uint32_t (&v)[8], uint32_t& amax2) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) amax2 = __vmaxu2(amax2, v[j] & 0x7FFF7FFFu);
+    for (int j = 0; j < 8; ++j) amax2 = max_abs_bf16x2(amax2, v[j]);
 }
 
-// 32 packed BF16 columns of this lane's row into a 32 x 32 box in the 64-byte swizzle.
-__device__ __forceinline__ void put_box(uint8_t* box, int lane, const uint32_t (&v)[16]) {
-    const int sw = (lane >> 1) & 3;
+// Codes of W words (4 W columns) of 32 rows to the transposed tensor [., M], whose row `col` is at
+// `to` (this lane's piece of 4 rows).  Four lanes turn 4 x 4 bytes by two exchanges: neighbouring
+// lanes swap odd for even bytes, then pairs of lanes high for low halves; lane 4 k + i then holds
+// rows 4 k .. 4 k + 3 of column 4 w + i, and a warp's store is four whole 32-byte sectors.
+template <int W>
+__device__ __forceinline__ void glu_turned(const uint32_t* q, uint8_t* to, int64_t M, int lane, bool in) {
+    const uint32_t sel1 = lane & 1 ? 0x3715u : 0x6240u, sel2 = lane & 2 ? 0x3276u : 0x5410u;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-        *reinterpret_cast<uint4*>(box + lane * 64 + ((j ^ sw) << 4)) =
-            make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    for (int w = 0; w < W; ++w) {
+        uint32_t x = __byte_perm(q[w], __shfl_xor_sync(0xFFFFFFFFu, q[w], 1), sel1);
+        x = __byte_perm(x, __shfl_xor_sync(0xFFFFFFFFu, x, 2), sel2);
+        if (in) *reinterpret_cast<uint32_t*>(to) = x;
+        to += 4 * M;
+    }
 }
 
 __device__ __forceinline__ f32x2 acc_pair(uint32_t a, uint32_t b) { return pair_of(__uint_as_float(a), __uint_as_float(b)); }
 
+// 16 accumulator columns each of g and u -> packed BF16 a.
 template <int ACT>
-__device__ __forceinline__ void glu_products(const uint32_t (&g)[32], const uint32_t (&u)[32], float inv,
-                                             uint32_t (&a)[16]) {
+__device__ __forceinline__ void glu_products(const uint32_t (&g)[16], const uint32_t (&u)[16], float inv, uint32_t (&a)[8]) {
     const f32x2 inv2 = twice(inv);
 #pragma unroll
-    for (int j = 0; j < 16; ++j)
+    for (int j = 0; j < 8; ++j)
         a[j] = bf16x2_of(mul2(glu_act<ACT>(mul2(acc_pair(g[2 * j], g[2 * j + 1]), inv2)),
                               mul2(acc_pair(u[2 * j], u[2 * j + 1]), inv2)));
 }
 
-// The accumulator's 32 columns of this lane's row as packed BF16.
-__device__ __forceinline__ void glu_stored(const uint32_t (&r)[32], float inv, uint32_t (&h)[16]) {
+// The accumulator's columns as packed BF16.
+__device__ __forceinline__ void glu_stored(const uint32_t (&r)[16], float inv, uint32_t (&h)[8]) {
     const f32x2 inv2 = twice(inv);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) h[j] = bf16x2_of(mul2(acc_pair(r[2 * j], r[2 * j + 1]), inv2));
+    for (int j = 0; j < 8; ++j) h[j] = bf16x2_of(mul2(acc_pair(r[2 * j], r[2 * j + 1]), inv2));
 }
 
-// dA of this lane's row (32 columns), its g and u from the boxes -> packed BF16 dg and du.
+// 16 columns of dA, g and u -> packed BF16 dg and du.
 template <int ACT>
-__device__ __forceinline__ void glu_gradients(const uint32_t (&r)[32], float inv, const uint8_t* gbox,
-                                              const uint8_t* ubox, int lane, uint32_t (&dg)[16], uint32_t (&du)[16]) {
-    const int sw = (lane >> 1) & 3;
+__device__ __forceinline__ void glu_gradients(const uint32_t (&r)[16], float inv, const uint32_t (&g)[8],
+                                              const uint32_t (&u)[8], uint32_t (&dg)[8], uint32_t (&du)[8]) {
     const f32x2 inv2 = twice(inv);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const int at = lane * 64 + ((k ^ sw) << 4);
-        const uint4 g4 = *reinterpret_cast<const uint4*>(gbox + at), u4 = *reinterpret_cast<const uint4*>(ubox + at);
-        const uint32_t gw[4] = {g4.x, g4.y, g4.z, g4.w}, uw[4] = {u4.x, u4.y, u4.z, u4.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const f32x2 d = mul2(acc_pair(r[8 * k + 2 * j], r[8 * k + 2 * j + 1]), inv2);
-            f32x2 f, slope;
-            glu_act_grad<ACT>(f32x2_of(gw[j]), f, slope);
-            dg[4 * k + j] = bf16x2_of(mul2(mul2(d, f32x2_of(uw[j])), slope));
-            du[4 * k + j] = bf16x2_of(mul2(d, f));
-        }
+    for (int j = 0; j < 8; ++j) {
+        const f32x2 d = mul2(acc_pair(r[2 * j], r[2 * j + 1]), inv2);
+        f32x2 f, slope;
+        glu_act_grad<ACT>(f32x2_of(g[j]), f, slope);
+        dg[j] = bf16x2_of(mul2(mul2(d, f32x2_of(u[j])), slope));
+        du[j] = bf16x2_of(mul2(d, f));
     }
 }
 
+// Arrive on an mbarrier of the cluster without ordering this thread's memory accesses: what the
+// arrival reports is that TMEM was read into registers, which the load's own wait has seen to.  (With
+// .release it waited until the warp's stores had reached memory, once a tile: of 16 384 x 6400 x 1600
+// backward a sixth of the epilogue's stalls.)
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" :: "r"(cluster_addr) : "memory");
+}
+
+// Two loads of 32 lanes x 16 columns in flight, then one wait.
+__device__ __forceinline__ void tmem_ld_2x16_sync(uint32_t taddr0, uint32_t taddr1, uint32_t (&r0)[16], uint32_t (&r1)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%33];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r0[0]), "=r"(r0[1]), "=r"(r0[2]), "=r"(r0[3]), "=r"(r0[4]), "=r"(r0[5]), "=r"(r0[6]), "=r"(r0[7]), "=r"(r0[8]), "=r"(r0[9]), "=r"(r0[10]), "=r"(r0[11]), "=r"(r0[12]), "=r"(r0[13]), "=r"(r0[14]), "=r"(r0[15]),
+          "=r"(r1[0]), "=r"(r1[1]), "=r"(r1[2]), "=r"(r1[3]), "=r"(r1[4]), "=r"(r1[5]), "=r"(r1[6]), "=r"(r1[7]), "=r"(r1[8]), "=r"(r1[9]), "=r"(r1[10]), "=r"(r1[11]), "=r"(r1[12]), "=r"(r1[13]), "=r"(r1[14]), "=r"(r1[15])
+        : "r"(taddr0), "r"(taddr1) : "memory");
+}
+
+// The tiles of one CTA (pair), n fastest, without a division a tile.
+struct TileWalk {
+    int64_t left, m, n, num_n, step, step_m, step_n;  // tiles from here to the last; this one's row and column block
+    __device__ __forceinline__ TileWalk(int64_t first, int64_t stride, int64_t tiles, int64_t columns)
+        : left(tiles - first), m(first / columns), n(first % columns), num_n(columns), step(stride),
+          step_m(stride / columns), step_n(stride % columns) {}
+    __device__ __forceinline__ bool more() const { return left > 0; }
+    __device__ __forceinline__ void next() {
+        left -= step;
+        m += step_m;
+        n += step_n;
+        if (n >= num_n) {
+            n -= num_n;
+            ++m;
+        }
+    }
+};
+
 template <int BN, bool PAIR, bool BWD>
-__global__ void __launch_bounds__(kGluThreads, 1)
+__global__ void __launch_bounds__((GluCfg<BN, PAIR, BWD>::THREADS), 1)
 glu_kernel(const __grid_constant__ GluMaps maps, const GluArgs p) {
     using C = GluCfg<BN, PAIR, BWD>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t* stage0 = smem + C::STAGES * C::STAGE_BYTES;  // the epilogue warps' buffers, 1024-aligned
-    uint64_t* bars = reinterpret_cast<uint64_t*>(stage0 + kGluWarps * C::WARP_BYTES);
+    uint8_t* boxes = smem + C::STAGES * C::STAGE_BYTES;  // 1024-aligned
+    uint64_t* bars = reinterpret_cast<uint64_t*>(boxes + C::LOAD_BYTES);
     uint64_t* full = bars;
     uint64_t* empty = full + C::STAGES;
     uint64_t* tfull = empty + C::STAGES;
     uint64_t* tempty = tfull + C::ACCS;
     uint64_t* drain = tempty + C::ACCS;
     uint64_t* loaded = drain + 1;  // backward: [warp][buffer]
-    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(loaded + 2 * kGluWarps);
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(loaded + C::LOADS * C::WARPS);
     volatile int* abort_flag = reinterpret_cast<int*>(tmem_holder) + 1;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -202,8 +250,7 @@ glu_kernel(const __grid_constant__ GluMaps maps, const GluArgs p) {
     const bool leader = rank == 0;
     const int64_t num_n = (p.F + C::OUT - 1) / C::OUT;
     const int64_t num_tiles = ((p.M + C::TILE_M - 1) / C::TILE_M) * num_n;
-    const int64_t first_tile = PAIR ? blockIdx.x / 2 : blockIdx.x;
-    const int64_t tile_stride = PAIR ? gridDim.x / 2 : gridDim.x;
+    TileWalk tile(PAIR ? blockIdx.x / 2 : blockIdx.x, PAIR ? gridDim.x / 2 : gridDim.x, num_tiles, num_n);
     const int num_kb = static_cast<int>((p.K + BK - 1) / BK);
 
     if (threadIdx.x == 0) {
@@ -213,10 +260,10 @@ glu_kernel(const __grid_constant__ GluMaps maps, const GluArgs p) {
         }
         for (int a = 0; a < C::ACCS; ++a) {
             mbar_init(smem_u32(&tfull[a]), 1);
-            mbar_init(smem_u32(&tempty[a]), kGluWarps * (PAIR ? 2 : 1));
+            mbar_init(smem_u32(&tempty[a]), C::WARPS * (PAIR ? 2 : 1));
         }
         mbar_init(smem_u32(drain), 1);
-        for (int i = 0; i < 2 * kGluWarps; ++i) mbar_init(smem_u32(&loaded[i]), 1);
+        for (int i = 0; i < C::LOADS * C::WARPS; ++i) mbar_init(smem_u32(&loaded[i]), 1);
         *abort_flag = 0;
         fence_mbar_init();
         tma_prefetch_desc(&maps.a);
@@ -245,9 +292,9 @@ glu_kernel(const __grid_constant__ GluMaps maps, const GluArgs p) {
             uint32_t phase = 0;
             int64_t issued = 0;
             bool ok = true;
-            for (int64_t tile = first_tile; tile < num_tiles && ok; tile += tile_stride) {
-                const int32_t m0 = static_cast<int32_t>((tile / num_n) * C::TILE_M + rank * BM);
-                const int32_t n0 = static_cast<int32_t>((tile % num_n) * C::OUT);
+            for (; tile.more() && ok; tile.next()) {
+                const int32_t m0 = static_cast<int32_t>(tile.m * C::TILE_M + rank * BM);
+                const int32_t n0 = static_cast<int32_t>(tile.n * C::OUT);
                 const int32_t up = static_cast<int32_t>(p.F) + n0;  // forward: the up-projection's rows of W1^T
                 for (int kb = 0; kb < num_kb; ++kb) {
                     if (!wait_phase(&empty[stage], phase ^ 1u, abort_flag, p.status)) { ok = false; break; }
@@ -285,7 +332,7 @@ glu_kernel(const __grid_constant__ GluMaps maps, const GluArgs p) {
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
             bool ok = true;
-            for (int64_t tile = first_tile; tile < num_tiles && ok; tile += tile_stride) {
+            for (; tile.more() && ok; tile.next()) {
                 if (!wait_phase(&tempty[acc], acc_phase ^ 1u, abort_flag, p.status)) break;
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
@@ -314,167 +361,169 @@ glu_kernel(const __grid_constant__ GluMaps maps, const GluArgs p) {
             wait_phase_drain(drain, 0);
         }
     } else {
-        const int q = warp & 3;           // TMEM lane quarter of this warp
-        const int c0 = (warp - 2) / 4;    // its first chunk; every second one is the other warp's
-        const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
+        constexpr int STEP = C::WARPS / 4;
+        const int quarter = warp & 3;     // TMEM lane quarter of this warp
+        const int c0 = (warp - 2) / 4;    // its first chunk, and every STEPth one from there
+        const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
         const uint32_t tempty0 = PAIR ? mapa_shared(smem_u32(&tempty[0]), 0) : smem_u32(&tempty[0]);
-        uint8_t* buf = stage0 + (warp - 2) * C::WARP_BYTES;
         const float inv = 1.0f / (__ldg(p.scale_a) * __ldg(p.scale_b));
         const float s_q = p.scale_q ? __ldg(p.scale_q) : 0.0f;
         uint32_t amax2 = 0, nsat = 0;
         int acc = 0;
         uint32_t acc_phase = 0;
-        bool ok = true, stored = false;
+        bool arrived = true;
 
-        auto first_row = [&](int64_t tile) { return (tile / num_n) * C::TILE_M + rank * BM + q * 32; };
-        auto first_col = [&](int64_t tile, int c) { return (tile % num_n) * C::OUT + c * 32; };
+        const int64_t row_in_tile = rank * BM + quarter * 32 + lane;
+        auto row_of = [&](const TileWalk& w) { return w.m * C::TILE_M + row_in_tile; };
+        auto col_of = [&](const TileWalk& w, int c) { return w.n * C::OUT + c * 32; };
 
-        // backward: this warp's next chunk of g and u, in the order in which they are used;
-        // `asked` of them are on the way or read, `used` of them read
-        uint64_t* bar = loaded + 2 * (warp - 2);
-        int64_t ask_tile = first_tile;
+        // backward: this warp's chunks of g and u, in the order in which they are used; `asked` of them
+        // are on the way or read, `used` of them read
+        constexpr int LOADS = C::LOADS > 0 ? C::LOADS : 1;
+        uint8_t* const box0 = boxes + (warp - 2) * C::LOADS * 2 * kBoxBytes;
+        uint64_t* const bar = loaded + C::LOADS * (warp - 2);
+        TileWalk ask_tile = tile;
         int ask_c = c0;
         uint32_t asked = 0, used = 0;
         auto ask = [&]() {
-            while (ask_tile < num_tiles && (ask_c >= C::CHUNKS || first_row(ask_tile) >= p.M || first_col(ask_tile, ask_c) >= p.F)) {
-                ask_tile += tile_stride;
+            while (ask_tile.more() && (ask_c >= C::CHUNKS || row_of(ask_tile) - lane >= p.M || col_of(ask_tile, ask_c) >= p.F)) {
+                ask_tile.next();
                 ask_c = c0;
             }
-            if (ask_tile >= num_tiles) return;
+            if (!ask_tile.more()) return;
             if (lane == 0) {
-                const uint32_t b = smem_u32(&bar[asked & 1]), to = smem_u32(buf + (asked & 1) * 4 * kBox);
-                const int32_t x = static_cast<int32_t>(first_col(ask_tile, ask_c)), y = static_cast<int32_t>(first_row(ask_tile));
-                mbar_arrive_expect_tx(b, 4 * kBox);
+                const uint32_t b = smem_u32(&bar[asked % LOADS]), to = smem_u32(box0 + (asked % LOADS) * 2 * kBoxBytes);
+                const int32_t x = static_cast<int32_t>(col_of(ask_tile, ask_c)), y = static_cast<int32_t>(row_of(ask_tile));
+                mbar_arrive_expect_tx(b, 2 * kBoxBytes);
                 tma_load_2d(to, &maps.h0, b, x, y);
-                tma_load_2d(to + 2 * kBox, &maps.h1, b, x, y);
+                tma_load_2d(to + kBoxBytes, &maps.h1, b, x, y);
             }
             ++asked;
-            ask_c += 2;
+            ask_c += STEP;
         };
-        if constexpr (BWD) ask();
+        if constexpr (BWD) {
+            for (int i = 0; i < LOADS; ++i) ask();
+        }
 
-        for (int64_t tile = first_tile; tile < num_tiles; tile += tile_stride) {
-            const int64_t row0 = first_row(tile);
-            ok = __all_sync(0xFFFFFFFFu, wait_phase(&tfull[acc], acc_phase, abort_flag, p.status));
-            if (!ok) break;
+        for (; tile.more(); tile.next()) {
+            const int64_t row = row_of(tile);
+            const bool in = row < p.M;
+            if (!__all_sync(0xFFFFFFFFu, wait_phase(&tfull[acc], acc_phase, abort_flag, p.status))) break;
             tc_fence_after();
             const uint32_t taddr = tmem_base + lane_base + static_cast<uint32_t>(acc * BN);
+            // this lane's part of the transposed codes: rows 4 (lane / 4) .. + 3 of the warp's 32, column lane % 4
+            const int64_t trow = row - lane + (lane >> 2) * 4;
+            const bool tin = trow < p.M;
+            bool released = false;
+            auto release = [&]() {  // this warp's columns of the accumulator are in registers
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (PAIR) mbar_arrive_cluster_relaxed(tempty0 + 8u * acc);
+                    else mbar_arrive(tempty0 + 8u * acc);
+                }
+                released = true;
+            };
 #pragma unroll 1
-            for (int c = c0; c < C::CHUNKS; c += 2) {
-                const int64_t col0 = first_col(tile, c);
-                if (row0 >= p.M || col0 >= p.F) break;
-                const int32_t x = static_cast<int32_t>(col0), y = static_cast<int32_t>(row0);
-                if constexpr (!BWD) {
-                    uint32_t g[32], u[32], a[16];
-                    tmem_ld_2x32_sync(taddr + c * 32, taddr + C::OUT + c * 32, g, u);
-                    if (col0 + 32 > p.F) {  // F ends inside the chunk: its last 16 columns are not the gate's
-#pragma unroll
-                        for (int j = 16; j < 32; ++j) g[j] = u[j] = 0;
-                    }
-                    switch (p.act) {
-                        case FP8Q_ACT_IDENTITY: glu_products<FP8Q_ACT_IDENTITY>(g, u, inv, a); break;
-                        case FP8Q_ACT_RELU: glu_products<FP8Q_ACT_RELU>(g, u, inv, a); break;
-                        case FP8Q_ACT_RELU2: glu_products<FP8Q_ACT_RELU2>(g, u, inv, a); break;
-                        case FP8Q_ACT_SILU: glu_products<FP8Q_ACT_SILU>(g, u, inv, a); break;
-                        default: glu_products<FP8Q_ACT_GELU>(g, u, inv, a); break;
-                    }
-                    if (stored) {  // the last chunk's stores have read the buffers
-                        if (lane == 0) bulk_wait_group_read<0>();
-                        __syncwarp();
-                    }
-                    if (p.has_o) {
-                        uint32_t hv[16];
-                        glu_stored(g, inv, hv);
-                        put_box(buf, lane, hv);
-                        glu_stored(u, inv, hv);
-                        put_box(buf + 2 * kBox, lane, hv);
-                    }
-                    if (p.has_d) put_box(buf + 4 * kBox, lane, a);
-                    if (p.scale_q)
-                        glu_codes<FP8Q_E4M3>(a, s_q, buf + 6 * kBox, buf + 7 * kBox, lane, p.has_q, p.has_t, amax2, nsat);
-                    else
-                        glu_amax(a, amax2);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (p.has_o) {
-                            tma_store_2d(&maps.o0, smem_u32(buf), x, y);
-                            tma_store_2d(&maps.o1, smem_u32(buf + 2 * kBox), x, y);
-                        }
-                        if (p.has_d) tma_store_2d(&maps.d, smem_u32(buf + 4 * kBox), x, y);
-                        if (p.has_q) tma_store_2d(&maps.q0, smem_u32(buf + 6 * kBox), x, y);
-                        if (p.has_t) tma_store_2d(&maps.t0, smem_u32(buf + 7 * kBox), y, x);
-                        bulk_commit_group();
-                    }
-                    stored = true;
-                } else {
-                    // the stores of the chunk before have read their buffers: the next chunk may be asked for
-                    if (stored) {
-                        if (lane == 0) bulk_wait_group_read<0>();
-                        __syncwarp();
-                    }
-                    ask();
-                    ok = __all_sync(0xFFFFFFFFu, wait_phase(&bar[used & 1], (used >> 1) & 1, abort_flag, p.status));
-                    if (!ok) break;
-                    uint8_t* box = buf + (used & 1) * 4 * kBox;
-                    uint8_t* codes = buf + 8 * kBox;
+            for (int c = c0; c < C::CHUNKS; c += STEP) {
+                const int64_t col0 = col_of(tile, c);
+                if (row - lane >= p.M || col0 >= p.F) break;
+                const bool whole = col0 + 32 <= p.F;  // otherwise F ends after 16 columns
+                const bool last = c + STEP >= C::CHUNKS || col0 + STEP * 32 >= p.F;
+                uint32_t q[BWD ? 2 : 1][8];
+                const uint8_t* box = box0 + (used % LOADS) * 2 * kBoxBytes + lane * 64;
+                if constexpr (BWD) {
+                    arrived = __all_sync(0xFFFFFFFFu, wait_phase(&bar[used % LOADS], (used / LOADS) & 1, abort_flag, p.status));
+                    if (!arrived) break;
                     ++used;
-                    uint32_t r[32], dg[16], du[16];
-                    tmem_ld_x32_sync(taddr + c * 32, r);
-                    switch (p.act) {
-                        case FP8Q_ACT_IDENTITY: glu_gradients<FP8Q_ACT_IDENTITY>(r, inv, box, box + 2 * kBox, lane, dg, du); break;
-                        case FP8Q_ACT_RELU: glu_gradients<FP8Q_ACT_RELU>(r, inv, box, box + 2 * kBox, lane, dg, du); break;
-                        case FP8Q_ACT_RELU2: glu_gradients<FP8Q_ACT_RELU2>(r, inv, box, box + 2 * kBox, lane, dg, du); break;
-                        case FP8Q_ACT_SILU: glu_gradients<FP8Q_ACT_SILU>(r, inv, box, box + 2 * kBox, lane, dg, du); break;
-                        default: glu_gradients<FP8Q_ACT_GELU>(r, inv, box, box + 2 * kBox, lane, dg, du); break;
-                    }
-                    if (p.has_o) {  // each lane over its own row of g and u
-                        put_box(box, lane, dg);
-                        put_box(box + 2 * kBox, lane, du);
-                    }
-                    if (p.scale_q) {
-                        glu_codes<FP8Q_E5M2>(dg, s_q, codes, codes + kBox, lane, p.has_q, p.has_t, amax2, nsat);
-                        glu_codes<FP8Q_E5M2>(du, s_q, codes + 2 * kBox, codes + 3 * kBox, lane, p.has_q, p.has_t, amax2, nsat);
+                }
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int64_t col = col0 + half * 16;
+                    const bool ok = in && (half == 0 || whole);
+                    if constexpr (!BWD) {
+                        uint32_t g[16], u[16], a[8];
+                        tmem_ld_2x16_sync(taddr + c * 32 + half * 16, taddr + C::OUT + c * 32 + half * 16, g, u);
+                        if (half == 1 && last) release();
+                        if (half == 1 && !whole) {  // (the accumulator's next columns are not the gate's)
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) g[j] = u[j] = 0;
+                        }
+                        switch (p.act) {
+                            case FP8Q_ACT_IDENTITY: glu_products<FP8Q_ACT_IDENTITY>(g, u, inv, a); break;
+                            case FP8Q_ACT_RELU: glu_products<FP8Q_ACT_RELU>(g, u, inv, a); break;
+                            case FP8Q_ACT_RELU2: glu_products<FP8Q_ACT_RELU2>(g, u, inv, a); break;
+                            case FP8Q_ACT_SILU: glu_products<FP8Q_ACT_SILU>(g, u, inv, a); break;
+                            default: glu_products<FP8Q_ACT_GELU>(g, u, inv, a); break;
+                        }
+                        if (p.o) {
+                            uint32_t hv[8];
+                            uint16_t* at = p.o + row * 2 * p.F + col;
+                            glu_stored(g, inv, hv);
+                            if (ok) st_32(at, hv, p.wide_bf);
+                            glu_stored(u, inv, hv);
+                            if (ok) st_32(at + p.F, hv, p.wide_bf);
+                        }
+                        if (p.d && ok) st_32(p.d + row * p.F + col, a, p.wide_bf);
+                        if (p.scale_q) glu_codes<FP8Q_E4M3>(a, s_q, &q[0][half * 4], amax2, nsat);
+                        else glu_amax(a, amax2);
                     } else {
-                        glu_amax(dg, amax2);
-                        glu_amax(du, amax2);
+                        uint32_t r[16], g[8], u[8], dg[8], du[8];
+                        tmem_ld_x16_sync(taddr + c * 32 + half * 16, r);
+                        if (half == 1 && last) release();
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const int at = ((2 * half + k) ^ ((lane >> 1) & 3)) << 4;
+                            const uint4 g4 = *reinterpret_cast<const uint4*>(box + at), u4 = *reinterpret_cast<const uint4*>(box + kBoxBytes + at);
+                            g[4 * k] = g4.x; g[4 * k + 1] = g4.y; g[4 * k + 2] = g4.z; g[4 * k + 3] = g4.w;
+                            u[4 * k] = u4.x; u[4 * k + 1] = u4.y; u[4 * k + 2] = u4.z; u[4 * k + 3] = u4.w;
+                        }
+                        if (half == 1) {  // every lane has read its g and u: the buffer takes another chunk
+                            __syncwarp();
+                            ask();
+                        }
+                        switch (p.act) {
+                            case FP8Q_ACT_IDENTITY: glu_gradients<FP8Q_ACT_IDENTITY>(r, inv, g, u, dg, du); break;
+                            case FP8Q_ACT_RELU: glu_gradients<FP8Q_ACT_RELU>(r, inv, g, u, dg, du); break;
+                            case FP8Q_ACT_RELU2: glu_gradients<FP8Q_ACT_RELU2>(r, inv, g, u, dg, du); break;
+                            case FP8Q_ACT_SILU: glu_gradients<FP8Q_ACT_SILU>(r, inv, g, u, dg, du); break;
+                            default: glu_gradients<FP8Q_ACT_GELU>(r, inv, g, u, dg, du); break;
+                        }
+                        if (p.o && ok) {
+                            uint16_t* at = p.o + row * 2 * p.F + col;
+                            st_32(at, dg, p.wide_bf);
+                            st_32(at + p.F, du, p.wide_bf);
+                        }
+                        if (p.scale_q) {
+                            glu_codes<FP8Q_E5M2>(dg, s_q, &q[0][half * 4], amax2, nsat);
+                            glu_codes<FP8Q_E5M2>(du, s_q, &q[BWD ? 1 : 0][half * 4], amax2, nsat);
+                        } else {
+                            glu_amax(dg, amax2);
+                            glu_amax(du, amax2);
+                        }
                     }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (p.has_o) {
-                            tma_store_2d(&maps.o0, smem_u32(box), x, y);
-                            tma_store_2d(&maps.o1, smem_u32(box + 2 * kBox), x, y);
-                        }
-                        if (p.has_q) {
-                            tma_store_2d(&maps.q0, smem_u32(codes), x, y);
-                            tma_store_2d(&maps.q1, smem_u32(codes + 2 * kBox), x, y);
-                        }
-                        if (p.has_t) {
-                            tma_store_2d(&maps.t0, smem_u32(codes + kBox), y, x);
-                            tma_store_2d(&maps.t1, smem_u32(codes + 3 * kBox), y, x);
-                        }
-                        bulk_commit_group();
+                }
+#pragma unroll
+                for (int k = 0; k < (BWD ? 2 : 1); ++k) {
+                    const int64_t col = col0 + k * p.F;
+                    if (p.q && in) {
+                        uint8_t* at = p.q + row * (BWD ? 2 : 1) * p.F + col;
+                        if (whole) st_32(at, q[k], p.wide_q);
+                        else st_v4(at, make_uint4(q[k][0], q[k][1], q[k][2], q[k][3]));
                     }
-                    stored = true;
+                    if (p.t) {
+                        uint8_t* at = p.t + (col + (lane & 3)) * p.M + trow;
+                        glu_turned<4>(q[k], at, p.M, lane, tin);
+                        if (whole) glu_turned<4>(q[k] + 4, at + 16 * p.M, p.M, lane, tin);
+                    }
                 }
             }
-            if (!ok) break;
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                if constexpr (PAIR) mbar_arrive_cluster(tempty0 + 8u * acc);
-                else mbar_arrive(tempty0 + 8u * acc);
-            }
+            if (!arrived) break;
+            if (!released) release();  // none of the tile is this warp's
             next_acc<C::ACCS>(acc, acc_phase);
         }
-        // no load may still be landing in shared memory when the CTA exits, and every store has read it
-        while (BWD && used < asked) {
-            wait_phase_drain(&bar[used & 1], (used >> 1) & 1);
-            ++used;
-        }
-        if (lane == 0) bulk_wait_group_read<0>();
-        __syncwarp();
+        // no load may still be landing in shared memory when the CTA exits
+        for (; BWD && used < asked; ++used) wait_phase_drain(&bar[used % LOADS], (used / LOADS) & 1);
         const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, max16x2(amax2));
         const uint32_t n = __reduce_add_sync(0xFFFFFFFFu, nsat);
         if (lane == 0) {
@@ -494,35 +543,21 @@ glu_kernel(const __grid_constant__ GluMaps maps, const GluArgs p) {
 }
 
 // ------------------------------------------------------------------- host --
-// One of the halves of a tensor that the epilogue moves in 32 x 32 boxes: `rows` rows of
-// `cols` elements, `ld` elements apart, BF16 (64-byte swizzle) or bytes (no swizzle).
-bool make_box_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld, bool bf16) {
+// A half of h [M,2F]: 32 x 32 boxes in the 64-byte swizzle.
+bool make_half_map(CUtensorMap* map, const void* base, int64_t M, int64_t F) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
-    cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-    cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld * (bf16 ? 2 : 1))};
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(F), static_cast<cuuint64_t>(M)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(4 * F)};
     cuuint32_t box[2] = {32, 32};
     cuuint32_t estr[2] = {1, 1};
-    return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base),
-              dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              bf16 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The tensors of a call.  Forward: x [M,K], w [2F,K], o = h_out, d = act_out, q [M,F], t [F,M].
-// Backward: x = dY [M,K], w = W2 [F,K], h [M,2F], o = dh, q [M,2F], t [2F,M].
-struct GluTensors {
-    const void* x;
-    const void* w;
-    const void* h;
-    void* o;
-    void* d;
-    void* q;
-    void* t;
-};
-
 template <int BN, bool PAIR, bool BWD>
-int launch_glu(const GluTensors& io, GluArgs p, cudaStream_t stream) {
+int launch_glu(GluArgs p, cudaStream_t stream) {
     using C = GluCfg<BN, PAIR, BWD>;
     const auto kern = glu_kernel<BN, PAIR, BWD>;
     // co-resident CTAs (pairs) of the current device, whose copy of the kernel may take the shared memory
@@ -542,7 +577,7 @@ int launch_glu(const GluTensors& io, GluArgs p, cudaStream_t stream) {
         attr[0].val.clusterDim.x = 2;
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
         cfg.gridDim = dim3(2 * sm_count());
-        cfg.blockDim = dim3(kGluThreads);
+        cfg.blockDim = dim3(C::THREADS);
         cfg.dynamicSmemBytes = C::SMEM_BYTES;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
@@ -553,29 +588,11 @@ int launch_glu(const GluTensors& io, GluArgs p, cudaStream_t stream) {
         return FP8Q_ERR_CUDA;
     }
     const int64_t M = p.M, F = p.F;
-    const int64_t halves = BWD ? 2 * F : F;  // columns of the codes
     alignas(64) GluMaps maps;
-    if (!make_kmajor_map(&maps.a, io.x, M, p.K, BM) || !make_kmajor_map(&maps.b, io.w, BWD ? F : 2 * F, p.K, C::B_BOX))
+    if (!make_kmajor_map(&maps.a, p.x, M, p.K, BM) || !make_kmajor_map(&maps.b, p.w, BWD ? F : 2 * F, p.K, C::B_BOX))
         return FP8Q_ERR_CUDA;
-    maps.h0 = maps.h1 = maps.o0 = maps.o1 = maps.d = maps.q0 = maps.q1 = maps.t0 = maps.t1 = maps.a;
-    const auto half = [](const void* base, int64_t bytes) { return static_cast<const uint8_t*>(base) + bytes; };
-    bool ok = true;
-    if (BWD) ok = make_box_map(&maps.h0, io.h, M, F, 2 * F, true) && make_box_map(&maps.h1, half(io.h, 2 * F), M, F, 2 * F, true);
-    if (io.o) ok = ok && make_box_map(&maps.o0, io.o, M, F, 2 * F, true) && make_box_map(&maps.o1, half(io.o, 2 * F), M, F, 2 * F, true);
-    if (io.d) ok = ok && make_box_map(&maps.d, io.d, M, F, F, true);
-    if (io.q) {
-        ok = ok && make_box_map(&maps.q0, io.q, M, F, halves, false);
-        if (BWD) ok = ok && make_box_map(&maps.q1, half(io.q, F), M, F, halves, false);
-    }
-    if (io.t) {
-        ok = ok && make_box_map(&maps.t0, io.t, F, M, M, false);
-        if (BWD) ok = ok && make_box_map(&maps.t1, half(io.t, F * M), F, M, M, false);
-    }
-    if (!ok) return FP8Q_ERR_CUDA;
-    p.has_o = io.o != nullptr;
-    p.has_d = io.d != nullptr;
-    p.has_q = io.q != nullptr;
-    p.has_t = io.t != nullptr;
+    maps.h0 = maps.h1 = maps.a;
+    if (BWD && (!make_half_map(&maps.h0, p.h, M, F) || !make_half_map(&maps.h1, p.h + F, M, F))) return FP8Q_ERR_CUDA;
     p.idesc = idesc_f8(BWD ? FP8Q_E5M2 : FP8Q_E4M3, FP8Q_E4M3, C::TILE_M, BN);
     const int64_t tiles = ((M + C::TILE_M - 1) / C::TILE_M) * ((F + C::OUT - 1) / C::OUT);
     const int n = static_cast<int>(std::min<int64_t>(tiles, units));
@@ -587,7 +604,7 @@ int launch_glu(const GluTensors& io, GluArgs p, cudaStream_t stream) {
     attr[1].val.clusterDim.x = 2;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.gridDim = dim3(PAIR ? 2 * n : n);
-    cfg.blockDim = dim3(kGluThreads);
+    cfg.blockDim = dim3(C::THREADS);
     cfg.dynamicSmemBytes = C::SMEM_BYTES;
     cfg.stream = stream;
     cfg.attrs = attr;
@@ -602,7 +619,7 @@ int launch_glu(const GluTensors& io, GluArgs p, cudaStream_t stream) {
 
 // The tile, scored as gemm.cu scores its own: waves x a tile's relative time.
 template <bool BWD>
-int dispatch_glu(const GluTensors& io, const GluArgs& p, cudaStream_t stream) {
+int dispatch_glu(const GluArgs& p, cudaStream_t stream) {
     struct Cand { bool pair; int bn; double t; };
     static constexpr Cand kCands[] = {{true, 256, 1.000}, {true, 192, 0.909}, {true, 128, 0.858},
                                       {false, 256, 1.102}, {false, 192, 0.897}, {false, 128, 0.843}, {false, 64, 0.750}};
@@ -617,14 +634,14 @@ int dispatch_glu(const GluTensors& io, const GluArgs& p, cudaStream_t stream) {
         if (best_cost < 0 || cost < best_cost) { best_cost = cost; best = c; }
     }
     if (best.pair) {
-        if (best.bn == 256) return launch_glu<256, true, BWD>(io, p, stream);
-        if (best.bn == 192) return launch_glu<192, true, BWD>(io, p, stream);
-        return launch_glu<128, true, BWD>(io, p, stream);
+        if (best.bn == 256) return launch_glu<256, true, BWD>(p, stream);
+        if (best.bn == 192) return launch_glu<192, true, BWD>(p, stream);
+        return launch_glu<128, true, BWD>(p, stream);
     }
-    if (best.bn == 256) return launch_glu<256, false, BWD>(io, p, stream);
-    if (best.bn == 192) return launch_glu<192, false, BWD>(io, p, stream);
-    if (best.bn == 128) return launch_glu<128, false, BWD>(io, p, stream);
-    return launch_glu<64, false, BWD>(io, p, stream);
+    if (best.bn == 256) return launch_glu<256, false, BWD>(p, stream);
+    if (best.bn == 192) return launch_glu<192, false, BWD>(p, stream);
+    if (best.bn == 128) return launch_glu<128, false, BWD>(p, stream);
+    return launch_glu<64, false, BWD>(p, stream);
 }
 
 // What both calls ask of their arguments: `a` [M,K] times `b`, scales, the optional outputs,
@@ -651,7 +668,7 @@ int check_glu(const void* a, const void* b, const float* scale_a, const float* s
     return FP8Q_OK;
 }
 
-int run_glu(bool bwd, const GluTensors& io, const GluArgs& p, unsigned flags, cudaStream_t stream) {
+int run_glu(bool bwd, GluArgs p, unsigned flags, cudaStream_t stream) {
     if (!(flags & FP8Q_ACCUMULATE) && (p.amax || p.sat)) {
         if (launch_pdl(clear_quant_kernel, dim3(1), dim3(1), 0, stream, p.amax, p.sat) != cudaSuccess) {
             (void)cudaGetLastError();
@@ -659,7 +676,10 @@ int run_glu(bool bwd, const GluTensors& io, const GluArgs& p, unsigned flags, cu
         }
     }
     if (p.M == 0) return FP8Q_OK;
-    return bwd ? dispatch_glu<true>(io, p, stream) : dispatch_glu<false>(io, p, stream);
+    // (a row of h, o or d is a multiple of 32 bytes long, one of q only where F is)
+    p.wide_bf = aligned_to(p.h, 32) && aligned_to(p.o, 32) && aligned_to(p.d, 32);
+    p.wide_q = aligned_to(p.q, 32) && p.F % 32 == 0;
+    return bwd ? dispatch_glu<true>(p, stream) : dispatch_glu<false>(p, stream);
 }
 
 }  // namespace
@@ -678,6 +698,12 @@ extern "C" int fp8_glu_fwd(const void* x_q, const void* w1t_q, const float* scal
     if (M != 0 && !act_out && !a_q && !a_q_t) return FP8Q_ERR_NULL;
     if (st != FP8Q_OK) return st;
     GluArgs p = {};
+    p.x = x_q;
+    p.w = w1t_q;
+    p.o = static_cast<uint16_t*>(h_out);
+    p.d = static_cast<uint16_t*>(act_out);
+    p.q = static_cast<uint8_t*>(a_q);
+    p.t = static_cast<uint8_t*>(a_q_t);
     p.scale_a = scale_x;
     p.scale_b = scale_w;
     p.scale_q = scale_a;
@@ -688,7 +714,7 @@ extern "C" int fp8_glu_fwd(const void* x_q, const void* w1t_q, const float* scal
     p.F = F;
     p.K = K;
     p.act = act;
-    return run_glu(false, GluTensors{x_q, w1t_q, nullptr, h_out, act_out, a_q, a_q_t}, p, flags, stream);
+    return run_glu(false, p, flags, stream);
 }
 
 extern "C" int fp8_gemm_dgrad_glu(const void* dy_q, const void* w2_q, const float* scale_dy, const float* scale_w,
@@ -701,6 +727,12 @@ extern "C" int fp8_gemm_dgrad_glu(const void* dy_q, const void* w2_q, const floa
     if (M != 0 && (!h || (!dh && !dh_q && !dh_q_t))) return FP8Q_ERR_NULL;
     if (st != FP8Q_OK) return st;
     GluArgs p = {};
+    p.x = dy_q;
+    p.w = w2_q;
+    p.h = static_cast<const uint16_t*>(h);
+    p.o = static_cast<uint16_t*>(dh);
+    p.q = static_cast<uint8_t*>(dh_q);
+    p.t = static_cast<uint8_t*>(dh_q_t);
     p.scale_a = scale_dy;
     p.scale_b = scale_w;
     p.scale_q = scale_dh;
@@ -711,5 +743,5 @@ extern "C" int fp8_gemm_dgrad_glu(const void* dy_q, const void* w2_q, const floa
     p.F = F;
     p.K = N;
     p.act = act;
-    return run_glu(true, GluTensors{dy_q, w2_q, h, dh, nullptr, dh_q, dh_q_t}, p, flags, stream);
+    return run_glu(true, p, flags, stream);
 }
