@@ -185,12 +185,15 @@ bn_fwd_kernel(const BnFwd<T> p, int team) {
 #pragma unroll
     for (int k = 0; k < S - 1; ++k) fill(k, base0 + sub + k * stride);
 
+    float gate_next = 1.0f;  // read a row ahead
+    if (p.gate && base0 + sub < M) gate_next = p.gate[base0 + sub];
     int stage = 0, buf = 0;
     for (uint32_t base = base0; base < M; base += stride) {
         const uint32_t row = base + sub;
         const bool in = row < M;
         fill(stage == 0 ? S - 1 : stage - 1, row + (S - 1) * stride);
-        const float gate = p.gate && in ? p.gate[row] : 1.0f;
+        const float gate = gate_next;
+        if (p.gate && row + stride < M) gate_next = p.gate[row + stride];
         cp_async_wait<S - 1>();
         if constexpr (SHIFT) __syncwarp();
         const uint4* at = ring + stage * kStage;
@@ -313,8 +316,9 @@ cudaError_t launch_bn_fwd_as(const BnFwd<T>& p, int team, unsigned block, cudaSt
 //     rhat = r rstd, g = dy w;  dr = dr_in + rstd (g - rhat sum(g rhat) / N)
 //     xhat = x rstd_post;       e = sum(dr wp xhat)
 //     dx = gate rstd_post (dr wp - xhat e / N)  [post],  gate dr wp  [not post]
-// The row's inputs come through a ring of two rows in shared memory.
-constexpr int kBnBwdStages = 2;
+// The row's inputs come through a ring of rows in shared memory: three, or two where the
+// residual is read too.
+constexpr int bn_bwd_stages(bool alpha) { return alpha ? 2 : 3; }
 enum { IN_DY, IN_R, IN_DR, IN_X, IN_RES };
 
 template <typename T, int C, bool WIDE, bool ALPHA, bool SHIFT>
@@ -322,7 +326,7 @@ __global__ void __launch_bounds__(512, 1)
 bn_bwd_kernel(const BnBwd<T> p, int team) {
     extern __shared__ uint4 s_ring[];
     __shared__ float s_sum[2][2][16];
-    constexpr int V = 16 / sizeof(T), H = V / 2, S = kBnBwdStages, TENSORS = ALPHA ? 5 : 4;
+    constexpr int V = 16 / sizeof(T), H = V / 2, S = bn_bwd_stages(ALPHA), TENSORS = ALPHA ? 5 : 4;
     constexpr int kSlots = warp_slots(SHIFT, !WIDE && C == 1), kStage = TENSORS * C * kSlots;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
     // WIDE: team = warps of a group; otherwise lanes of a row
@@ -388,7 +392,8 @@ bn_bwd_kernel(const BnBwd<T> p, int team) {
             if (!has(c))
                 for (int k = 0; k < S * TENSORS; ++k) ring[(k * C + c) * kSlots] = make_uint4(0, 0, 0, 0);
     }
-    fill(0, base0 + sub);
+#pragma unroll
+    for (int k = 0; k < S - 1; ++k) fill(k, base0 + sub + k * stride);
 
     auto group_sum = [&](float v, float* s) {
         v = team_sum<C == 1 && !WIDE>(v, lanes);
@@ -400,15 +405,23 @@ bn_bwd_kernel(const BnBwd<T> p, int team) {
         }
         return v;
     };
+    // a row's gate and statistics, read a row ahead
+    float gate_next = 1.0f, rp_next = 1.0f, rs_next = 0.0f;
+    auto scalars = [&](uint32_t row) {
+        if (row >= M) return;
+        if (p.gate) gate_next = p.gate[row];
+        if (p.rstd_post) rp_next = p.rstd_post[row];
+        if (p.dy) rs_next = p.rstd[row];
+    };
+    scalars(base0 + sub);
     int stage = 0, buf = 0;
     // (a group, or a warp with one row, is done at its own last row; lanes of several rows together)
     for (uint32_t base = base0; (WIDE || C > 1 ? base + sub : base) < M; base += stride) {
         const uint32_t row = base + sub;
         const bool in = row < M;
-        fill(stage ^ 1, row + stride);
-        const float gate = p.gate && in ? p.gate[row] : 1.0f;
-        const float rp = p.rstd_post && in ? p.rstd_post[row] : 1.0f;
-        const float rs = p.dy && in ? p.rstd[row] : 0.0f;
+        fill(stage == 0 ? S - 1 : stage - 1, row + (S - 1) * stride);
+        const float gate = gate_next, rp = rp_next, rs = rs_next;
+        scalars(row + stride);
         cp_async_wait<S - 1>();
         if constexpr (SHIFT) __syncwarp();
         const uint4* at = ring + stage * kStage;
@@ -519,7 +532,7 @@ bn_bwd_kernel(const BnBwd<T> p, int team) {
                 }
             }
         }
-        stage ^= 1;
+        stage = stage == S - 1 ? 0 : stage + 1;
         buf ^= 1;
         if constexpr (SHIFT) __syncwarp();
     }
@@ -575,7 +588,7 @@ cudaError_t launch_bn_bwd_as(BnBwd<T> p, int team, unsigned block, int most, int
     static DeviceTable<17> table;
     const auto kern = bn_bwd_kernel<T, C, WIDE, ALPHA, SHIFT>;
     const int warps = block / 32;
-    const size_t ring = size_t(kBnBwdStages) * (ALPHA ? 5 : 4) * C * warps * warp_slots(SHIFT, !WIDE && C == 1) * 16;
+    const size_t ring = size_t(bn_bwd_stages(ALPHA)) * (ALPHA ? 5 : 4) * C * warps * warp_slots(SHIFT, !WIDE && C == 1) * 16;
     const size_t sums = size_t(warps) * 2 * 32 * C * V * sizeof(float);
     const size_t smem = std::max(ring, sums);
     int n = 0;
