@@ -61,31 +61,188 @@ struct BnBwd {
 
 namespace {
 
-// Sum over the row of one value a thread: a team of lanes, or (CTA) all warps by one exchange
-// through `s` (16 floats), in a fixed order.
-template <bool CTA, bool PART>
-__device__ __forceinline__ float row_sum(float v, int team, float* s, int warp, int lane, int nw) {
-    v = team_sum<PART>(v, team);
-    if constexpr (CTA) {
-        if (lane == 0) s[warp] = v;
-        __syncthreads();
-        v = 0.0f;
-        for (int k = 0; k < nw; ++k) v += s[k];
-    }
+__device__ __forceinline__ uint32_t cluster_nctarank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
     return v;
 }
 
+// (a0, a1) -> a0 + a1
 __device__ __forceinline__ float fold(f32x2 v) {
     const float2 f = split(v);
     return f.x + f.y;
 }
 
-// The forward: one pass over rows of 16-byte pieces, from a ring of rows in shared memory.
+// A thread's columns.  On the 16-byte grid a thread has whole 16-byte pieces: piece t + 32 c
+// of its row, c < C, V columns each.  Off it (SHIFT) neither rows nor tensors of one row share an
+// alignment, and a thread has the 4-byte words of its range of columns that lie L lanes apart: pairs
+// of adjacent 2-byte columns, or single 4-byte ones.  The ring then holds the 16-byte granules that
+// a row touches, one after the other, and a word is cut from the two that it may lie across by one
+// funnel shift; reads are free of bank conflicts and stores whole words, shifted by one element
+// through the neighbouring lane where the row starts between two words.  (Cutting whole pieces from
+// two granules each, and joining them for the stores, took three times the instructions: forward
+// bf16 65536 x 1601 315 us, backward 451 us.)
+template <typename T, int C, bool SHIFT>
+struct Columns {
+    static constexpr int V = 16 / sizeof(T), H = V / 2;
+    int t, lanes, first, N;  // lane of the range, its lanes, its first column
+    // pair i of piece c: its first column, and how far its second one is
+    __device__ __forceinline__ int col(int c, int i) const {
+        if constexpr (!SHIFT) return first + (t + 32 * c) * V + 2 * i;
+        else if constexpr (sizeof(T) == 2) return first + 2 * (t + lanes * (c * H + i));
+        else return first + t + lanes * 2 * (c * H + i);
+    }
+    __device__ __forceinline__ int apart() const { return SHIFT && sizeof(T) == 4 ? lanes : 1; }
+    // whether the thread's piece c has columns of the row (on the grid: all or none of them)
+    __device__ __forceinline__ bool has(int c) const { return col(c, 0) < N; }
+    __device__ __forceinline__ bool has(int c, int i, int e) const { return col(c, i) + e * apart() < N; }
+
+    __device__ __forceinline__ void params(const Params<T>& w, int c, f32x2 (&v)[H]) const {
+        if constexpr (SHIFT) {
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                const int j = col(c, i), k = j + apart();
+                v[i] = pair_of(j < N ? w.at(j) : 0.0f, k < N ? w.at(k) : 0.0f);
+            }
+        } else {
+            load_params2<T, V, false>(w, col(c, 0), N, v);
+        }
+    }
+    // The copies of this thread of one row of a tensor into its range's slots at `to`.
+    __device__ __forceinline__ void fill(uint32_t to, const T* row) const {
+        if constexpr (SHIFT) {
+            const uint32_t mis = granule_offset(row);
+            const uint8_t* base = reinterpret_cast<const uint8_t*>(row) - mis;
+            const int begin = first * static_cast<int>(sizeof(T)), end = N * static_cast<int>(sizeof(T)) + static_cast<int>(mis);
+#pragma unroll
+            for (int c = 0; c <= C; ++c) {
+                const int g = c < C ? t + lanes * c : lanes * C, at = begin + g * 16;
+                if (c < C || t == lanes - 1) cp_async16_or_zero(to + g * 16, at < end ? base + at : base, at < end);
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                if (has(c)) cp_async16(to + (t + 32 * c) * 16, row + col(c, 0));
+        }
+    }
+    // Piece c from the slots; `row` for its alignment.  TAIL: columns behind the row are made 0.
+    __device__ __forceinline__ void read(const uint4* slots, const T* row, int c, bool tail, f32x2 (&v)[H]) const {
+        if constexpr (SHIFT) {
+            const uint32_t mis = granule_offset(row);
+            const uint32_t* words = reinterpret_cast<const uint32_t*>(slots) + (mis >> 2);
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                if constexpr (sizeof(T) == 2) {
+                    const uint32_t* w = words + t + lanes * (c * H + i);
+                    const uint32_t u = __funnelshift_r(w[0], w[1], (mis & 2) * 8);
+                    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+                        v[i] = pair_of(bf16lo_to_f32(u), bf16hi_to_f32(u));
+                    } else {
+                        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u));
+                        v[i] = pair_of(f.x, f.y);
+                    }
+                } else {
+                    const uint32_t* w = words + t + lanes * 2 * (c * H + i);
+                    v[i] = pair_of(__uint_as_float(w[0]), __uint_as_float(w[lanes]));
+                }
+                if (tail) {
+                    const float2 f = split(v[i]);
+                    v[i] = pair_of(has(c, i, 0) ? f.x : 0.0f, has(c, i, 1) ? f.y : 0.0f);
+                }
+            }
+        } else {
+            Piece<T, V> a;
+            a.raw = slots[t + 32 * c];
+            unpack2(a, v);
+        }
+    }
+    // Piece c, already rounded, to the row; `carry` goes from piece to piece.  All lanes call it; `in`: the
+    // row exists.
+    __device__ __forceinline__ void put(T* row, int c, uint4 q, uint32_t& carry, bool in) const {
+        if constexpr (!SHIFT) {
+            if (in && has(c)) st_v4(row + col(c, 0), q);
+            return;
+        }
+        const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (in && has(c, i / 2, i & 1)) reinterpret_cast<uint32_t*>(row)[col(c, i / 2) + (i & 1) * lanes] = u[i];
+        } else {
+            uint16_t* const out = reinterpret_cast<uint16_t*>(row);
+            const bool between = reinterpret_cast<uintptr_t>(row) & 2;  // (of a lane's own row)
+            const int lane = threadIdx.x & 31, from = (lane & ~(lanes - 1)) | ((t + lanes - 1) & (lanes - 1));
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                const int j = col(c, i), left = in ? N - j : -1;  // columns from this pair's first on
+                const uint32_t before = __shfl_sync(0xFFFFFFFFu, u[i], from);
+                if (!between) {
+                    if (left >= 2) *reinterpret_cast<uint32_t*>(out + j) = u[i];
+                    else if (left == 1) out[j] = static_cast<uint16_t>(u[i]);
+                } else {
+                    const uint32_t prev = t == 0 ? carry : before;
+                    const bool head = c == 0 && i == 0 && t == 0, last = c == C - 1 && i == H - 1 && t == lanes - 1;
+                    if (left >= 1) {
+                        if (head) out[j] = static_cast<uint16_t>(u[i]);
+                        else *reinterpret_cast<uint32_t*>(out + j - 1) = __funnelshift_r(prev, u[i], 16);
+                        if (last && left >= 2) out[j + 1] = static_cast<uint16_t>(u[i] >> 16);
+                    } else if (left == 0 && !head) {
+                        out[j - 1] = static_cast<uint16_t>(prev >> 16);
+                    }
+                }
+                carry = before;  // lane 0's: the range's last lane
+            }
+        }
+    }
+    // The codes of piece c of the rounded y, its magnitudes and saturations.
+    __device__ __forceinline__ void quant(const QuantOut& o, float s, uint8_t* row, int c, const Piece<T, V>& y, uint32_t& amax,
+                                          uint32_t& amax2, uint32_t& nsat) const {
+        if constexpr (SHIFT) {
+            float f[V];
+            y.unpack(f);
+            const float fmax = fp8_max_value(o.fmt);
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                const float v0 = __fmul_rn(f[2 * i], s), v1 = __fmul_rn(f[2 * i + 1], s);
+                const int j = col(c, i), k = j + apart();
+                const uint32_t q = cast_pair(v0, v1, o.fmt);
+                if (j < N) {
+                    amax = max(amax, __float_as_uint(fabsf(f[2 * i])));
+                    nsat += fabsf(v0) > fmax;
+                    if (row) row[j] = static_cast<uint8_t>(q);
+                }
+                if (k < N) {
+                    amax = max(amax, __float_as_uint(fabsf(f[2 * i + 1])));
+                    nsat += fabsf(v1) > fmax;
+                    if (row) row[k] = static_cast<uint8_t>(q >> 8);
+                }
+            }
+        } else {
+            uint8_t* dst = row ? row + col(c, 0) : nullptr;
+            if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+                if (o.fmt == FP8Q_E5M2) quant_bf16x8<FP8Q_E5M2>(s, y.raw, dst, amax2, nsat);
+                else quant_bf16x8<FP8Q_E4M3>(s, y.raw, dst, amax2, nsat);
+            } else {
+                quant_piece<T, V>(o, s, y, dst, V, true, amax, nsat);
+            }
+        }
+    }
+};
+
+// Slots of a warp's ring for one row of one tensor; rows: each team of lanes has a row of its own.
+__host__ __device__ constexpr int bn_slots(int C, bool shift, bool rows) { return !shift ? 32 * C : rows ? 64 : 32 * C + 1; }
+
+// The forward: one pass over rows, from a ring of S rows in shared memory.
 //   NARROW (CTA = false)  `team` lanes of a warp take a row, up to 64 columns a lane
 //   CTA                   a CTA of up to 512 threads takes a row, 32 columns a thread
 // The row stays in registers from its one read to its one write; its two sums of squares (of
 // the block's output, and of the stored stream) are team shuffles, or an exchange each.
-// Weights: in registers up to 32 columns a lane, in shared memory above.  S rows of the ring.
+// Weights: in registers up to 32 columns a lane, in shared memory above.
 template <typename T, int C, bool CTA, bool SHIFT, int S>
 __global__ void __launch_bounds__(CTA ? 512 : 128)
 bn_fwd_kernel(const BnFwd<T> p, int team) {
@@ -93,20 +250,14 @@ bn_fwd_kernel(const BnFwd<T> p, int team) {
     __shared__ float s_sum[2][2][16];
     constexpr int V = 16 / sizeof(T), H = V / 2;
     constexpr bool kHeld = C * V <= 32;
-    constexpr int kSlots = warp_slots(SHIFT, !CTA && C == 1), kStage = 2 * C * kSlots;
+    constexpr int kTensor = bn_slots(C, SHIFT, !CTA && C == 1), kStage = 2 * kTensor;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
     if constexpr (C > 1 || CTA) team = 32;
-    const int t = CTA ? warp * 32 * C + lane : lane & (team - 1);  // piece c of this thread is piece t + 32 c
-    const int N = static_cast<int>(p.N), pieces = (N + V - 1) / V;
+    const int N = static_cast<int>(p.N);
+    const Columns<T, C, SHIFT> my{lane & (team - 1), team, CTA ? warp * 32 * C * V : 0, N};
     const float inv_n = 1.0f / static_cast<float>(N);
     const f32x2 zero2 = pair_of(0.0f, 0.0f);
-    auto has = [&](int c) { return t + c * 32 < pieces; };
-    auto count = [&](int c) { return SHIFT ? min(V, N - (t + c * 32) * V) : V; };
-    uint4 carry = make_uint4(0, 0, 0, 0);
-    auto put = [&](uint4 q, T* start, int c, int valid) {
-        const bool head = c == 0 && (CTA ? lane : t) == 0, tail = t + c * 32 == pieces - 1 || (CTA && c == C - 1 && lane == 31);
-        store_shifted<T, true, true>(q, carry, start, t + c * 32, valid, head, tail);
-    };
+    uint32_t carry = 0;
     pdl_wait();
 
     // [w, wp][four columns of a piece][c][lane]
@@ -117,15 +268,15 @@ bn_fwd_kernel(const BnFwd<T> p, int team) {
         if constexpr (kHeld) {
 #pragma unroll
             for (int i = 0; i < H; ++i) w[c][i] = wp[c][i] = zero2;
-            if (has(c)) {
-                load_params2<T, V, SHIFT>(p.w, (t + c * 32) * V, N, w[c]);
-                load_params2<T, V, SHIFT>(p.wp, (t + c * 32) * V, N, wp[c]);
+            if (my.has(c)) {
+                my.params(p.w, c, w[c]);
+                my.params(p.wp, c, wp[c]);
             }
-        } else if (warp == c % 4 && has(c)) {
+        } else if (warp == c % 4 && my.has(c)) {
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 f32x2 f[H];
-                load_params2<T, V, SHIFT>(q ? p.wp : p.w, (t + c * 32) * V, N, f);
+                my.params(q ? p.wp : p.w, c, f);
 #pragma unroll
                 for (int i = 0; i < V / 4; ++i) {
                     const float2 a = split(f[2 * i]), b = split(f[2 * i + 1]);
@@ -155,36 +306,38 @@ bn_fwd_kernel(const BnFwd<T> p, int team) {
     const int rows_warp = CTA ? 1 : 32 / team, rows_cta = CTA ? 1 : rows_warp * nw;
     const uint32_t M = static_cast<uint32_t>(p.M), stride = gridDim.x * rows_cta, base0 = blockIdx.x * rows_cta;
     const uint32_t sub = CTA ? 0 : warp * rows_warp + lane / team;
-    uint4* const ring = s_ring + warp * (S * kStage) + lane + (SHIFT ? lane / team : 0);  // [stage][x, residual][c][slot]
-    const bool team_end = SHIFT && (CTA ? lane == 31 : t == team - 1);
+    // [stage][x, residual][slots], a team's from its own first slot
+    uint4* const ring = s_ring + warp * (S * kStage) + (lane / team) * (team * C + (SHIFT ? 1 : 0));
     const uint32_t ring_at = smem_u32(ring);
-    auto fill_tensor = [&](uint32_t to, const T* start) {
-        const uint32_t mis = SHIFT ? granule_offset(start) : 0;
-        const uint8_t* first = reinterpret_cast<const uint8_t*>(start) - mis;
-        const int end = N * static_cast<int>(sizeof(T)) + static_cast<int>(mis);
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-            if constexpr (SHIFT) copy_granules<false>(to + c * kSlots * 16, first, t + c * 32, end, team_end);
-            else if (has(c)) cp_async16(to + c * kSlots * 16, start + (t + c * 32) * V);
-        }
-    };
+    // (off the grid a range's last columns may lie behind the row; on it a piece has all or none)
+    auto tail = [&](int c) { return SHIFT && (CTA || c == C - 1); };
     auto fill = [&](int stage, uint32_t row) {  // nothing for a row past the last
         if (row < M) {
             const uint32_t to = ring_at + stage * kStage * 16;
-            fill_tensor(to, p.x + row * p.ldx);
-            if (p.res) fill_tensor(to + C * kSlots * 16, p.res + row * p.ld_res);
+            my.fill(to, p.x + row * p.ldx);
+            if (p.res) my.fill(to + kTensor * 16, p.res + row * p.ld_res);
         }
         cp_async_commit();
     };
     if constexpr (!SHIFT) {  // pieces past the row are zeros in every stage, and stay so
 #pragma unroll
         for (int c = 0; c < C; ++c)
-            if (!has(c))
-                for (int k = 0; k < S * 2; ++k) ring[(k * C + c) * kSlots] = make_uint4(0, 0, 0, 0);
+            if (!my.has(c))
+                for (int k = 0; k < S * 2; ++k) ring[k * kTensor + my.t + 32 * c] = make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int k = 0; k < S - 1; ++k) fill(k, base0 + sub + k * stride);
 
+    auto row_sum = [&](float v, float* sums) {  // in a fixed order
+        v = team_sum<C == 1 && !CTA>(v, team);
+        if constexpr (CTA) {
+            if (lane == 0) sums[warp] = v;
+            __syncthreads();
+            v = 0.0f;
+            for (int k = 0; k < nw; ++k) v += sums[k];
+        }
+        return v;
+    };
     float gate_next = 1.0f;  // read a row ahead
     if (p.gate && base0 + sub < M) gate_next = p.gate[base0 + sub];
     int stage = 0, buf = 0;
@@ -197,29 +350,21 @@ bn_fwd_kernel(const BnFwd<T> p, int team) {
         cp_async_wait<S - 1>();
         if constexpr (SHIFT) __syncwarp();
         const uint4* at = ring + stage * kStage;
-        const uint32_t mis_x = SHIFT ? granule_offset(p.x + row * p.ldx) : 0;
-        const uint32_t mis_r = SHIFT && p.res ? granule_offset(p.res + row * p.ld_res) : 0;
-        auto clip = [&](int c, f32x2 (&v)[H]) {
-            if constexpr (SHIFT) {
-                if (!has(c) || count(c) < V) zero_from<V>(v, has(c) ? count(c) : 0);
-            }
-        };
+        const T* const x_row = p.x + row * p.ldx;
+        const T* const res_row = p.res + row * p.ld_res;
         f32x2 v[C][H];
         f32x2 sq[2] = {zero2, zero2};
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            Piece<T, V> a;
-            a.raw = read_piece<T, SHIFT>(at + c * kSlots, mis_x);
-            unpack2(a, v[c]);
-            clip(c, v[c]);
+            my.read(at, x_row, c, tail(c), v[c]);
 #pragma unroll
             for (int i = 0; i < H; ++i) sq[i & 1] = fma2(v[c][i], v[c][i], sq[i & 1]);
         }
         float rp = 1.0f;
         if (p.post) {
-            const float sum = row_sum<CTA, C == 1 && !CTA>(fold(add2(sq[0], sq[1])), team, s_sum[buf][0], warp, lane, nw);
+            const float sum = row_sum(fold(add2(sq[0], sq[1])), s_sum[buf][0]);
             rp = 1.0f / sqrtf(__fmaf_rn(sum, inv_n, p.eps));
-            if (p.rstd_post && in && t == 0) p.rstd_post[row] = rp;
+            if (p.rstd_post && in && my.t + my.first == 0) p.rstd_post[row] = rp;
         }
         const f32x2 rp2 = pair_of(rp, rp), gate2 = pair_of(gate, gate), alpha2 = pair_of(alpha, alpha);
         sq[0] = sq[1] = zero2;
@@ -230,65 +375,52 @@ bn_fwd_kernel(const BnFwd<T> p, int team) {
 #pragma unroll
             for (int i = 0; i < H; ++i) v[c][i] = mul2(mul2(mul2(v[c][i], rp2), f[i]), gate2);
             if (p.res) {
-                Piece<T, V> a;
-                a.raw = read_piece<T, SHIFT>(at + (C + c) * kSlots, mis_r);
                 f32x2 r[H];
-                unpack2(a, r);
+                my.read(at + kTensor, res_row, c, tail(c), r);
 #pragma unroll
                 for (int i = 0; i < H; ++i) v[c][i] = fma2(alpha2, r[i], v[c][i]);
             }
             Piece<T, V> a;
             pack2(a, v[c]);
-            if (p.r_out) {
-                const int valid = in && has(c) ? count(c) : 0;
-                if constexpr (SHIFT) put(a.raw, p.r_out + row * p.ld_r, c, valid);
-                else if (valid) a.store(p.r_out + row * p.ld_r + (t + c * 32) * V);
-            }
+            if (p.r_out) my.put(p.r_out + row * p.ld_r, c, a.raw, carry, in);
             unpack2(a, v[c]);
-            if (!SHIFT && !has(c)) {
+            // (weights of columns behind the row are not set: 0 times them may be a NaN)
+            if constexpr (SHIFT) {
+                if (tail(c)) {
+#pragma unroll
+                    for (int i = 0; i < H; ++i) {
+                        const float2 e = split(v[c][i]);
+                        v[c][i] = pair_of(my.has(c, i, 0) ? e.x : 0.0f, my.has(c, i, 1) ? e.y : 0.0f);
+                    }
+                }
+            } else if (!my.has(c)) {
 #pragma unroll
                 for (int i = 0; i < H; ++i) v[c][i] = zero2;
             }
-            clip(c, v[c]);
 #pragma unroll
             for (int i = 0; i < H; ++i) sq[i & 1] = fma2(v[c][i], v[c][i], sq[i & 1]);
         }
         if (p.pre) {
-            const float sum = row_sum<CTA, C == 1 && !CTA>(fold(add2(sq[0], sq[1])), team, s_sum[buf][1], warp, lane, nw);
+            const float sum = row_sum(fold(add2(sq[0], sq[1])), s_sum[buf][1]);
             const float rstd = 1.0f / sqrtf(__fmaf_rn(sum, inv_n, p.eps));
-            if (p.rstd && in && t == 0) p.rstd[row] = rstd;
+            if (p.rstd && in && my.t + my.first == 0) p.rstd[row] = rstd;
             const f32x2 rstd2 = pair_of(rstd, rstd);
 #pragma unroll
             for (int c = 0; c < C; ++c) {
-                const int valid = in && has(c) ? count(c) : 0;
-                if (!SHIFT && valid == 0) continue;
+                if (!SHIFT && !(in && my.has(c))) continue;
                 f32x2 f[H];
                 weights(0, c, f);
 #pragma unroll
                 for (int i = 0; i < H; ++i) v[c][i] = mul2(mul2(v[c][i], rstd2), f[i]);
                 Piece<T, V> y;
                 pack2(y, v[c]);
-                if (p.y) {
-                    if constexpr (SHIFT) put(y.raw, p.y + row * p.ldy, c, valid);
-                    else y.store(p.y + row * p.ldy + (t + c * 32) * V);
-                }
-                if (p.quant.on && valid > 0) {
-                    uint8_t* dst = p.quant.q ? p.quant.q + row * p.N + (t + c * 32) * V : nullptr;
-                    const bool whole = !SHIFT || (valid == V && (reinterpret_cast<uintptr_t>(dst) & (V - 1)) == 0);
-                    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-                        if (whole) {
-                            if (p.quant.fmt == FP8Q_E5M2) quant_bf16x8<FP8Q_E5M2>(s, y.raw, dst, amax2, nsat);
-                            else quant_bf16x8<FP8Q_E4M3>(s, y.raw, dst, amax2, nsat);
-                            continue;
-                        }
-                    }
-                    quant_piece<T, V>(p.quant, s, y, dst, valid, whole, amax, nsat);
-                }
+                if (p.y) my.put(p.y + row * p.ldy, c, y.raw, carry, in);
+                if (p.quant.on && in) my.quant(p.quant, s, p.quant.q ? p.quant.q + row * p.N : nullptr, c, y, amax, amax2, nsat);
             }
         }
         stage = stage == S - 1 ? 0 : stage + 1;
         buf ^= 1;
-        if constexpr (SHIFT) __syncwarp();  // the granules that a neighbour read may be overwritten now
+        if constexpr (SHIFT) __syncwarp();  // the granules that other lanes read may be overwritten now
     }
     pdl_launch_dependents();
     cp_async_wait<0>();
@@ -300,7 +432,7 @@ cudaError_t launch_bn_fwd_as(const BnFwd<T>& p, int team, unsigned block, cudaSt
     constexpr int V = 16 / sizeof(T);
     static DeviceTable<17> table;
     const auto kern = bn_fwd_kernel<T, C, CTA, SHIFT, S>;
-    size_t smem = size_t(S) * 2 * C * (block / 32) * warp_slots(SHIFT, !CTA && C == 1) * 16;
+    size_t smem = size_t(S) * 2 * (block / 32) * bn_slots(C, SHIFT, !CTA && C == 1) * 16;
     if (C * V > 32) smem += size_t(2) * C * 32 * V * sizeof(float);
     int n = 0;
     const cudaError_t e = resident_ctas(table, kern, block, smem, kMaxRing, &n);
@@ -310,76 +442,69 @@ cudaError_t launch_bn_fwd_as(const BnFwd<T>& p, int team, unsigned block, cudaSt
     return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(block), smem, stream, p, team);
 }
 
-// The backward: `team` lanes of a warp (NARROW, up to 2 pieces a lane), or a group of warps
-// (WIDE, 2 pieces a lane) take a row; a CTA is several warps or groups.  A thread keeps its
-// columns' weights and sums for all its rows.
+// The backward.  A thread keeps its columns' weights and sums for all its rows.
+//   NARROW   `team` lanes of a warp take a row, up to 2 pieces a lane
+//   WIDE     a group of `team` warps takes a row; a CTA is several groups
+//   CLUSTER  the CTAs of a cluster take a row, all their warps one group; sums cross by
+//            distributed shared memory
 //     rhat = r rstd, g = dy w;  dr = dr_in + rstd (g - rhat sum(g rhat) / N)
 //     xhat = x rstd_post;       e = sum(dr wp xhat)
 //     dx = gate rstd_post (dr wp - xhat e / N)  [post],  gate dr wp  [not post]
 // The row's inputs come through a ring of rows in shared memory: three, or two where the
 // residual is read too.
+enum BnMode { BN_NARROW, BN_WIDE, BN_CLUSTER };
 constexpr int bn_bwd_stages(bool alpha) { return alpha ? 2 : 3; }
 enum { IN_DY, IN_R, IN_DR, IN_X, IN_RES };
 
-template <typename T, int C, bool WIDE, bool ALPHA, bool SHIFT>
+template <typename T, int C, BnMode MODE, bool ALPHA, bool SHIFT>
 __global__ void __launch_bounds__(512, 1)
 bn_bwd_kernel(const BnBwd<T> p, int team) {
     extern __shared__ uint4 s_ring[];
     __shared__ float s_sum[2][2][16];
     constexpr int V = 16 / sizeof(T), H = V / 2, S = bn_bwd_stages(ALPHA), TENSORS = ALPHA ? 5 : 4;
-    constexpr int kSlots = warp_slots(SHIFT, !WIDE && C == 1), kStage = TENSORS * C * kSlots;
+    constexpr bool kWarp = MODE == BN_NARROW;
+    constexpr int kTensor = bn_slots(C, SHIFT, kWarp && C == 1), kStage = TENSORS * kTensor;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-    // WIDE: team = warps of a group; otherwise lanes of a row
-    const int group = WIDE ? warp / team : warp, wg = WIDE ? warp - group * team : 0;
-    const int lanes = WIDE || C > 1 ? 32 : team;
-    const int t = WIDE ? wg * 32 * C + lane : lane & (lanes - 1);
-    const int N = static_cast<int>(p.N), pieces = (N + V - 1) / V;
+    const uint32_t rank = MODE == BN_CLUSTER ? cluster_ctarank() : 0, ctas = MODE == BN_CLUSTER ? cluster_nctarank() : 1;
+    if constexpr (MODE == BN_CLUSTER) team = nw;
+    // otherwise (NARROW) team = lanes of a row
+    const int group = kWarp ? warp : warp / team, wg = kWarp ? 0 : rank * nw + warp - group * team;
+    const int lanes = !kWarp || C > 1 ? 32 : team;
+    const int N = static_cast<int>(p.N);
+    const Columns<T, C, SHIFT> my{lane & (lanes - 1), lanes, wg * 32 * C * V, N};
+    const bool leads = my.t + my.first == 0;
     const float inv_n = 1.0f / static_cast<float>(N);
     const f32x2 zero2 = pair_of(0.0f, 0.0f);
-    auto has = [&](int c) { return t + c * 32 < pieces; };
-    auto count = [&](int c) { return SHIFT ? min(V, N - (t + c * 32) * V) : V; };
-    uint4 carry = make_uint4(0, 0, 0, 0);
-    auto put = [&](uint4 q, T* start, int c, int valid) {
-        const bool head = c == 0 && (WIDE ? lane : t) == 0, tail = t + c * 32 == pieces - 1 || (WIDE && c == C - 1 && lane == 31);
-        store_shifted<T, true, true>(q, carry, start, t + c * 32, valid, head, tail);
-    };
+    uint32_t carry = 0;
     pdl_wait();
     f32x2 w[C][H], wp[C][H], dw[C][H], dwp[C][H];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
 #pragma unroll
         for (int i = 0; i < H; ++i) w[c][i] = wp[c][i] = dw[c][i] = dwp[c][i] = zero2;
-        if (has(c)) {
-            load_params2<T, V, SHIFT>(p.w, (t + c * 32) * V, N, w[c]);
-            load_params2<T, V, SHIFT>(p.wp, (t + c * 32) * V, N, wp[c]);
+        if (my.has(c)) {
+            my.params(p.w, c, w[c]);
+            my.params(p.wp, c, wp[c]);
         }
     }
     const float alpha = p.alpha ? *p.alpha : 1.0f;
     f32x2 dalpha2 = zero2;
 
-    const int groups = WIDE ? nw / team : nw, rows_warp = WIDE ? 1 : 32 / lanes, rows_cta = groups * rows_warp;
-    const uint32_t M = static_cast<uint32_t>(p.M), stride = gridDim.x * rows_cta, base0 = blockIdx.x * rows_cta;
-    const uint32_t sub = group * rows_warp + (WIDE ? 0 : lane / lanes);
-    uint4* const ring = s_ring + warp * (S * kStage) + lane + (SHIFT && !WIDE ? lane / lanes : 0);
-    const bool team_end = SHIFT && (WIDE ? lane == 31 : t == lanes - 1);
+    const int groups = kWarp ? nw : nw / team, rows_warp = kWarp ? 32 / lanes : 1, rows_cta = groups * rows_warp;
+    const uint32_t M = static_cast<uint32_t>(p.M), block = blockIdx.x / ctas;
+    const uint32_t stride = gridDim.x / ctas * rows_cta, base0 = block * rows_cta;
+    const uint32_t sub = group * rows_warp + (kWarp ? lane / lanes : 0);
+    uint4* const ring = s_ring + warp * (S * kStage) + (lane / lanes) * (lanes * C + (SHIFT ? 1 : 0));
     const uint32_t ring_at = smem_u32(ring);
+    auto tail = [&](int c) { return SHIFT && (!kWarp || c == C - 1); };
     auto fill_tensor = [&](uint32_t to, const T* base, int64_t at) {
-        if (base == nullptr) return;
-        const T* start = base + at;
-        const uint32_t mis = SHIFT ? granule_offset(start) : 0;
-        const uint8_t* first = reinterpret_cast<const uint8_t*>(start) - mis;
-        const int end = N * static_cast<int>(sizeof(T)) + static_cast<int>(mis);
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-            if constexpr (SHIFT) copy_granules<false>(to + c * kSlots * 16, first, t + c * 32, end, team_end);
-            else if (has(c)) cp_async16(to + c * kSlots * 16, start + (t + c * 32) * V);
-        }
+        if (base) my.fill(to, base + at);
     };
     auto fill = [&](int stage, uint32_t row) {
         if (row < M) {
-            const uint32_t to = ring_at + stage * kStage * 16, step = C * kSlots * 16;
+            const uint32_t to = ring_at + stage * kStage * 16, step = kTensor * 16;
             fill_tensor(to + IN_DY * step, p.dy, row * p.ld_dy);
-            if (p.dy) fill_tensor(to + IN_R * step, p.r, row * p.ld_r);
+            fill_tensor(to + IN_R * step, p.r, row * p.ld_r);
             fill_tensor(to + IN_DR * step, p.dr, row * p.ld_dr);
             fill_tensor(to + IN_X * step, p.x, row * p.ldx);
             if constexpr (ALPHA) fill_tensor(to + IN_RES * step, p.res, row * p.ld_res);
@@ -389,19 +514,28 @@ bn_bwd_kernel(const BnBwd<T> p, int team) {
     if constexpr (!SHIFT) {
 #pragma unroll
         for (int c = 0; c < C; ++c)
-            if (!has(c))
-                for (int k = 0; k < S * TENSORS; ++k) ring[(k * C + c) * kSlots] = make_uint4(0, 0, 0, 0);
+            if (!my.has(c))
+                for (int k = 0; k < S * TENSORS; ++k) ring[k * kTensor + my.t + 32 * c] = make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int k = 0; k < S - 1; ++k) fill(k, base0 + sub + k * stride);
 
-    auto group_sum = [&](float v, float* s) {
-        v = team_sum<C == 1 && !WIDE>(v, lanes);
-        if constexpr (WIDE) {
-            if (lane == 0) s[warp] = v;
+    auto group_sum = [&](float v, float* sums) {  // in a fixed order
+        v = team_sum<C == 1 && kWarp>(v, lanes);
+        if constexpr (MODE == BN_WIDE) {
+            if (lane == 0) sums[warp] = v;
             named_barrier(1 + group, team * 32);
             v = 0.0f;
-            for (int k = 0; k < team; ++k) v += s[group * team + k];
+            for (int k = 0; k < team; ++k) v += sums[group * team + k];
+        }
+        if constexpr (MODE == BN_CLUSTER) {
+            if (lane == 0) sums[warp] = v;
+            cluster_sync_all();
+            // lane k adds warp k of every CTA, then the lanes are added
+            v = 0.0f;
+            if (lane < nw)
+                for (uint32_t r = 0; r < ctas; ++r) v += ld_cluster_f32(mapa_shared(smem_u32(sums + lane), r));
+            v = team_sum<false>(v, 32);
         }
         return v;
     };
@@ -416,7 +550,7 @@ bn_bwd_kernel(const BnBwd<T> p, int team) {
     scalars(base0 + sub);
     int stage = 0, buf = 0;
     // (a group, or a warp with one row, is done at its own last row; lanes of several rows together)
-    for (uint32_t base = base0; (WIDE || C > 1 ? base + sub : base) < M; base += stride) {
+    for (uint32_t base = base0; (!kWarp || C > 1 ? base + sub : base) < M; base += stride) {
         const uint32_t row = base + sub;
         const bool in = row < M;
         fill(stage == 0 ? S - 1 : stage - 1, row + (S - 1) * stride);
@@ -431,12 +565,7 @@ bn_bwd_kernel(const BnBwd<T> p, int team) {
                 for (int i = 0; i < H; ++i) v[i] = zero2;
                 return;
             }
-            Piece<T, V> a;
-            a.raw = read_piece<T, SHIFT>(at + (which * C + c) * kSlots, SHIFT ? granule_offset(base_p + off) : 0);
-            unpack2(a, v);
-            if constexpr (SHIFT) {
-                if (!has(c) || count(c) < V) zero_from<V>(v, has(c) ? count(c) : 0);
-            }
+            my.read(at + which * kTensor, base_p + off, c, tail(c), v);
         };
         f32x2 dr[C][H];
         // the norm before the next block
@@ -488,9 +617,7 @@ bn_bwd_kernel(const BnBwd<T> p, int team) {
                 for (int i = 0; i < H; ++i) f[i] = mul2(dr[c][i], alpha2);
                 Piece<T, V> a;
                 pack2(a, f);
-                const int valid = in && has(c) ? count(c) : 0;
-                if constexpr (SHIFT) put(a.raw, p.dres + row * p.ld_dres, c, valid);
-                else if (valid) a.store(p.dres + row * p.ld_dres + (t + c * 32) * V);
+                my.put(p.dres + row * p.ld_dres, c, a.raw, carry, in);
             }
         }
         // the block's output, its norm and its gate
@@ -511,7 +638,7 @@ bn_bwd_kernel(const BnBwd<T> p, int team) {
             float along = 0.0f;
             if (p.post || p.dgate) {
                 along = group_sum(fold(add2(acc[0], acc[1])), s_sum[buf][1]);
-                if (p.dgate && in && t == 0) p.dgate[row] = along;
+                if (p.dgate && in && leads) p.dgate[row] = along;
             }
             if (p.dx) {
                 const float a1 = p.post ? -along * inv_n : 0.0f;
@@ -526,9 +653,7 @@ bn_bwd_kernel(const BnBwd<T> p, int team) {
                     }
                     Piece<T, V> a;
                     pack2(a, f);
-                    const int valid = in && has(c) ? count(c) : 0;
-                    if constexpr (SHIFT) put(a.raw, p.dx + row * p.ld_dx, c, valid);
-                    else if (valid) a.store(p.dx + row * p.ld_dx + (t + c * 32) * V);
+                    my.put(p.dx + row * p.ld_dx, c, a.raw, carry, in);
                 }
             }
         }
@@ -539,65 +664,101 @@ bn_bwd_kernel(const BnBwd<T> p, int team) {
     cp_async_wait<0>();
     __syncthreads();
     pdl_launch_dependents();
-    if (p.part == nullptr) return;
-
-    // the CTA's sums in shared memory: [warp or group][dw, dwp][columns], added in order
-    float* const s_part = reinterpret_cast<float*>(s_ring);
-    const int columns = WIDE ? team * 32 * C * V : 32 * C * V;  // of a group's (warp's) lanes
+    if (p.part) {
+        // the CTA's sums in shared memory: [warp or group][dw, dwp][columns], added in order
+        float* const s_part = reinterpret_cast<float*>(s_ring);
+        const int columns = (kWarp ? 1 : team) * 32 * C * V, first = static_cast<int>(rank) * columns;
+        const int width = lanes * C * V, teams = kWarp ? 32 / lanes : 1;  // (several rows a warp: a team's columns)
+        float* const d = s_part + group * 2 * columns + (lane / lanes) * width - first;
 #pragma unroll
-    for (int c = 0; c < C; ++c)
+        for (int c = 0; c < C; ++c)
 #pragma unroll
-        for (int i = 0; i < H; ++i) {
-            const int at = ((WIDE ? wg * 32 * C : 0) + lane + c * 32) * V + 2 * i;
-            const float2 a = split(dw[c][i]), b = split(dwp[c][i]);
-            float* d = s_part + group * 2 * columns;
-            d[at] = a.x;
-            d[at + 1] = a.y;
-            d[columns + at] = b.x;
-            d[columns + at + 1] = b.y;
-        }
-    __syncthreads();
-    float* const out = p.part + int64_t(blockIdx.x) * 2 * p.N;
-    // (NARROW with several rows a warp: each team of lanes holds sums of all columns)
-    const int teams = WIDE ? 1 : 32 / lanes, width = WIDE || C > 1 ? columns : lanes * V;
-    for (int j = threadIdx.x; j < N; j += blockDim.x) {
-        float a = 0.0f, b = 0.0f;
-        for (int g = 0; g < groups; ++g)
-            for (int k = 0; k < teams; ++k) {
-                a += s_part[g * 2 * columns + k * width + j];
-                b += s_part[g * 2 * columns + columns + k * width + j];
+            for (int i = 0; i < H; ++i) {
+                const int j = my.col(c, i), k = j + my.apart();
+                const float2 a = split(dw[c][i]), b = split(dwp[c][i]);
+                d[j] = a.x;
+                d[k] = a.y;
+                d[columns + j] = b.x;
+                d[columns + k] = b.y;
             }
-        out[j] = a;
-        out[p.N + j] = b;
-    }
-    if constexpr (ALPHA) {
-        float a = team_sum<false>(fold(dalpha2), 32);
-        if (lane == 0) s_sum[0][0][warp] = a;
         __syncthreads();
-        if (threadIdx.x == 0) {
-            a = 0.0f;
-            for (int k = 0; k < nw; ++k) a += s_sum[0][0][k];
-            p.part[int64_t(p.parts) * 2 * p.N + blockIdx.x] = a;
+        float* const out = p.part + int64_t(block) * 2 * p.N;
+        for (int j = threadIdx.x; j < columns && first + j < N; j += blockDim.x) {
+            if (kWarp && j >= width) break;
+            float a = 0.0f, b = 0.0f;
+            for (int g = 0; g < groups; ++g)
+                for (int k = 0; k < teams; ++k) {
+                    a += s_part[g * 2 * columns + k * width + j];
+                    b += s_part[g * 2 * columns + columns + k * width + j];
+                }
+            out[first + j] = a;
+            out[p.N + first + j] = b;
+        }
+        if constexpr (ALPHA) {
+            float a = team_sum<false>(fold(dalpha2), 32);
+            if (lane == 0) s_sum[0][0][warp] = a;
+            if constexpr (MODE == BN_CLUSTER) cluster_sync_all();
+            else __syncthreads();
+            if (threadIdx.x == 0 && rank == 0) {
+                a = 0.0f;
+                for (uint32_t r = 0; r < ctas; ++r)
+                    for (int k = 0; k < nw; ++k)
+                        a += MODE == BN_CLUSTER ? ld_cluster_f32(mapa_shared(smem_u32(&s_sum[0][0][k]), r)) : s_sum[0][0][k];
+                p.part[int64_t(p.parts) * 2 * p.N + block] = a;
+            }
         }
     }
+    if constexpr (MODE == BN_CLUSTER) cluster_sync_all();  // the sums that another CTA reads stay until it has
 }
 
-template <typename T, int C, bool WIDE, bool ALPHA, bool SHIFT>
-cudaError_t launch_bn_bwd_as(BnBwd<T> p, int team, unsigned block, int most, int* parts, cudaStream_t stream) {
+template <typename T, int C, BnMode MODE, bool ALPHA, bool SHIFT>
+cudaError_t launch_bn_bwd_as(BnBwd<T> p, int team, unsigned block, int ctas, int most, int* parts, cudaStream_t stream) {
     constexpr int V = 16 / sizeof(T);
-    static DeviceTable<17> table;
-    const auto kern = bn_bwd_kernel<T, C, WIDE, ALPHA, SHIFT>;
+    const auto kern = bn_bwd_kernel<T, C, MODE, ALPHA, SHIFT>;
     const int warps = block / 32;
-    const size_t ring = size_t(bn_bwd_stages(ALPHA)) * (ALPHA ? 5 : 4) * C * warps * warp_slots(SHIFT, !WIDE && C == 1) * 16;
+    const size_t ring = size_t(bn_bwd_stages(ALPHA)) * (ALPHA ? 5 : 4) * warps * bn_slots(C, SHIFT, MODE == BN_NARROW && C == 1) * 16;
     const size_t sums = size_t(warps) * 2 * 32 * C * V * sizeof(float);
     const size_t smem = std::max(ring, sums);
-    int n = 0;
-    const cudaError_t e = resident_ctas(table, kern, block, smem, kMaxRing, &n);
-    if (e != cudaSuccess) return e;
-    const int64_t rows = WIDE ? warps / team : warps * (C > 1 ? 1 : 32 / team);
-    const int64_t grid = std::min<int64_t>(std::min<int64_t>((p.M + rows - 1) / rows, int64_t(n) * sm_count()), most);
-    p.parts = *parts = static_cast<int>(grid);
-    return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(block), smem, stream, p, team);
+    if constexpr (MODE == BN_CLUSTER) {
+        static DeviceTable<17 * 9> table;  // clusters that run at a time, by warps and CTAs of one
+        int device = 0, n = 0;
+        cudaError_t e = cudaGetDevice(&device);
+        if (e != cudaSuccess) return e;
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = ctas;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        cfg.gridDim = dim3(ctas * sm_count());
+        cfg.blockDim = dim3(block);
+        cfg.dynamicSmemBytes = smem;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = table.get(device, warps * 9 + ctas, &n, [&](int* clusters) {
+            cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxRing);
+            if (err == cudaSuccess) err = cudaOccupancyMaxActiveClusters(clusters, kern, &cfg);
+            return err;
+        });
+        if (e != cudaSuccess) return e;
+        if (n < 1) return cudaErrorNotSupported;
+        const int64_t grid = std::min<int64_t>(std::min<int64_t>(p.M, n), most);
+        p.parts = *parts = static_cast<int>(grid);
+        cfg.gridDim = dim3(static_cast<unsigned>(grid * ctas));
+        cfg.stream = stream;
+        cfg.numAttrs = 2;
+        return cudaLaunchKernelEx(&cfg, kern, p, team);
+    } else {
+        static DeviceTable<17> table;
+        int n = 0;
+        const cudaError_t e = resident_ctas(table, kern, block, smem, kMaxRing, &n);
+        if (e != cudaSuccess) return e;
+        const int64_t rows = MODE == BN_WIDE ? warps / team : warps * (C > 1 ? 1 : 32 / team);
+        const int64_t grid = std::min<int64_t>(std::min<int64_t>((p.M + rows - 1) / rows, int64_t(n) * sm_count()), most);
+        p.parts = *parts = static_cast<int>(grid);
+        return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(block), smem, stream, p, team);
+    }
 }
 
 }  // namespace
@@ -632,13 +793,18 @@ template <typename T, bool ALPHA, bool SHIFT>
 cudaError_t launch_bn_bwd(const BnBwd<T>& p, int most, int* parts, cudaStream_t stream) {
     constexpr int V = 16 / sizeof(T), kC = 2;  // pieces a lane
     const int64_t pieces = (p.N + V - 1) / V;
-    if (pieces <= 32) return launch_bn_bwd_as<T, 1, false, ALPHA, SHIFT>(p, team_of(pieces), 256, most, parts, stream);
-    if (pieces <= 32 * kC) return launch_bn_bwd_as<T, kC, false, ALPHA, SHIFT>(p, 32, 512, most, parts, stream);
-    const int64_t team = (pieces + 32 * kC - 1) / (32 * kC);
+    if (pieces <= 32) return launch_bn_bwd_as<T, 1, BN_NARROW, ALPHA, SHIFT>(p, team_of(pieces), 256, 1, most, parts, stream);
+    if (pieces <= 32 * kC) return launch_bn_bwd_as<T, kC, BN_NARROW, ALPHA, SHIFT>(p, 32, 512, 1, most, parts, stream);
+    const int64_t team = (pieces + 32 * kC - 1) / (32 * kC);  // warps of a row
     if (team <= 16) {
         const unsigned block = static_cast<unsigned>(16 / team * team) * 32;
-        return launch_bn_bwd_as<T, kC, true, ALPHA, SHIFT>(p, static_cast<int>(team), block, most, parts, stream);
+        return launch_bn_bwd_as<T, kC, BN_WIDE, ALPHA, SHIFT>(p, static_cast<int>(team), block, 1, most, parts, stream);
     }
+    for (int ctas = 2; ctas <= 8; ctas *= 2)  // (portable cluster sizes)
+        if (team <= 16 * ctas) {
+            const unsigned block = static_cast<unsigned>((team + ctas - 1) / ctas) * 32;
+            return launch_bn_bwd_as<T, kC, BN_CLUSTER, ALPHA, SHIFT>(p, 32, block, ctas, most, parts, stream);
+        }
     return cudaErrorNotSupported;
 }
 
