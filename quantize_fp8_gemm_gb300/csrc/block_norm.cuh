@@ -87,7 +87,9 @@ __device__ __forceinline__ float fold(f32x2 v) {
 // through the neighbouring lane where the row starts between two words.  (Cutting whole pieces from
 // two granules each, and joining them for the stores, took three times the instructions: forward
 // bf16 65536 x 1601 315 us, backward 451 us.)
-template <typename T, int C, bool SHIFT>
+// BRANCH: rows that start on a word are told from the others by a branch (forward bf16 65536 x 1601
+// 277 us without, 223 with; the backward, short of registers, 389 without and 437 with).
+template <typename T, int C, bool SHIFT, bool BRANCH>
 struct Columns {
     static constexpr int V = 16 / sizeof(T), H = V / 2;
     int t, lanes, first, N;  // lane of the range, its lanes, its first column
@@ -102,15 +104,59 @@ struct Columns {
     __device__ __forceinline__ bool has(int c) const { return col(c, 0) < N; }
     __device__ __forceinline__ bool has(int c, int i, int e) const { return col(c, i) + e * apart() < N; }
 
-    __device__ __forceinline__ void params(const Params<T>& w, int c, f32x2 (&v)[H]) const {
-        if constexpr (SHIFT) {
+    // The parameters of pieces c0 .. c0 + P - 1 (0 behind the row): every load is under way before the
+    // first is used.
+    template <int P>
+    __device__ __forceinline__ void params(const Params<T>& w, int c0, f32x2 (&v)[P][H]) const {
+        const float* const f = static_cast<const float*>(w.p);
+        const T* const h = static_cast<const T*>(w.p);
+        if (w.p == nullptr) {
 #pragma unroll
-            for (int i = 0; i < H; ++i) {
-                const int j = col(c, i), k = j + apart();
-                v[i] = pair_of(j < N ? w.at(j) : 0.0f, k < N ? w.at(k) : 0.0f);
+            for (int k = 0; k < P * H; ++k)
+                v[k / H][k % H] = pair_of(has(c0 + k / H, k % H, 0) ? w.none : 0.0f, has(c0 + k / H, k % H, 1) ? w.none : 0.0f);
+        } else if constexpr (!SHIFT) {  // (whole pieces of aligned vectors)
+            if (w.f32) {
+                float4 raw[P][V / 4];
+#pragma unroll
+                for (int k = 0; k < P * (V / 4); ++k) {
+                    const int c = k / (V / 4), i = k % (V / 4);
+                    raw[c][i] = has(c0 + c) ? __ldg(reinterpret_cast<const float4*>(f + col(c0 + c, 2 * i))) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                }
+#pragma unroll
+                for (int k = 0; k < P * (V / 4); ++k) {
+                    const float4 q = raw[k / (V / 4)][k % (V / 4)];
+                    v[k / (V / 4)][2 * (k % (V / 4))] = pair_of(q.x, q.y);
+                    v[k / (V / 4)][2 * (k % (V / 4)) + 1] = pair_of(q.z, q.w);
+                }
+            } else {
+                Piece<T, V> raw[P];
+#pragma unroll
+                for (int c = 0; c < P; ++c)
+                    raw[c].raw = has(c0 + c) ? __ldg(reinterpret_cast<const uint4*>(h + col(c0 + c, 0))) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int c = 0; c < P; ++c) unpack2(raw[c], v[c]);
             }
+        } else if (w.f32) {
+            float raw[P * H][2];
+#pragma unroll
+            for (int k = 0; k < P * H; ++k) {
+                const int c = c0 + k / H, i = k % H, j = col(c, i);
+                raw[k][0] = has(c, i, 0) ? __ldg(f + j) : 0.0f;
+                raw[k][1] = has(c, i, 1) ? __ldg(f + j + apart()) : 0.0f;
+            }
+#pragma unroll
+            for (int k = 0; k < P * H; ++k) v[k / H][k % H] = pair_of(raw[k][0], raw[k][1]);
         } else {
-            load_params2<T, V, false>(w, col(c, 0), N, v);
+            T raw[P * H][2];
+            const T zero = from_f32<T>(0.0f);
+#pragma unroll
+            for (int k = 0; k < P * H; ++k) {
+                const int c = c0 + k / H, i = k % H, j = col(c, i);
+                raw[k][0] = has(c, i, 0) ? h[j] : zero;
+                raw[k][1] = has(c, i, 1) ? h[j + apart()] : zero;
+            }
+#pragma unroll
+            for (int k = 0; k < P * H; ++k) v[k / H][k % H] = pair_of(to_f32(raw[k][0]), to_f32(raw[k][1]));
         }
     }
     // The copies of this thread of one row of a tensor into its range's slots at `to`.
@@ -130,31 +176,46 @@ struct Columns {
                 if (has(c)) cp_async16(to + (t + 32 * c) * 16, row + col(c, 0));
         }
     }
-    // Piece c from the slots; `row` for its alignment.  TAIL: columns behind the row are made 0.
+    // Whether the range ends behind the row (the same for all lanes).
+    __device__ __forceinline__ bool cut() const { return first + lanes * C * V > N; }
+    __device__ __forceinline__ static f32x2 unpack_word(uint32_t u) {
+        if constexpr (std::is_same<T, __half>::value) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u));
+            return pair_of(f.x, f.y);
+        } else {
+            return pair_of(bf16lo_to_f32(u), bf16hi_to_f32(u));
+        }
+    }
+    // Columns behind the row: 0.
+    __device__ __forceinline__ void clip(int c, f32x2 (&v)[H]) const {
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            const float2 f = split(v[i]);
+            v[i] = pair_of(has(c, i, 0) ? f.x : 0.0f, has(c, i, 1) ? f.y : 0.0f);
+        }
+    }
+    // Piece c from the slots; `row` for its alignment.  tail: columns behind the row are made 0.
     __device__ __forceinline__ void read(const uint4* slots, const T* row, int c, bool tail, f32x2 (&v)[H]) const {
         if constexpr (SHIFT) {
             const uint32_t mis = granule_offset(row);
-            const uint32_t* words = reinterpret_cast<const uint32_t*>(slots) + (mis >> 2);
+            const uint32_t* const words = reinterpret_cast<const uint32_t*>(slots) + (mis >> 2) + t;
+            if constexpr (sizeof(T) == 4) {
 #pragma unroll
-            for (int i = 0; i < H; ++i) {
-                if constexpr (sizeof(T) == 2) {
-                    const uint32_t* w = words + t + lanes * (c * H + i);
-                    const uint32_t u = __funnelshift_r(w[0], w[1], (mis & 2) * 8);
-                    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-                        v[i] = pair_of(bf16lo_to_f32(u), bf16hi_to_f32(u));
-                    } else {
-                        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u));
-                        v[i] = pair_of(f.x, f.y);
-                    }
-                } else {
-                    const uint32_t* w = words + t + lanes * 2 * (c * H + i);
+                for (int i = 0; i < H; ++i) {
+                    const uint32_t* w = words + lanes * 2 * (c * H + i);
                     v[i] = pair_of(__uint_as_float(w[0]), __uint_as_float(w[lanes]));
                 }
-                if (tail) {
-                    const float2 f = split(v[i]);
-                    v[i] = pair_of(has(c, i, 0) ? f.x : 0.0f, has(c, i, 1) ? f.y : 0.0f);
+            } else if (!BRANCH || (mis & 2)) {
+#pragma unroll
+                for (int i = 0; i < H; ++i) {
+                    const uint32_t* w = words + lanes * (c * H + i);
+                    v[i] = unpack_word(__funnelshift_r(w[0], w[1], (mis & 2) * 8));
                 }
+            } else {
+#pragma unroll
+                for (int i = 0; i < H; ++i) v[i] = unpack_word(words[lanes * (c * H + i)]);
             }
+            if (tail) clip(c, v);
         } else {
             Piece<T, V> a;
             a.raw = slots[t + 32 * c];
@@ -162,24 +223,31 @@ struct Columns {
         }
     }
     // Piece c, already rounded, to the row; `carry` goes from piece to piece.  All lanes call it; `in`: the
-    // row exists.
-    __device__ __forceinline__ void put(T* row, int c, uint4 q, uint32_t& carry, bool in) const {
+    // row exists; tail: the piece may end behind the row (always, where teams of lanes have rows of their own).
+    __device__ __forceinline__ void put(T* row, int c, uint4 q, uint32_t& carry, bool in, bool tail) const {
         if constexpr (!SHIFT) {
             if (in && has(c)) st_v4(row + col(c, 0), q);
             return;
         }
         const uint32_t u[4] = {q.x, q.y, q.z, q.w};
         if constexpr (sizeof(T) == 4) {
+            uint32_t* const out = reinterpret_cast<uint32_t*>(row);
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                if (in && has(c, i / 2, i & 1)) reinterpret_cast<uint32_t*>(row)[col(c, i / 2) + (i & 1) * lanes] = u[i];
+                if (in && (!tail || has(c, i / 2, i & 1))) out[col(c, i / 2) + (i & 1) * lanes] = u[i];
         } else {
             uint16_t* const out = reinterpret_cast<uint16_t*>(row);
-            const bool between = reinterpret_cast<uintptr_t>(row) & 2;  // (of a lane's own row)
+            const bool between = reinterpret_cast<uintptr_t>(row) & 2;  // the row starts between two words
+            if (!tail && !between) {
+#pragma unroll
+                for (int i = 0; i < H; ++i)
+                    if (in) *reinterpret_cast<uint32_t*>(out + col(c, i)) = u[i];
+                return;
+            }
             const int lane = threadIdx.x & 31, from = (lane & ~(lanes - 1)) | ((t + lanes - 1) & (lanes - 1));
 #pragma unroll
             for (int i = 0; i < H; ++i) {
-                const int j = col(c, i), left = in ? N - j : -1;  // columns from this pair's first on
+                const int j = col(c, i), left = !in ? -1 : tail ? N - j : 2;  // columns from this pair's first on
                 const uint32_t before = __shfl_sync(0xFFFFFFFFu, u[i], from);
                 if (!between) {
                     if (left >= 2) *reinterpret_cast<uint32_t*>(out + j) = u[i];
@@ -200,8 +268,8 @@ struct Columns {
         }
     }
     // The codes of piece c of the rounded y, its magnitudes and saturations.
-    __device__ __forceinline__ void quant(const QuantOut& o, float s, uint8_t* row, int c, const Piece<T, V>& y, uint32_t& amax,
-                                          uint32_t& amax2, uint32_t& nsat) const {
+    __device__ __forceinline__ void quant(const QuantOut& o, float s, uint8_t* row, int c, bool tail, const Piece<T, V>& y,
+                                          uint32_t& amax, uint32_t& amax2, uint32_t& nsat) const {
         if constexpr (SHIFT) {
             float f[V];
             y.unpack(f);
@@ -211,12 +279,12 @@ struct Columns {
                 const float v0 = __fmul_rn(f[2 * i], s), v1 = __fmul_rn(f[2 * i + 1], s);
                 const int j = col(c, i), k = j + apart();
                 const uint32_t q = cast_pair(v0, v1, o.fmt);
-                if (j < N) {
+                if (!tail || j < N) {
                     amax = max(amax, __float_as_uint(fabsf(f[2 * i])));
                     nsat += fabsf(v0) > fmax;
                     if (row) row[j] = static_cast<uint8_t>(q);
                 }
-                if (k < N) {
+                if (!tail || k < N) {
                     amax = max(amax, __float_as_uint(fabsf(f[2 * i + 1])));
                     nsat += fabsf(v1) > fmax;
                     if (row) row[k] = static_cast<uint8_t>(q >> 8);
@@ -254,51 +322,12 @@ bn_fwd_kernel(const BnFwd<T> p, int team) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
     if constexpr (C > 1 || CTA) team = 32;
     const int N = static_cast<int>(p.N);
-    const Columns<T, C, SHIFT> my{lane & (team - 1), team, CTA ? warp * 32 * C * V : 0, N};
+    const Columns<T, C, SHIFT, true> my{lane & (team - 1), team, CTA ? warp * 32 * C * V : 0, N};
     const float inv_n = 1.0f / static_cast<float>(N);
     const f32x2 zero2 = pair_of(0.0f, 0.0f);
     uint32_t carry = 0;
     pdl_wait();
 
-    // [w, wp][four columns of a piece][c][lane]
-    float4* const s_par = reinterpret_cast<float4*>(s_ring + nw * (S * kStage)) + lane;
-    f32x2 w[kHeld ? C : 1][H], wp[kHeld ? C : 1][H];
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-        if constexpr (kHeld) {
-#pragma unroll
-            for (int i = 0; i < H; ++i) w[c][i] = wp[c][i] = zero2;
-            if (my.has(c)) {
-                my.params(p.w, c, w[c]);
-                my.params(p.wp, c, wp[c]);
-            }
-        } else if (warp == c % 4 && my.has(c)) {
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                f32x2 f[H];
-                my.params(q ? p.wp : p.w, c, f);
-#pragma unroll
-                for (int i = 0; i < V / 4; ++i) {
-                    const float2 a = split(f[2 * i]), b = split(f[2 * i + 1]);
-                    s_par[((q * (V / 4) + i) * C + c) * 32] = make_float4(a.x, a.y, b.x, b.y);
-                }
-            }
-        }
-    }
-    if constexpr (!kHeld) __syncthreads();
-    auto weights = [&](int q, int c, f32x2 (&f)[H]) {
-        if constexpr (kHeld) {
-#pragma unroll
-            for (int i = 0; i < H; ++i) f[i] = q ? wp[c][i] : w[c][i];
-        } else {
-#pragma unroll
-            for (int i = 0; i < V / 4; ++i) {
-                const float4 v = s_par[((q * (V / 4) + i) * C + c) * 32];
-                f[2 * i] = pair_of(v.x, v.y);
-                f[2 * i + 1] = pair_of(v.z, v.w);
-            }
-        }
-    };
     const float s = p.quant.on ? *p.quant.scale : 0.0f;
     const float alpha = p.alpha ? *p.alpha : 1.0f;
     uint32_t amax = 0, amax2 = 0, nsat = 0;
@@ -310,7 +339,8 @@ bn_fwd_kernel(const BnFwd<T> p, int team) {
     uint4* const ring = s_ring + warp * (S * kStage) + (lane / team) * (team * C + (SHIFT ? 1 : 0));
     const uint32_t ring_at = smem_u32(ring);
     // (off the grid a range's last columns may lie behind the row; on it a piece has all or none)
-    auto tail = [&](int c) { return SHIFT && (CTA || c == C - 1); };
+    const bool cut = SHIFT && my.cut();
+    auto tail = [&](int c) { return SHIFT && (CTA ? cut : c == C - 1); };
     auto fill = [&](int stage, uint32_t row) {  // nothing for a row past the last
         if (row < M) {
             const uint32_t to = ring_at + stage * kStage * 16;
@@ -327,6 +357,42 @@ bn_fwd_kernel(const BnFwd<T> p, int team) {
     }
 #pragma unroll
     for (int k = 0; k < S - 1; ++k) fill(k, base0 + sub + k * stride);
+
+    // [w, wp][four columns of a piece][c][lane]
+    float4* const s_par = reinterpret_cast<float4*>(s_ring + nw * (S * kStage)) + lane;
+    f32x2 w[kHeld ? C : 1][H], wp[kHeld ? C : 1][H];
+    if constexpr (kHeld) {
+        my.params(p.w, 0, w);
+        my.params(p.wp, 0, wp);
+    } else {
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            if (warp != c % 4) continue;
+            f32x2 f[2][1][H];
+            my.params(p.w, c, f[0]);
+            my.params(p.wp, c, f[1]);
+#pragma unroll
+            for (int k = 0; k < 2 * (V / 4); ++k) {
+                const int q = k / (V / 4), i = k % (V / 4);
+                const float2 a = split(f[q][0][2 * i]), b = split(f[q][0][2 * i + 1]);
+                s_par[(k * C + c) * 32] = make_float4(a.x, a.y, b.x, b.y);
+            }
+        }
+        __syncthreads();
+    }
+    auto weights = [&](int q, int c, f32x2 (&f)[H]) {
+        if constexpr (kHeld) {
+#pragma unroll
+            for (int i = 0; i < H; ++i) f[i] = q ? wp[c][i] : w[c][i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < V / 4; ++i) {
+                const float4 v = s_par[((q * (V / 4) + i) * C + c) * 32];
+                f[2 * i] = pair_of(v.x, v.y);
+                f[2 * i + 1] = pair_of(v.z, v.w);
+            }
+        }
+    };
 
     auto row_sum = [&](float v, float* sums) {  // in a fixed order
         v = team_sum<C == 1 && !CTA>(v, team);
@@ -382,17 +448,11 @@ bn_fwd_kernel(const BnFwd<T> p, int team) {
             }
             Piece<T, V> a;
             pack2(a, v[c]);
-            if (p.r_out) my.put(p.r_out + row * p.ld_r, c, a.raw, carry, in);
+            if (p.r_out) my.put(p.r_out + row * p.ld_r, c, a.raw, carry, in, tail(c));
             unpack2(a, v[c]);
             // (weights of columns behind the row are not set: 0 times them may be a NaN)
             if constexpr (SHIFT) {
-                if (tail(c)) {
-#pragma unroll
-                    for (int i = 0; i < H; ++i) {
-                        const float2 e = split(v[c][i]);
-                        v[c][i] = pair_of(my.has(c, i, 0) ? e.x : 0.0f, my.has(c, i, 1) ? e.y : 0.0f);
-                    }
-                }
+                if (tail(c)) my.clip(c, v[c]);
             } else if (!my.has(c)) {
 #pragma unroll
                 for (int i = 0; i < H; ++i) v[c][i] = zero2;
@@ -414,8 +474,8 @@ bn_fwd_kernel(const BnFwd<T> p, int team) {
                 for (int i = 0; i < H; ++i) v[c][i] = mul2(mul2(v[c][i], rstd2), f[i]);
                 Piece<T, V> y;
                 pack2(y, v[c]);
-                if (p.y) my.put(p.y + row * p.ldy, c, y.raw, carry, in);
-                if (p.quant.on && in) my.quant(p.quant, s, p.quant.q ? p.quant.q + row * p.N : nullptr, c, y, amax, amax2, nsat);
+                if (p.y) my.put(p.y + row * p.ldy, c, y.raw, carry, in, tail(c));
+                if (p.quant.on && in) my.quant(p.quant, s, p.quant.q ? p.quant.q + row * p.N : nullptr, c, tail(c), y, amax, amax2, nsat);
             }
         }
         stage = stage == S - 1 ? 0 : stage + 1;
@@ -471,22 +531,12 @@ bn_bwd_kernel(const BnBwd<T> p, int team) {
     const int group = kWarp ? warp : warp / team, wg = kWarp ? 0 : rank * nw + warp - group * team;
     const int lanes = !kWarp || C > 1 ? 32 : team;
     const int N = static_cast<int>(p.N);
-    const Columns<T, C, SHIFT> my{lane & (lanes - 1), lanes, wg * 32 * C * V, N};
+    const Columns<T, C, SHIFT, false> my{lane & (lanes - 1), lanes, wg * 32 * C * V, N};
     const bool leads = my.t + my.first == 0;
     const float inv_n = 1.0f / static_cast<float>(N);
     const f32x2 zero2 = pair_of(0.0f, 0.0f);
     uint32_t carry = 0;
     pdl_wait();
-    f32x2 w[C][H], wp[C][H], dw[C][H], dwp[C][H];
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-#pragma unroll
-        for (int i = 0; i < H; ++i) w[c][i] = wp[c][i] = dw[c][i] = dwp[c][i] = zero2;
-        if (my.has(c)) {
-            my.params(p.w, c, w[c]);
-            my.params(p.wp, c, wp[c]);
-        }
-    }
     const float alpha = p.alpha ? *p.alpha : 1.0f;
     f32x2 dalpha2 = zero2;
 
@@ -519,6 +569,12 @@ bn_bwd_kernel(const BnBwd<T> p, int team) {
     }
 #pragma unroll
     for (int k = 0; k < S - 1; ++k) fill(k, base0 + sub + k * stride);
+
+    f32x2 w[C][H], wp[C][H], dw[C][H], dwp[C][H];
+    my.params(p.w, 0, w);
+    my.params(p.wp, 0, wp);
+#pragma unroll
+    for (int k = 0; k < C * H; ++k) dw[k / H][k % H] = dwp[k / H][k % H] = zero2;
 
     auto group_sum = [&](float v, float* sums) {  // in a fixed order
         v = team_sum<C == 1 && kWarp>(v, lanes);
@@ -617,7 +673,7 @@ bn_bwd_kernel(const BnBwd<T> p, int team) {
                 for (int i = 0; i < H; ++i) f[i] = mul2(dr[c][i], alpha2);
                 Piece<T, V> a;
                 pack2(a, f);
-                my.put(p.dres + row * p.ld_dres, c, a.raw, carry, in);
+                my.put(p.dres + row * p.ld_dres, c, a.raw, carry, in, tail(c));
             }
         }
         // the block's output, its norm and its gate
@@ -653,7 +709,7 @@ bn_bwd_kernel(const BnBwd<T> p, int team) {
                     }
                     Piece<T, V> a;
                     pack2(a, f);
-                    my.put(p.dx + row * p.ld_dx, c, a.raw, carry, in);
+                    my.put(p.dx + row * p.ld_dx, c, a.raw, carry, in, tail(c));
                 }
             }
         }
