@@ -503,7 +503,7 @@ cudaError_t launch_bn_fwd_as(const BnFwd<T>& p, int team, unsigned block, cudaSt
 }
 
 // The backward.  A thread keeps its columns' weights and sums for all its rows.
-//   NARROW   `team` lanes of a warp take a row, up to 2 pieces a lane
+//   NARROW   `team` lanes of a warp take a row, up to 3 pieces a lane
 //   WIDE     a group of `team` warps takes a row; a CTA is several groups
 //   CLUSTER  the CTAs of a cluster take a row, all their warps one group; sums cross by
 //            distributed shared memory
@@ -512,12 +512,16 @@ cudaError_t launch_bn_fwd_as(const BnFwd<T>& p, int team, unsigned block, cudaSt
 //     dx = gate rstd_post (dr wp - xhat e / N)  [post],  gate dr wp  [not post]
 // The row's inputs come through a ring of rows in shared memory: three, or two where the
 // residual is read too.
+// What bounds it: memory where the rows are on the grid and fill the lanes (bf16 65536 x 2048 239 us,
+// 1.00 of the measured copy rate; 131072 x 1600 400 us, 0.93; fp32 65536 x 1600 355 us, 1.04); off it the
+// instructions that cut words and shift them back (bf16 65536 x 1601 0.46); rows over a cluster (8192 x
+// 16384 417 us, 0.57) wait at the cluster's barriers for the stores before them.
 enum BnMode { BN_NARROW, BN_WIDE, BN_CLUSTER };
 constexpr int bn_bwd_stages(bool alpha) { return alpha ? 2 : 3; }
 enum { IN_DY, IN_R, IN_DR, IN_X, IN_RES };
 
 template <typename T, int C, BnMode MODE, bool ALPHA, bool SHIFT>
-__global__ void __launch_bounds__(512, 1)
+__global__ void __launch_bounds__(C >= 3 ? 256 : 512, 1)
 bn_bwd_kernel(const BnBwd<T> p, int team) {
     extern __shared__ uint4 s_ring[];
     __shared__ float s_sum[2][2][16];
@@ -852,6 +856,20 @@ cudaError_t launch_bn_bwd(const BnBwd<T>& p, int most, int* parts, cudaStream_t 
     if (pieces <= 32) return launch_bn_bwd_as<T, 1, BN_NARROW, ALPHA, SHIFT>(p, team_of(pieces), 256, 1, most, parts, stream);
     if (pieces <= 32 * kC) return launch_bn_bwd_as<T, kC, BN_NARROW, ALPHA, SHIFT>(p, 32, 512, 1, most, parts, stream);
     const int64_t team = (pieces + 32 * kC - 1) / (32 * kC);  // warps of a row
+    // Two-byte types: a warp a row up to 24 columns a lane (65536 x 768: 93 us, 111 in two warps of 16), and 32
+    // columns a lane where 16 would leave a seventh of the lanes idle (131072 x 1600: 400 us, 433) or make a whole
+    // CTA one group (8192 x 8192: 129, 142); where they fill the lanes 16 are better (65536 x 2048: 239, 252), and
+    // off the grid (65536 x 1601: 401, 457).
+    if constexpr (V == 8) {
+        if (pieces <= 96) return launch_bn_bwd_as<T, 3, BN_NARROW, ALPHA, SHIFT>(p, 32, 256, 1, most, parts, stream);
+        if constexpr (!SHIFT) {
+            const int64_t four = (pieces + 127) / 128;
+            if (four <= 8 && four * 2 <= team && (pieces * 20 < team * 64 * 17 || team > 8)) {
+                const unsigned block = static_cast<unsigned>(8 / four * four) * 32;
+                return launch_bn_bwd_as<T, 4, BN_WIDE, ALPHA, SHIFT>(p, static_cast<int>(four), block, 1, most, parts, stream);
+            }
+        }
+    }
     if (team <= 16) {
         const unsigned block = static_cast<unsigned>(16 / team * team) * 32;
         return launch_bn_bwd_as<T, kC, BN_WIDE, ALPHA, SHIFT>(p, static_cast<int>(team), block, 1, most, parts, stream);
