@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -513,36 +514,44 @@ def _dtype_code(t, name: str) -> int:
     return code
 
 
+# The checks below ask a good tensor as little as they can (an attribute is 70 to 100 ns on the Grace host, and a
+# call has a dozen tensors); what is wrong with a bad one is found out afterwards.
 def _rows(t, M: int, N: int, dtype, name: str):
     """(device pointer, row stride) of an optional [M,N] CUDA tensor of one type whose rows are N
     adjacent elements."""
     if t is None:
         return None, 0
+    try:
+        if t.is_cuda and t.dtype is dtype and t.shape == (M, N):
+            ld, inner = t.stride()
+            if M <= 1:
+                ld = N
+            if (inner == 1 or N == 1) and ld >= N:
+                return t.data_ptr(), ld
+            raise ValueError(f"{name} needs rows of adjacent elements that do not overlap (strides {(ld, inner)})")
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.shape != (M, N):
-        raise ValueError(f"{name} is {list(t.shape)}, the call needs {[M, N]}")
-    ld, inner = t.stride()
-    if M <= 1:
-        ld = N
-    if (inner != 1 and N > 1) or ld < N:
-        raise ValueError(f"{name} needs rows of adjacent elements that do not overlap (strides {(ld, inner)})")
-    return t.data_ptr(), ld
+    raise ValueError(f"{name} is {list(t.shape)}, the call needs {[M, N]}")
 
 
 def _vec(t, n: int, dtype, name: str):
     """Device pointer of an optional packed CUDA vector of n elements of one type."""
     if t is None:
         return None
+    try:
+        if t.is_cuda and t.dtype is dtype and t.numel() == n and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{name} must hold {n} packed elements")
-    return t.data_ptr()
+    raise ValueError(f"{name} must hold {n} packed elements")
 
 
 def _rng(t):
@@ -554,23 +563,38 @@ def _cell(t, dtype, name: str):
     """Device pointer of an optional CUDA tensor whose first element a call uses."""
     if t is None:
         return None
+    try:
+        if t.is_cuda and t.dtype is dtype and t.numel():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.numel() < 1:
-        raise ValueError(f"{name} is empty")
-    return t.data_ptr()
+    raise ValueError(f"{name} is empty")
 
 
 def _codes(t, n: int):
     """Device pointer of an optional packed CUDA tensor of n one-byte codes."""
     if t is None:
         return None
+    try:
+        if t.is_cuda and t.nbytes == n == t.numel() and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError("q_out must be a CUDA tensor")
-    if t.element_size() != 1 or t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"q_out must hold {n} packed one-byte codes")
+    raise ValueError(f"q_out must hold {n} packed one-byte codes")
+
+
+def _buffer(t):
+    """Device pointer of a packed CUDA workspace."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("workspace must be a CUDA tensor")
+    if not t.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     return t.data_ptr()
 
 
@@ -578,13 +602,17 @@ def _packed(t, rows: int, cols: int, dtype, name: str):
     """Device pointer of an optional packed [rows, cols] CUDA tensor of a type (None: one-byte codes)."""
     if t is None:
         return None
+    try:
+        if t.is_cuda and (t.dtype is dtype or dtype is None and t.element_size() == 1) and t.shape == (rows, cols) \
+                and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.element_size() != 1 if dtype is None else t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype or 'one-byte codes'}, not {t.dtype}")
-    if t.shape != (rows, cols) or not t.is_contiguous():
-        raise ValueError(f"{name} must be packed {[rows, cols]}, not {list(t.shape)} with strides {t.stride()}")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be packed {[rows, cols]}, not {list(t.shape)} with strides {t.stride()}")
 
 
 def _here(t, name: str) -> None:
@@ -697,6 +725,12 @@ class BlockNormBwdArgs(ctypes.Structure):
                 ("post_norm", ctypes.c_int), ("flags", ctypes.c_uint)]
 
 
+# the two structs as bytes: a third of the time that a ctypes structure takes to fill
+_block_norm = struct.Struct("@qqiiPqPqPqPqPPPPPPPPPPfiiI")
+_block_norm_bwd = struct.Struct("@qqiiPqPqPqPqPqPqPqPPPPPPPPPPPniI")
+assert _block_norm.size == ctypes.sizeof(BlockNormArgs) and _block_norm_bwd.size == ctypes.sizeof(BlockNormBwdArgs)
+
+
 def block_norm_fwd(x: torch.Tensor, weight, y, *, eps: float = 1e-5, rstd=None, residual=None, alpha=None, gate=None,
                    post_weight=None, post_norm: bool = False, rstd_post=None, r_out=None, fmt: int = E4M3, scale=None,
                    q_out=None, amax_out=None, sat_count=None, flags: int = 0, stream=None) -> None:
@@ -714,13 +748,16 @@ def block_norm_fwd(x: torch.Tensor, weight, y, *, eps: float = 1e-5, rstd=None, 
     py, ldy = _rows(y, M, N, dtype, "y")
     pcode, ptype = _param_code(x, weight, post_weight, code)
     f32 = torch.float32
-    a = BlockNormArgs(
-        M, N, code, pcode, px, ldx, pres, ldres, pr, ldr, py, ldy, _vec(weight, N, ptype, "weight"),
-        _vec(post_weight, N, ptype, "post_weight"), _vec(gate, M, f32, "gate"), _cell(alpha, f32, "alpha"),
-        _vec(rstd, M, f32, "rstd"), _vec(rstd_post, M, f32, "rstd_post"), _cell(scale, f32, "scale"),
-        _codes(q_out, M * N), _cell(amax_out, f32, "amax_out"), _cell(sat_count, torch.int64, "sat_count"), eps, fmt,
-        bool(post_norm), flags)
-    _check("block_norm_fwd", lib().block_norm_fwd(ctypes.byref(a), _stream(stream)))
+    args = _block_norm.pack(
+        M, N, code, pcode, px or 0, ldx, pres or 0, ldres, pr or 0, ldr, py or 0, ldy,
+        0 if weight is None else _vec(weight, N, ptype, "weight"),
+        0 if post_weight is None else _vec(post_weight, N, ptype, "post_weight"),
+        0 if gate is None else _vec(gate, M, f32, "gate"), 0 if alpha is None else _cell(alpha, f32, "alpha"),
+        0 if rstd is None else _vec(rstd, M, f32, "rstd"), 0 if rstd_post is None else _vec(rstd_post, M, f32, "rstd_post"),
+        0 if scale is None else _cell(scale, f32, "scale"), 0 if q_out is None else _codes(q_out, M * N),
+        0 if amax_out is None else _cell(amax_out, f32, "amax_out"),
+        0 if sat_count is None else _cell(sat_count, torch.int64, "sat_count"), eps, fmt, bool(post_norm), flags)
+    _check("block_norm_fwd", lib().block_norm_fwd(args, _stream(stream)))
 
 
 def block_norm_bwd_workspace_bytes(M: int, N: int) -> int:
@@ -747,14 +784,17 @@ def block_norm_bwd(dy, r, rstd, weight, *, dr=None, x=None, residual=None, alpha
     pdx, lddx = _rows(dx, M, N, dtype, "dx")
     pcode, ptype = _param_code(first, weight, post_weight, code)
     f32 = torch.float32
-    a = BlockNormBwdArgs(
-        M, N, code, pcode, pdy, lddy, pr, ldr, pdr, lddr, px, ldx, pres, ldres, pdres, lddres, pdx, lddx,
-        _vec(weight, N, ptype, "weight"), _vec(post_weight, N, ptype, "post_weight"), _vec(gate, M, f32, "gate"),
-        _cell(alpha, f32, "alpha"), _vec(rstd, M, f32, "rstd"), _vec(rstd_post, M, f32, "rstd_post"),
-        _vec(dweight, N, f32, "dweight"), _vec(dpost_weight, N, f32, "dpost_weight"), _vec(dgate, M, f32, "dgate"),
-        _cell(dalpha, f32, "dalpha"), _ptr(workspace, None, "workspace"),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), bool(post_norm), flags)
-    _check("block_norm_bwd", lib().block_norm_bwd(ctypes.byref(a), _stream(stream)))
+    args = _block_norm_bwd.pack(
+        M, N, code, pcode, pdy or 0, lddy, pr or 0, ldr, pdr or 0, lddr, px or 0, ldx, pres or 0, ldres, pdres or 0, lddres,
+        pdx or 0, lddx, 0 if weight is None else _vec(weight, N, ptype, "weight"),
+        0 if post_weight is None else _vec(post_weight, N, ptype, "post_weight"),
+        0 if gate is None else _vec(gate, M, f32, "gate"), 0 if alpha is None else _cell(alpha, f32, "alpha"),
+        0 if rstd is None else _vec(rstd, M, f32, "rstd"), 0 if rstd_post is None else _vec(rstd_post, M, f32, "rstd_post"),
+        0 if dweight is None else _vec(dweight, N, f32, "dweight"),
+        0 if dpost_weight is None else _vec(dpost_weight, N, f32, "dpost_weight"),
+        0 if dgate is None else _vec(dgate, M, f32, "dgate"), 0 if dalpha is None else _cell(dalpha, f32, "dalpha"),
+        0 if workspace is None else _buffer(workspace), 0 if workspace is None else workspace.nbytes, bool(post_norm), flags)
+    _check("block_norm_bwd", lib().block_norm_bwd(args, _stream(stream)))
 
 
 # -- the gated feed-forward block --
