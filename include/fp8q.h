@@ -788,7 +788,8 @@ int dropout_bwd(const void* dy, int64_t ld_dy, void* dx, int64_t ld_dx, int64_t 
  * single linear layer (fp8_gemm_wgrad, fp8_gemm_dgrad on the [M,2F] gradient).
  * act is an fp8q_act:  SiLU g / (1 + exp(-g));  GELU in its tanh form,
  * g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2;  the others as above, with
- * the derivative 0 of ReLU and ReLU^2 at 0.
+ * the derivative 0 of ReLU and ReLU^2 at 0.  (1 / (1 + exp(-z)) counts as 0
+ * where it is below 2^-126: z < -87.)
  */
 
 /*

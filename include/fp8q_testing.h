@@ -47,6 +47,17 @@ int fp8q_gemm_set_tile(int pair, int bn);
 int fp8q_mx_set_tile(int pair, int bn);
 
 /*
+ * fp8q_glu_set_tile -- pin the tile of fp8_glu_fwd and fp8_gemm_dgrad_glu (a
+ * tuning knob), or (-1, 0) for the automatic choice (the default):
+ *   pair  0: one CTA per tile of 128 rows x bn accumulator columns, bn in {64, 128, 192, 256}
+ *         1: a CTA pair per 256 rows, bn in {128, 192, 256}; taken by calls of more
+ *            than 128 rows, others choose automatically
+ * (The forward's bn / 2 output columns take bn accumulator columns.)
+ * Returns FP8Q_ERR_UNSUPPORTED for any other combination (nothing changes).
+ */
+int fp8q_glu_set_tile(int pair, int bn);
+
+/*
  * fp8q_gemm_test_hold_loads -- failure-path hook.  While on != 0, the GEMM
  * kernels launched afterwards issue no operand loads, so their first bounded
  * wait runs out (after about 2 s): the kernel ORs FP8Q_DEV_TIMEOUT into the

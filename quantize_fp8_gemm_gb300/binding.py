@@ -87,6 +87,8 @@ def lib() -> ctypes.CDLL:
         L.fp8q_test_noalloc_fill.restype = i32
         L.fp8q_mx_set_tile.argtypes = [i32, i32]
         L.fp8q_mx_set_tile.restype = i32
+        L.fp8q_glu_set_tile.argtypes = [i32, i32]
+        L.fp8q_glu_set_tile.restype = i32
         L.fp8_quant_mx.argtypes = [P, i64, i64, i32, i32, P, P, P, P, P, P, P, P]
         L.fp8_gemm_mx.argtypes = [P, P, P, P, P, i64, i64, i64, i32, i32, P, P]
         L.fp8_mx_scale_bytes.argtypes = [i64, i64]
@@ -876,6 +878,11 @@ def fp8q_gemm_test_hold_loads(on: bool) -> None:
 def fp8q_mx_set_tile(pair: int, bn: int = 0) -> None:
     """Pin fp8_gemm_mx's tile: pair 0/1, width 128 or 256; (0, 0) = automatic."""
     _check("fp8q_mx_set_tile", lib().fp8q_mx_set_tile(int(pair), int(bn)))
+
+
+def fp8q_glu_set_tile(pair: int, bn: int = 0) -> None:
+    """Pin the tile of the gated kernels (pair = -1: the automatic choice)."""
+    _check("fp8q_glu_set_tile", lib().fp8q_glu_set_tile(pair, bn))
 
 
 def fp8q_test_set_fused_grid(ctas: int) -> None:

@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(512) bn_fwd_loop_kernel(const BnFwd<T> p) {
         }
     }
     pdl_launch_dependents();
-    if (p.quant.on) publish_quant(p.quant, amax, nsat);
+    finish_quant(p, amax, nsat);
 }
 
 // The stream's gradient at one element, `along` = sum(g rhat) / N.
@@ -224,6 +224,7 @@ int run_bn_fwd(const fp8q_block_norm_args& a, const QuantOut& quant, cudaStream_
     p.post = a.post_norm != 0;
     p.pre = a.y || quant.on || a.rstd;
     p.quant = quant;
+    p.alone = a.M == 1 && !(a.flags & FP8Q_ACCUMULATE);  // (one row is one CTA)
     constexpr int V = 16 / sizeof(T);
     const bool grid16 = a.N % V == 0 && rows16(a.x, a.ldx, sizeof(T)) && rows16(a.residual, a.ld_residual, sizeof(T)) &&
                         rows16(a.r_out, a.ld_r, sizeof(T)) && rows16(a.y, a.ldy, sizeof(T)) && aligned16(a.weight) &&
@@ -326,7 +327,7 @@ extern "C" int block_norm_fwd(const fp8q_block_norm_args* args, cudaStream_t str
         !aligned_to(a.sat_count, 8))
         return FP8Q_ERR_ALIGN;
     if (!device_is_sm103()) return FP8Q_ERR_UNSUPPORTED;
-    if (!(a.flags & FP8Q_ACCUMULATE) && (a.amax_out || a.sat_count)) {
+    if (!(a.flags & FP8Q_ACCUMULATE) && (a.amax_out || a.sat_count) && a.M != 1) {
         if (launch_pdl(clear_quant_kernel, dim3(1), dim3(1), 0, stream, a.amax_out, a.sat_count) != cudaSuccess) {
             (void)cudaGetLastError();
             return FP8Q_ERR_CUDA;

@@ -28,6 +28,7 @@ struct BnFwd {
     float* rstd_post;
     float eps;
     bool post, pre;        // norm after the block, norm before the next one
+    bool alone;            // one CTA, whose maximum and count are the call's: stored, not added
     QuantOut quant;
 };
 
@@ -76,6 +77,31 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr) {
 __device__ __forceinline__ float fold(f32x2 v) {
     const float2 f = split(v);
     return f.x + f.y;
+}
+
+// The maximum and count of a call's only CTA: stored, so that nothing has to clear them first.
+__device__ __forceinline__ void store_quant(const QuantOut& o, uint32_t amax, uint32_t nsat) {
+    __shared__ uint32_t s_amax[16], s_sat[16];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    amax = __reduce_max_sync(0xFFFFFFFFu, amax);
+    nsat = __reduce_add_sync(0xFFFFFFFFu, nsat);
+    if (lane == 0) {
+        s_amax[warp] = amax;
+        s_sat[warp] = nsat;
+    }
+    __syncthreads();
+    if (warp != 0) return;
+    amax = __reduce_max_sync(0xFFFFFFFFu, lane < nw ? s_amax[lane] : 0u);
+    nsat = __reduce_add_sync(0xFFFFFFFFu, lane < nw ? s_sat[lane] : 0u);
+    if (lane != 0) return;
+    if (o.amax) *o.amax = __uint_as_float(amax);
+    if (o.sat) *o.sat = nsat;
+}
+template <typename T>
+__device__ __forceinline__ void finish_quant(const BnFwd<T>& p, uint32_t amax, uint32_t nsat) {
+    if (!p.quant.on) return;
+    if (p.alone) store_quant(p.quant, amax, nsat);
+    else publish_quant(p.quant, amax, nsat);
 }
 
 // A thread's columns.  On the 16-byte grid a thread has whole 16-byte pieces: piece t + 32 c
@@ -484,7 +510,7 @@ bn_fwd_kernel(const BnFwd<T> p, int team) {
     }
     pdl_launch_dependents();
     cp_async_wait<0>();
-    if (p.quant.on) publish_quant(p.quant, max(amax, max16x2(amax2) << 16), nsat);
+    finish_quant(p, max(amax, max16x2(amax2) << 16), nsat);
 }
 
 template <typename T, int C, bool CTA, bool SHIFT, int S = 3>

@@ -32,8 +32,10 @@
 #include "glu_ops.cuh"
 #include "norm_ops.cuh"
 #include "quant_ops.cuh"
+#include "../../include/fp8q_testing.h"
 
 #include <algorithm>
+#include <atomic>
 
 namespace fp8q {
 
@@ -66,6 +68,7 @@ struct GluArgs {
     int64_t M, F, K;
     uint32_t idesc;
     int act;
+    uint32_t a_bytes;  // of a CTA's box of A: of a call of less than 128 rows the rows that there are
     bool wide_bf, wide_q;  // every 16 columns of h, o and d (32 of q) of a row are one 32-byte sector
 };
 
@@ -307,7 +310,7 @@ glu_kernel(const __grid_constant__ GluMaps maps, const GluArgs p) {
                         tma_load_2d_pair(sb, &maps.b, fb, kb * BK, row);
                     } else {
                         const uint32_t fb = smem_u32(&full[stage]);
-                        mbar_arrive_expect_tx(fb, C::TX_BYTES);
+                        mbar_arrive_expect_tx(fb, C::TX_BYTES - C::A_BYTES + p.a_bytes);
                         tma_load_2d(sa, &maps.a, fb, kb * BK, m0);
                         tma_load_2d(sb, &maps.b, fb, kb * BK, n0);
                         if constexpr (!BWD) tma_load_2d(sb + C::B_BOX * BK, &maps.b, fb, kb * BK, up);
@@ -445,7 +448,7 @@ glu_kernel(const __grid_constant__ GluMaps maps, const GluArgs p) {
                         uint32_t g[16], u[16], a[8];
                         tmem_ld_2x16_sync(taddr + c * 32 + half * 16, taddr + C::OUT + c * 32 + half * 16, g, u);
                         if (half == 1 && last) release();
-                        if (half == 1 && !whole) {  // (the accumulator's next columns are not the gate's)
+                        if ((half == 1 && !whole) || !in) {  // (not the gate's columns; no rows of x)
 #pragma unroll
                             for (int j = 0; j < 16; ++j) g[j] = u[j] = 0;
                         }
@@ -471,6 +474,10 @@ glu_kernel(const __grid_constant__ GluMaps maps, const GluArgs p) {
                         uint32_t r[16], g[8], u[8], dg[8], du[8];
                         tmem_ld_x16_sync(taddr + c * 32 + half * 16, r);
                         if (half == 1 && last) release();
+                        if (!in) {  // (no rows of dY: g and u are zeros, but NaN times zero is none)
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) r[j] = 0;
+                        }
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
                             const int at = ((2 * half + k) ^ ((lane >> 1) & 3)) << 4;
@@ -589,7 +596,11 @@ int launch_glu(GluArgs p, cudaStream_t stream) {
     }
     const int64_t M = p.M, F = p.F;
     alignas(64) GluMaps maps;
-    if (!make_kmajor_map(&maps.a, p.x, M, p.K, BM) || !make_kmajor_map(&maps.b, p.w, BWD ? F : 2 * F, p.K, C::B_BOX))
+    // a call of fewer rows than a tile copies those alone, to whole swizzle atoms (16 x 1600 -> 6400: filling the
+    // other rows with zeros took 3 us of 11); what the other rows' accumulators hold is not used
+    const int a_rows = !PAIR && M < BM ? static_cast<int>((M + 7) / 8 * 8) : BM;
+    p.a_bytes = static_cast<uint32_t>(a_rows * BK);
+    if (!make_kmajor_map(&maps.a, p.x, M, p.K, a_rows) || !make_kmajor_map(&maps.b, p.w, BWD ? F : 2 * F, p.K, C::B_BOX))
         return FP8Q_ERR_CUDA;
     maps.h0 = maps.h1 = maps.a;
     if (BWD && (!make_half_map(&maps.h0, p.h, M, F) || !make_half_map(&maps.h1, p.h + F, M, F))) return FP8Q_ERR_CUDA;
@@ -617,20 +628,32 @@ int launch_glu(GluArgs p, cudaStream_t stream) {
     return FP8Q_OK;
 }
 
-// The tile, scored as gemm.cu scores its own: waves x a tile's relative time.
+// The tile: the one of the least estimated time  c + waves (e + m K / 1000)  in us, where waves are
+// the tiles over the CTAs (pairs) that run at a time, rounded up; c, e and m are fits to the seven
+// tiles' times over nine shapes a direction (128 to 16384 rows, 256 x 1024 to 1600 x 6400; within 15 %
+// each).  A tile's time depends on its width less than on K, and wide tiles lose more to a last wave that
+// is not full: 8192 x 768 -> 2048 backward is 38 us in 128-wide pair tiles, 42 in 256-wide ones; 8192 x
+// 1600 -> 6400 109 in 256-wide ones and 125 in 128.
+std::atomic<int> g_glu_tile{-1};  // fp8q_glu_set_tile: -1 = by the estimate, else (pair << 16) | bn
+
 template <bool BWD>
 int dispatch_glu(const GluArgs& p, cudaStream_t stream) {
-    struct Cand { bool pair; int bn; double t; };
-    static constexpr Cand kCands[] = {{true, 256, 1.000}, {true, 192, 0.909}, {true, 128, 0.858},
-                                      {false, 256, 1.102}, {false, 192, 0.897}, {false, 128, 0.843}, {false, 64, 0.750}};
+    struct Cand { bool pair; int bn; double c, e, m; };
+    static constexpr Cand kForward[] = {{true, 256, 3.99, 3.72, 1.22}, {true, 192, 4.56, 2.64, 1.25}, {true, 128, 3.85, 1.33, 1.64},
+                                        {false, 256, 3.87, 3.37, 2.23}, {false, 192, 4.14, 2.42, 1.93},
+                                        {false, 128, 3.76, 1.46, 1.68}, {false, 64, 3.37, 0.73, 1.90}};
+    static constexpr Cand kBackward[] = {{true, 256, 7.55, 7.36, 1.35}, {true, 192, 7.34, 5.83, 1.08}, {true, 128, 5.64, 3.76, 1.16},
+                                         {false, 256, 6.91, 6.97, 1.99}, {false, 192, 6.22, 6.41, 1.47},
+                                         {false, 128, 4.88, 4.35, 0.98}, {false, 64, 4.12, 2.73, 1.15}};
     const int64_t sms = sm_count();
-    Cand best = kCands[5];
+    Cand best = (BWD ? kBackward : kForward)[5];
     double best_cost = -1.0;
-    for (const Cand& c : kCands) {
+    for (const Cand& c : BWD ? kBackward : kForward) {
         if (c.pair && p.M <= BM) continue;
         const int64_t tile_m = c.pair ? 2 * BM : BM, units = c.pair ? sms / 2 : sms, out = BWD ? c.bn : c.bn / 2;
         const int64_t tiles = ((p.M + tile_m - 1) / tile_m) * ((p.F + out - 1) / out);
-        const double cost = static_cast<double>((tiles + units - 1) / units) * c.t;
+        const double cost = c.c + static_cast<double>((tiles + units - 1) / units) * (c.e + c.m * 1e-3 * static_cast<double>(p.K));
+        if (g_glu_tile.load(std::memory_order_relaxed) == ((c.pair ? 1 << 16 : 0) | c.bn)) { best = c; break; }
         if (best_cost < 0 || cost < best_cost) { best_cost = cost; best = c; }
     }
     if (best.pair) {
@@ -687,6 +710,16 @@ int run_glu(bool bwd, GluArgs p, unsigned flags, cudaStream_t stream) {
 }  // namespace fp8q
 
 using namespace fp8q;
+
+extern "C" int fp8q_glu_set_tile(int pair, int bn) {
+    if (pair == -1) {
+        g_glu_tile.store(-1);
+        return FP8Q_OK;
+    }
+    if ((pair != 0 && pair != 1) || (bn != 128 && bn != 192 && bn != 256 && (bn != 64 || pair))) return FP8Q_ERR_UNSUPPORTED;
+    g_glu_tile.store((pair << 16) | bn);
+    return FP8Q_OK;
+}
 
 extern "C" int fp8_glu_fwd(const void* x_q, const void* w1t_q, const float* scale_x, const float* scale_w, int act,
                            void* h_out, void* act_out, const float* scale_a, void* a_q, void* a_q_t, float* amax_out,

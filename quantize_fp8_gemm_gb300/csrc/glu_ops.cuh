@@ -24,7 +24,7 @@ constexpr float kGelu2CB = 0.07135481282779408f;  // 2 sqrt(2 / pi) 0.044715
 
 __device__ __forceinline__ f32x2 twice(float v) { return pair_of(v, v); }
 
-// 1 / (1 + 2^e): 0 where 2^e runs over.
+// 1 / (1 + 2^e); 0 where it is below float32's normal range (e above 126).
 __device__ __forceinline__ f32x2 logistic2(f32x2 e) {
     const float2 f = split(e);
     float a, b;

@@ -55,7 +55,7 @@ def check_codes(v, scale, fmt, q, q_t, amax, sat):
 
 
 # one token to several row tiles of pairs, widths of one block to several column tiles, ends inside boxes
-SHAPES = [(1, 16, 16), (1, 208, 1600), (3, 16, 64), (16, 48, 32), (31, 80, 144), (64, 128, 64), (100, 272, 400),
+SHAPES = [(1, 16, 16), (1, 208, 1600), (1, 48, 8192), (1, 32, 8208), (2, 2000, 528), (3, 16, 64), (4, 10000, 96), (5, 64, 2064), (16, 48, 32), (31, 80, 144), (64, 128, 64), (100, 272, 400),
           (128, 256, 128), (129, 144, 528), (256, 512, 768), (300, 1040, 96), (1000, 336, 256), (2048, 2736, 128)]
 
 
@@ -115,6 +115,36 @@ def test_backward_activations(B, M, F, N, act):
     R.assert_within(dh, want, tol, "dh")
 
 
+TILES = [(0, 64), (0, 128), (0, 192), (0, 256), (1, 128), (1, 192), (1, 256)]
+
+
+@pytest.fixture
+def tile(B, request):
+    B.fp8q_glu_set_tile(*request.param)
+    yield request.param
+    B.fp8q_glu_set_tile(-1)
+
+
+@pytest.mark.parametrize("M,F,K", [(144, 272, 80), (496, 1040, 336), (4000, 144, 48)])
+@pytest.mark.parametrize("tile", TILES, indirect=True, ids=str)
+def test_every_tile(B, tile, M, F, K):
+    """Each tile at ends inside its rows, chunks and 128-byte k-blocks; results do not depend on it."""
+    test_forward(B, M, F, K, "silu")
+    test_backward(B, M, F, K, "gelu")
+    x, w, sx, sw = fwd_inputs(M, F, K, 5)
+    a, b = poison(M, F, dtype=torch.bfloat16), poison(M, F, dtype=torch.bfloat16)
+    B.fp8_glu_fwd(x, w, sx, sw, act_out=a)
+    B.fp8q_glu_set_tile(-1)
+    B.fp8_glu_fwd(x, w, sx, sw, act_out=b)
+    assert torch.equal(a, b)
+
+
+def test_tile_hook_refuses(B):
+    for bad in ((0, 96), (1, 64), (2, 128), (0, 0)):
+        with pytest.raises(B.Fp8qError):
+            B.fp8q_glu_set_tile(*bad)
+
+
 @pytest.mark.parametrize("M,F,K", [(48, 80, 144), (272, 400, 128)])
 def test_outputs_alone(B, M, F, K):
     """Each optional output asked for by itself has the bits it has among the others."""
@@ -135,6 +165,54 @@ def test_outputs_alone(B, M, F, K):
         assert torch.equal(one, full), name
     B.fp8_gemm_dgrad_glu(dy, w2, sdy, sw2, hb, dh=hb)  # over its input
     assert torch.equal(hb, dh)
+
+
+@pytest.mark.parametrize("M,F,K", [(48, 64, 48), (272, 208, 64)])
+def test_tensors_off_the_32_byte_grid(B, M, F, K):
+    """16-byte alignment is all that is asked of a tensor: outputs and h at odd multiples of it."""
+    def at16(rows, cols, dtype):
+        buf = torch.zeros(rows * cols * dtype.itemsize + 48, dtype=torch.uint8, device="cuda")
+        start = 16 if buf.data_ptr() % 32 == 0 else 0
+        t = buf[start:start + rows * cols * dtype.itemsize].view(dtype).view(rows, cols)
+        assert t.data_ptr() % 32 == 16
+        return t, lambda: not buf[:start].any() and not buf[start + rows * cols * dtype.itemsize:].any()
+
+    bf, u8 = torch.bfloat16, torch.uint8
+    x, w, sx, sw = fwd_inputs(M, F, K, 21)
+    want = [torch.empty(M, 2 * F, dtype=bf, device="cuda"), torch.empty(M, F, dtype=bf, device="cuda"),
+            torch.empty(M, F, dtype=u8, device="cuda"), torch.empty(F, M, dtype=u8, device="cuda")]
+    outs = [at16(M, 2 * F, bf), at16(M, F, bf), at16(M, F, u8), at16(F, M, u8)]
+    for h, a, q, t in (want, [o for o, _ in outs]):
+        B.fp8_glu_fwd(x, w, sx, sw, h_out=h, act_out=a, scale_a=cell(30), a_q=q, a_q_t=t)
+    assert all(torch.equal(o, v) and clean() for (o, clean), v in zip(outs, want))
+    dy, w2, sdy, sw2, hb = bwd_inputs(M, F, K, 22)
+    h16 = at16(M, 2 * F, bf)[0]
+    h16.copy_(hb)
+    want = [torch.empty(M, 2 * F, dtype=bf, device="cuda"), torch.empty(M, 2 * F, dtype=u8, device="cuda"), torch.empty(2 * F, M, dtype=u8, device="cuda")]
+    outs = [at16(M, 2 * F, bf), at16(M, 2 * F, u8), at16(2 * F, M, u8)]
+    for h, (dh, q, t) in ((hb, want), (h16, [o for o, _ in outs])):
+        B.fp8_gemm_dgrad_glu(dy, w2, sdy, sw2, h, dh=dh, scale_dh=cell(100), dh_q=q, dh_q_t=t)
+    assert all(torch.equal(o, v) and clean() for (o, clean), v in zip(outs, want))
+
+
+def test_large_values_and_gate_tails(B):
+    """Gates far in the exponential's tails (it overflows at -89) and squares past float32's range of codes."""
+    M, F, N = 32, 64, 48
+    dy, w, sdy, sw, h = bwd_inputs(M, F, N, 31)
+    g = torch.tensor([-300.0, -100.0, -89.0, -88.0, -30.0, -1e-3, 0.0, 1e-30, 20.0, 88.0, 100.0, 3000.0], device="cuda")
+    h[:, :12] = g.to(torch.bfloat16)
+    for act in ("silu", "gelu"):
+        dh = poison(M, 2 * F, dtype=torch.bfloat16)
+        B.fp8_gemm_dgrad_glu(dy, w, sdy, sw, h, act=R.ACTS[act], dh=dh)
+        want, tol = R.bwd(dy.view(E5).double() / sdy.double(), w.view(E4).double() / sw.double(), h.double(), act)
+        assert bool(torch.isfinite(dh).all())
+        R.assert_within(dh, want, tol, act)
+    x, w, sx, sw = fwd_inputs(M, F, N, 32)
+    for act in ("silu", "gelu"):  # g and u of some thousands, both signs
+        a = poison(M, F, dtype=torch.bfloat16)
+        B.fp8_glu_fwd(x, w, sx, sw / 3000, act=R.ACTS[act], act_out=a)
+        *_, a64, _, _, ta = R.fwd(x.view(E4).double() / sx.double(), w.view(E4).double() / (sw / 3000).double(), act)
+        R.assert_within(a, a64, ta, act)
 
 
 def test_accumulate_and_empty(B):
