@@ -817,12 +817,28 @@ int dropout_bwd(const void* dy, int64_t ld_dy, void* dx, int64_t ld_dx, int64_t 
  *   M, F, K  M >= 0 (0: only amax_out and sat_count are zeroed); F >= 16,
  *            F % 16 == 0; K >= 16, K % 16 == 0.
  *   status   as for fp8_gemm_fwd.
- * Tensors are packed and 16-byte aligned, and must not overlap.
+ * Tensors are packed and 16-byte aligned, and must not overlap.  Zero the struct
+ * and set what the call needs.
  */
-int fp8_glu_fwd(const void* x_q, const void* w1t_q, const float* scale_x, const float* scale_w, int act,
-                void* h_out, void* act_out, const float* scale_a, void* a_q, void* a_q_t,
-                float* amax_out, unsigned long long* sat_count, int64_t M, int64_t F, int64_t K,
-                unsigned flags, int* status, cudaStream_t stream);
+typedef struct {
+    const void* x_q;
+    const void* w1t_q;
+    const float* scale_x;
+    const float* scale_w;
+    void* h_out;
+    void* act_out;
+    const float* scale_a;
+    void* a_q;
+    void* a_q_t;
+    float* amax_out;
+    unsigned long long* sat_count;
+    int64_t M, F, K;
+    int act;
+    unsigned flags;
+    int* status;
+} fp8q_glu_args;
+
+int fp8_glu_fwd(const fp8q_glu_args* args, cudaStream_t stream);
 
 /*
  * fp8_gemm_dgrad_glu -- the gated block's gradient in the down-projection's dgrad
@@ -845,10 +861,25 @@ int fp8_glu_fwd(const void* x_q, const void* w1t_q, const float* scale_x, const 
  *   M, N, F  M >= 0; N >= 16, N % 16 == 0 (the contraction); F as for fp8_glu_fwd.
  * Apart from dh over h the tensors must not overlap; packed, 16-byte aligned.
  */
-int fp8_gemm_dgrad_glu(const void* dy_q, const void* w2_q, const float* scale_dy, const float* scale_w,
-                       const void* h, int act, void* dh, const float* scale_dh, void* dh_q, void* dh_q_t,
-                       float* amax_out, unsigned long long* sat_count, int64_t M, int64_t N, int64_t F,
-                       unsigned flags, int* status, cudaStream_t stream);
+typedef struct {
+    const void* dy_q;
+    const void* w2_q;
+    const float* scale_dy;
+    const float* scale_w;
+    const void* h;
+    void* dh;
+    const float* scale_dh;
+    void* dh_q;
+    void* dh_q_t;
+    float* amax_out;
+    unsigned long long* sat_count;
+    int64_t M, N, F;
+    int act;
+    unsigned flags;
+    int* status;
+} fp8q_dgrad_glu_args;
+
+int fp8_gemm_dgrad_glu(const fp8q_dgrad_glu_args* args, cudaStream_t stream);
 
 /*
  * Norms before and after a block

@@ -93,8 +93,8 @@ def lib() -> ctypes.CDLL:
         L.fp8_gemm_mx.argtypes = [P, P, P, P, P, i64, i64, i64, i32, i32, P, P]
         L.fp8_mx_scale_bytes.argtypes = [i64, i64]
         L.fp8_mx_scale_bytes.restype = i64
-        L.fp8_glu_fwd.argtypes = [P, P, P, P, i32, P, P, P, P, P, P, P, i64, i64, i64, ctypes.c_uint, P, P]
-        L.fp8_gemm_dgrad_glu.argtypes = [P, P, P, P, P, i32, P, P, P, P, P, P, i64, i64, i64, ctypes.c_uint, P, P]
+        L.fp8_glu_fwd.argtypes = [P, P]
+        L.fp8_gemm_dgrad_glu.argtypes = [P, P]
         L.block_norm_fwd.argtypes = [P, P]
         L.block_norm_bwd.argtypes = [P, P]
         L.block_norm_bwd_workspace_bytes.argtypes = [i64, i64]
@@ -800,6 +800,26 @@ def block_norm_bwd(dy, r, rstd, weight, *, dr=None, x=None, residual=None, alpha
 
 
 # -- the gated feed-forward block --
+class GluArgs(ctypes.Structure):
+    """fp8q_glu_args."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("x_q", "w1t_q", "scale_x", "scale_w", "h_out", "act_out", "scale_a", "a_q",
+                                               "a_q_t", "amax_out", "sat_count")] + \
+               [(n, ctypes.c_int64) for n in ("M", "F", "K")] + \
+               [("act", ctypes.c_int), ("flags", ctypes.c_uint), ("status", ctypes.c_void_p)]
+
+
+class DgradGluArgs(ctypes.Structure):
+    """fp8q_dgrad_glu_args."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("dy_q", "w2_q", "scale_dy", "scale_w", "h", "dh", "scale_dh", "dh_q",
+                                               "dh_q_t", "amax_out", "sat_count")] + \
+               [(n, ctypes.c_int64) for n in ("M", "N", "F")] + \
+               [("act", ctypes.c_int), ("flags", ctypes.c_uint), ("status", ctypes.c_void_p)]
+
+
+_glu = struct.Struct("@PPPPPPPPPPPqqqiIP")  # either of them, as bytes
+assert _glu.size == ctypes.sizeof(GluArgs) == ctypes.sizeof(DgradGluArgs)
+
+
 def fp8_glu_fwd(x_q: torch.Tensor, w1t_q: torch.Tensor, scale_x: torch.Tensor, scale_w: torch.Tensor, *,
                 act: int = ACT_SILU, h_out=None, act_out=None, scale_a=None, a_q=None, a_q_t=None, amax_out=None,
                 sat_count=None, flags: int = 0, status=None, stream=None) -> None:
@@ -815,13 +835,16 @@ def fp8_glu_fwd(x_q: torch.Tensor, w1t_q: torch.Tensor, scale_x: torch.Tensor, s
         raise ValueError(f"w1t_q has {rows} rows: the gate's and as many of the up-projection")
     _here(x_q, "x_q")
     bf, f32 = torch.bfloat16, torch.float32
-    st = lib().fp8_glu_fwd(
-        _packed(x_q, M, K, None, "x_q"), _packed(w1t_q, rows, K, None, "w1t_q"), _cell(scale_x, f32, "scale_x"),
-        _cell(scale_w, f32, "scale_w"), act, _packed(h_out, M, rows, bf, "h_out"), _packed(act_out, M, F, bf, "act_out"),
-        _cell(scale_a, f32, "scale_a"), _packed(a_q, M, F, None, "a_q"), _packed(a_q_t, F, M, None, "a_q_t"),
-        _cell(amax_out, f32, "amax_out"), _cell(sat_count, torch.int64, "sat_count"), M, F, K, flags,
-        _cell(status, torch.int32, "status"), _stream(stream))
-    _check("fp8_glu_fwd", st)
+    args = _glu.pack(
+        _packed(x_q, M, K, None, "x_q"), _packed(w1t_q, rows, K, None, "w1t_q"), _cell(scale_x, f32, "scale_x") or 0,
+        _cell(scale_w, f32, "scale_w") or 0, 0 if h_out is None else _packed(h_out, M, rows, bf, "h_out"),
+        0 if act_out is None else _packed(act_out, M, F, bf, "act_out"),
+        0 if scale_a is None else _cell(scale_a, f32, "scale_a"), 0 if a_q is None else _packed(a_q, M, F, None, "a_q"),
+        0 if a_q_t is None else _packed(a_q_t, F, M, None, "a_q_t"),
+        0 if amax_out is None else _cell(amax_out, f32, "amax_out"),
+        0 if sat_count is None else _cell(sat_count, torch.int64, "sat_count"), M, F, K, act, flags,
+        0 if status is None else _cell(status, torch.int32, "status"))
+    _check("fp8_glu_fwd", lib().fp8_glu_fwd(args, _stream(stream)))
 
 
 def fp8_gemm_dgrad_glu(dy_q: torch.Tensor, w2_q: torch.Tensor, scale_dy: torch.Tensor, scale_w: torch.Tensor,
@@ -836,13 +859,16 @@ def fp8_gemm_dgrad_glu(dy_q: torch.Tensor, w2_q: torch.Tensor, scale_dy: torch.T
     F = w2_q.shape[0]
     _here(dy_q, "dy_q")
     bf, f32 = torch.bfloat16, torch.float32
-    st = lib().fp8_gemm_dgrad_glu(
-        _packed(dy_q, M, N, None, "dy_q"), _packed(w2_q, F, N, None, "w2_q"), _cell(scale_dy, f32, "scale_dy"),
-        _cell(scale_w, f32, "scale_w"), _packed(h, M, 2 * F, bf, "h"), act, _packed(dh, M, 2 * F, bf, "dh"),
-        _cell(scale_dh, f32, "scale_dh"), _packed(dh_q, M, 2 * F, None, "dh_q"),
-        _packed(dh_q_t, 2 * F, M, None, "dh_q_t"), _cell(amax_out, f32, "amax_out"),
-        _cell(sat_count, torch.int64, "sat_count"), M, N, F, flags, _cell(status, torch.int32, "status"), _stream(stream))
-    _check("fp8_gemm_dgrad_glu", st)
+    args = _glu.pack(
+        _packed(dy_q, M, N, None, "dy_q"), _packed(w2_q, F, N, None, "w2_q"), _cell(scale_dy, f32, "scale_dy") or 0,
+        _cell(scale_w, f32, "scale_w") or 0, _packed(h, M, 2 * F, bf, "h") or 0,
+        0 if dh is None else _packed(dh, M, 2 * F, bf, "dh"), 0 if scale_dh is None else _cell(scale_dh, f32, "scale_dh"),
+        0 if dh_q is None else _packed(dh_q, M, 2 * F, None, "dh_q"),
+        0 if dh_q_t is None else _packed(dh_q_t, 2 * F, M, None, "dh_q_t"),
+        0 if amax_out is None else _cell(amax_out, f32, "amax_out"),
+        0 if sat_count is None else _cell(sat_count, torch.int64, "sat_count"), M, N, F, act, flags,
+        0 if status is None else _cell(status, torch.int32, "status"))
+    _check("fp8_gemm_dgrad_glu", lib().fp8_gemm_dgrad_glu(args, _stream(stream)))
 
 
 def fp8q_naive_act(h, act: int, act_out, *, stream=None) -> None:

@@ -721,60 +721,58 @@ extern "C" int fp8q_glu_set_tile(int pair, int bn) {
     return FP8Q_OK;
 }
 
-extern "C" int fp8_glu_fwd(const void* x_q, const void* w1t_q, const float* scale_x, const float* scale_w, int act,
-                           void* h_out, void* act_out, const float* scale_a, void* a_q, void* a_q_t, float* amax_out,
-                           unsigned long long* sat_count, int64_t M, int64_t F, int64_t K, unsigned flags, int* status,
-                           cudaStream_t stream) {
-    const int st = check_glu(x_q, w1t_q, scale_x, scale_w, act, nullptr, h_out, act_out, scale_a, a_q, a_q_t, amax_out,
-                             sat_count, M, F, K, flags, status);
+extern "C" int fp8_glu_fwd(const fp8q_glu_args* args, cudaStream_t stream) {
+    if (!args) return FP8Q_ERR_NULL;
+    const fp8q_glu_args& a = *args;
+    const int st = check_glu(a.x_q, a.w1t_q, a.scale_x, a.scale_w, a.act, nullptr, a.h_out, a.act_out, a.scale_a, a.a_q,
+                             a.a_q_t, a.amax_out, a.sat_count, a.M, a.F, a.K, a.flags, a.status);
     if (st != FP8Q_OK && st != FP8Q_ERR_UNSUPPORTED) return st;
-    if (M != 0 && !act_out && !a_q && !a_q_t) return FP8Q_ERR_NULL;
+    if (a.M != 0 && !a.act_out && !a.a_q && !a.a_q_t) return FP8Q_ERR_NULL;
     if (st != FP8Q_OK) return st;
     GluArgs p = {};
-    p.x = x_q;
-    p.w = w1t_q;
-    p.o = static_cast<uint16_t*>(h_out);
-    p.d = static_cast<uint16_t*>(act_out);
-    p.q = static_cast<uint8_t*>(a_q);
-    p.t = static_cast<uint8_t*>(a_q_t);
-    p.scale_a = scale_x;
-    p.scale_b = scale_w;
-    p.scale_q = scale_a;
-    p.amax = amax_out;
-    p.sat = sat_count;
-    p.status = status;
-    p.M = M;
-    p.F = F;
-    p.K = K;
-    p.act = act;
-    return run_glu(false, p, flags, stream);
+    p.x = a.x_q;
+    p.w = a.w1t_q;
+    p.o = static_cast<uint16_t*>(a.h_out);
+    p.d = static_cast<uint16_t*>(a.act_out);
+    p.q = static_cast<uint8_t*>(a.a_q);
+    p.t = static_cast<uint8_t*>(a.a_q_t);
+    p.scale_a = a.scale_x;
+    p.scale_b = a.scale_w;
+    p.scale_q = a.scale_a;
+    p.amax = a.amax_out;
+    p.sat = a.sat_count;
+    p.status = a.status;
+    p.M = a.M;
+    p.F = a.F;
+    p.K = a.K;
+    p.act = a.act;
+    return run_glu(false, p, a.flags, stream);
 }
 
-extern "C" int fp8_gemm_dgrad_glu(const void* dy_q, const void* w2_q, const float* scale_dy, const float* scale_w,
-                                  const void* h, int act, void* dh, const float* scale_dh, void* dh_q, void* dh_q_t,
-                                  float* amax_out, unsigned long long* sat_count, int64_t M, int64_t N, int64_t F,
-                                  unsigned flags, int* status, cudaStream_t stream) {
-    const int st = check_glu(dy_q, w2_q, scale_dy, scale_w, act, h, dh, nullptr, scale_dh, dh_q, dh_q_t, amax_out,
-                             sat_count, M, F, N, flags, status);
+extern "C" int fp8_gemm_dgrad_glu(const fp8q_dgrad_glu_args* args, cudaStream_t stream) {
+    if (!args) return FP8Q_ERR_NULL;
+    const fp8q_dgrad_glu_args& a = *args;
+    const int st = check_glu(a.dy_q, a.w2_q, a.scale_dy, a.scale_w, a.act, a.h, a.dh, nullptr, a.scale_dh, a.dh_q,
+                             a.dh_q_t, a.amax_out, a.sat_count, a.M, a.F, a.N, a.flags, a.status);
     if (st != FP8Q_OK && st != FP8Q_ERR_UNSUPPORTED) return st;
-    if (M != 0 && (!h || (!dh && !dh_q && !dh_q_t))) return FP8Q_ERR_NULL;
+    if (a.M != 0 && (!a.h || (!a.dh && !a.dh_q && !a.dh_q_t))) return FP8Q_ERR_NULL;
     if (st != FP8Q_OK) return st;
     GluArgs p = {};
-    p.x = dy_q;
-    p.w = w2_q;
-    p.h = static_cast<const uint16_t*>(h);
-    p.o = static_cast<uint16_t*>(dh);
-    p.q = static_cast<uint8_t*>(dh_q);
-    p.t = static_cast<uint8_t*>(dh_q_t);
-    p.scale_a = scale_dy;
-    p.scale_b = scale_w;
-    p.scale_q = scale_dh;
-    p.amax = amax_out;
-    p.sat = sat_count;
-    p.status = status;
-    p.M = M;
-    p.F = F;
-    p.K = N;
-    p.act = act;
-    return run_glu(true, p, flags, stream);
+    p.x = a.dy_q;
+    p.w = a.w2_q;
+    p.h = static_cast<const uint16_t*>(a.h);
+    p.o = static_cast<uint16_t*>(a.dh);
+    p.q = static_cast<uint8_t*>(a.dh_q);
+    p.t = static_cast<uint8_t*>(a.dh_q_t);
+    p.scale_a = a.scale_dy;
+    p.scale_b = a.scale_w;
+    p.scale_q = a.scale_dh;
+    p.amax = a.amax_out;
+    p.sat = a.sat_count;
+    p.status = a.status;
+    p.M = a.M;
+    p.F = a.F;
+    p.K = a.N;
+    p.act = a.act;
+    return run_glu(true, p, a.flags, stream);
 }

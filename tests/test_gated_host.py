@@ -66,14 +66,17 @@ def test_norm_reference_against_autograd(post, pre):
 
 
 def glu(lib, x=A, w=A, sx=A, sw=A, act=3, h=A, a=A, s=A, q=A, qt=A, amax=A, sat=A, M=32, F=48, K=64, flags=0, st=None):
-    return lib.fp8_glu_fwd(x, w, sx, sw, act, h, a, s, q, qt, amax, sat, M, F, K, flags, st, None)
+    args = B.GluArgs(x, w, sx, sw, h, a, s, q, qt, amax, sat, M, F, K, act, flags, st)
+    return lib.fp8_glu_fwd(ctypes.byref(args), None)
 
 
 def dglu(lib, dy=A, w=A, sdy=A, sw=A, h=A, act=3, dh=A, s=A, q=A, qt=A, amax=A, sat=A, M=32, N=64, F=48, flags=0, st=None):
-    return lib.fp8_gemm_dgrad_glu(dy, w, sdy, sw, h, act, dh, s, q, qt, amax, sat, M, N, F, flags, st, None)
+    args = B.DgradGluArgs(dy, w, sdy, sw, h, dh, s, q, qt, amax, sat, M, N, F, act, flags, st)
+    return lib.fp8_gemm_dgrad_glu(ctypes.byref(args), None)
 
 
 def test_gated_argument_checks(lib):
+    assert lib.fp8_glu_fwd(None, None) == ERR_NULL and lib.fp8_gemm_dgrad_glu(None, None) == ERR_NULL
     for call, width in ((glu, "K"), (dglu, "N")):
         for k in ("w", "sw", "s"):
             assert call(lib, **{k: None}) == ERR_NULL, k
@@ -206,6 +209,15 @@ def test_binding_refuses_host_tensors_and_shapes():
         B.fp8_glu_fwd(q, w1[:31], f, f, act_out=x)
     with pytest.raises(TypeError):
         B.fp8_gemm_dgrad_glu(q, w1, f, f, x, dh=x)
+
+
+@pytest.mark.parametrize("form,cls", [(B._block_norm, B.BlockNormArgs), (B._block_norm_bwd, B.BlockNormBwdArgs),
+                                      (B._glu, B.GluArgs), (B._glu, B.DgradGluArgs)])
+def test_packed_arguments_are_the_structs(form, cls):
+    """The bytes that the binding packs, field by field the ctypes structure's."""
+    values = [0.5 if t is ctypes.c_float else 1000 + i if t is not ctypes.c_int else i % 3 for i, (_, t) in enumerate(cls._fields_)]
+    got = cls.from_buffer_copy(form.pack(*values))
+    assert [getattr(got, n) for n, _ in cls._fields_] == values
 
 
 @pytest.fixture(scope="module")
