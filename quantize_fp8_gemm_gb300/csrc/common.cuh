@@ -24,6 +24,8 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 int sm_count();
 // True when the current device is compute capability 10.3 (GB300).
 bool device_is_sm103();
+// Whether fp8q_gemm_test_hold_loads is on.
+bool gemm_loads_held();
 
 #define FP8Q_CHECK_LAUNCH()                                     \
     do {                                                        \

@@ -1539,6 +1539,8 @@ int launch_eq(const Shape& s, const void* a, const void* b, const float* sa, con
 
 using namespace fp8q;
 
+bool fp8q::gemm_loads_held() { return g_hold_loads.load() != 0; }
+
 extern "C" void fp8q_gemm_test_hold_loads(int on) { g_hold_loads.store(on != 0 ? 1 : 0); }
 
 extern "C" int fp8q_test_gemm_tile(int64_t M, int64_t N, int fused, int* pair, int* bn) {

@@ -68,6 +68,7 @@ struct GluArgs {
     int64_t M, F, K;
     uint32_t idesc;
     int act;
+    bool hold;         // test hook: no operand is loaded, so that the first wait runs out
     uint32_t a_bytes;  // of a CTA's box of A: of a call of less than 128 rows the rows that there are
     bool wide_bf, wide_q;  // every 16 columns of h, o and d (32 of q) of a row are one 32-byte sector
 };
@@ -295,7 +296,7 @@ glu_kernel(const __grid_constant__ GluMaps maps, const GluArgs p) {
             uint32_t phase = 0;
             int64_t issued = 0;
             bool ok = true;
-            for (; tile.more() && ok; tile.next()) {
+            for (; tile.more() && ok && !p.hold; tile.next()) {
                 const int32_t m0 = static_cast<int32_t>(tile.m * C::TILE_M + rank * BM);
                 const int32_t n0 = static_cast<int32_t>(tile.n * C::OUT);
                 const int32_t up = static_cast<int32_t>(p.F) + n0;  // forward: the up-projection's rows of W1^T
@@ -700,6 +701,7 @@ int run_glu(bool bwd, GluArgs p, unsigned flags, cudaStream_t stream) {
     }
     if (p.M == 0) return FP8Q_OK;
     // (a row of h, o or d is a multiple of 32 bytes long, one of q only where F is)
+    p.hold = gemm_loads_held();
     p.wide_bf = aligned_to(p.h, 32) && aligned_to(p.o, 32) && aligned_to(p.d, 32);
     p.wide_q = aligned_to(p.q, 32) && p.F % 32 == 0;
     return bwd ? dispatch_glu<true>(p, stream) : dispatch_glu<false>(p, stream);

@@ -280,3 +280,53 @@ def test_captured(B):
         g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip((y, amax, dx, dw), want))
+
+
+@pytest.mark.parametrize("N,T", [(64, BF), (250, HF), (1600, BF), (1001, HF), (4104, BF), (20001, BF), (768, FP)])
+def test_one_row_and_codes(B, N, T):
+    """One row is one CTA, which stores the maximum and count itself; with ACCUMULATE it adds to them."""
+    s = make(1, N, T, 77)
+    y, q = torch.empty_like(s["x"]), torch.empty(1, N, dtype=torch.uint8, device="cuda")
+    amax, sat, scale = torch.full((1,), 1e9, device="cuda"), torch.full((1,), 50, device="cuda"), torch.full((1,), 400.0, device="cuda")
+    kw = dict(eps=EPS, residual=s["residual"], post_weight=s["wp"], post_norm=True, scale=scale, q_out=q, sat_count=sat)
+    B.block_norm_fwd(s["x"], s["w"], y, amax_out=amax, **kw)
+    count = int(((y.float() * 400).abs() > 448).sum())
+    assert float(amax) == float(y.float().abs().max()) and int(sat) == count > 0
+    big = torch.full((1,), 1e9, device="cuda")
+    B.block_norm_fwd(s["x"], s["w"], y, amax_out=big, flags=B.ACCUMULATE, **kw)
+    assert float(big) == 1e9 and int(sat) == 2 * count
+
+
+def test_two_streams_at_once(B):
+    """Backward calls side by side, each with a workspace of its own."""
+    sets = [make(3000, 1600, BF, 60 + i) for i in range(2)]
+    stats = [((s["r"].float().square().mean(1) + EPS).rsqrt(), (s["x"].float().square().mean(1) + EPS).rsqrt()) for s in sets]
+    size = B.block_norm_bwd_workspace_bytes(3000, 1600)
+
+    def outs():
+        return [torch.empty_like(sets[0]["x"]), torch.empty(1600, device="cuda"), torch.empty(1600, device="cuda"),
+                torch.empty(size, dtype=torch.uint8, device="cuda")]
+
+    def run(i, o):
+        s, (rstd, rp) = sets[i], stats[i]
+        for _ in range(3):
+            B.block_norm_bwd(s["dy"], s["r"], rstd, s["w"], dr=s["dr"], x=s["x"], post_weight=s["wp"], post_norm=True, rstd_post=rp,
+                             dx=o[0], dweight=o[1], dpost_weight=o[2], workspace=o[3])
+
+    alone, both = [outs() for _ in range(2)], [outs() for _ in range(2)]
+    for i in range(2):
+        run(i, alone[i])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for i in range(2):
+        with torch.cuda.stream(streams[i]):
+            run(i, both[i])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for x, y in zip(alone, both) for a, b in zip(x[:3], y[:3]))
+
+
+@pytest.mark.parametrize("N,T", [(12288, BF), (16377, HF), (6000, FP), (40000, BF)])
+def test_rows_over_a_cluster(B, N, T):
+    """Rows that two, four and eight CTAs share, several a cluster."""
+    check_bwd(B, 400, N, T, gate=True, alpha=True)
+    check_bwd(B, 400, N, T)

@@ -271,3 +271,56 @@ def test_captured_and_streams(B):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(got, ref.flip(0)) and torch.equal(amax, amax2)
+
+
+@pytest.mark.parametrize("M", [64, 300])
+def test_a_wait_that_runs_out_is_reported(B, M):
+    """No operand arrives (a hook): the kernels give up after about 2 s, say so and leave the context usable."""
+    F, K = 80, 64
+    x, w, sx, sw = fwd_inputs(M, F, K, 8)
+    dy, w2, sdy, sw2, h = bwd_inputs(M, F, K, 9)
+    a, dh = poison(M, F, dtype=torch.bfloat16), poison(M, 2 * F, dtype=torch.bfloat16)
+    want = [t.clone() for t in (a, dh)]
+    B.fp8_glu_fwd(x, w, sx, sw, act_out=want[0])
+    B.fp8_gemm_dgrad_glu(dy, w2, sdy, sw2, h, dh=want[1])
+    for call in (lambda st: B.fp8_glu_fwd(x, w, sx, sw, act_out=a, status=st), lambda st: B.fp8_gemm_dgrad_glu(dy, w2, sdy, sw2, h, dh=dh, status=st)):
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        B.fp8q_gemm_test_hold_loads(True)
+        try:
+            call(status)
+            torch.cuda.synchronize()
+        finally:
+            B.fp8q_gemm_test_hold_loads(False)
+        assert int(status) & B.DEV_TIMEOUT
+        status.zero_()
+        call(status)
+        assert int(status) == 0
+    assert torch.equal(a, want[0]) and torch.equal(dh, want[1])
+
+
+def test_two_streams_at_once(B):
+    """Calls of both kernels side by side on two streams have the bits they have alone."""
+    M, F, K = 2048, 1040, 256
+    sets = [fwd_inputs(M, F, K, 40 + i) for i in range(2)]
+    backs = [bwd_inputs(M, F, K, 50 + i) for i in range(2)]
+
+    def run(i, out):
+        x, w, sx, sw = sets[i]
+        dy, w2, sdy, sw2, h = backs[i]
+        for _ in range(4):
+            B.fp8_glu_fwd(x, w, sx, sw, scale_a=out[4], a_q=out[0], a_q_t=out[1], amax_out=out[2])
+            B.fp8_gemm_dgrad_glu(dy, w2, sdy, sw2, h, dh=out[3])
+
+    def outs():
+        return [poison(M, F, dtype=torch.uint8), poison(F, M, dtype=torch.uint8), cell(0), poison(M, 2 * F, dtype=torch.bfloat16), cell(30)]
+
+    alone, both = [outs() for _ in range(2)], [outs() for _ in range(2)]
+    for i in range(2):
+        run(i, alone[i])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for i in range(2):
+        with torch.cuda.stream(streams[i]):
+            run(i, both[i])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for x, y in zip(alone, both) for a, b in zip(x, y))
