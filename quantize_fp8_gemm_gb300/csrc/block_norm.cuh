@@ -104,17 +104,23 @@ __device__ __forceinline__ void finish_quant(const BnFwd<T>& p, uint32_t amax, u
     else publish_quant(p.quant, amax, nsat);
 }
 
+// cp.async of the first `bytes` bytes of a granule, and zeros for the others.
+__device__ __forceinline__ void cp_async16_part(uint32_t smem_addr, const void* gmem, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(smem_addr), "l"(gmem), "r"(bytes) : "memory");
+}
+
 // A thread's columns.  On the 16-byte grid a thread has whole 16-byte pieces: piece t + 32 c
 // of its row, c < C, V columns each.  Off it (SHIFT) neither rows nor tensors of one row share an
 // alignment, and a thread has the 4-byte words of its range of columns that lie L lanes apart: pairs
 // of adjacent 2-byte columns, or single 4-byte ones.  The ring then holds the 16-byte granules that
 // a row touches, one after the other, and a word is cut from the two that it may lie across by one
 // funnel shift; reads are free of bank conflicts and stores whole words, shifted by one element
-// through the neighbouring lane where the row starts between two words.  (Cutting whole pieces from
-// two granules each, and joining them for the stores, took three times the instructions: forward
-// bf16 65536 x 1601 315 us, backward 451 us.)
+// through the neighbouring lane where the row starts between two words.  The row's last granule is copied
+// in part and the rest zero-filled, so that nothing read needs a check.  (Cutting whole pieces from two
+// granules each, and joining them for the stores: forward bf16 65536 x 1601 315 us, backward 451;
+// now 219 and 366.)
 // BRANCH: rows that start on a word are told from the others by a branch (forward bf16 65536 x 1601
-// 277 us without, 223 with; the backward, short of registers, 389 without and 437 with).
+// 277 us without, 219 with; the backward, short of registers, 389 without and 437 with).
 template <typename T, int C, bool SHIFT, bool BRANCH>
 struct Columns {
     static constexpr int V = 16 / sizeof(T), H = V / 2;
@@ -194,7 +200,9 @@ struct Columns {
 #pragma unroll
             for (int c = 0; c <= C; ++c) {
                 const int g = c < C ? t + lanes * c : lanes * C, at = begin + g * 16;
-                if (c < C || t == lanes - 1) cp_async16_or_zero(to + g * 16, at < end ? base + at : base, at < end);
+                // (what lies behind the row is zeros in the slots: its last granule is copied in part)
+                const int bytes = min(max(end - at, 0), 16);
+                if (c < C || t == lanes - 1) cp_async16_part(to + g * 16, bytes > 0 ? base + at : base, bytes);
             }
         } else {
 #pragma unroll
@@ -212,16 +220,8 @@ struct Columns {
             return pair_of(bf16lo_to_f32(u), bf16hi_to_f32(u));
         }
     }
-    // Columns behind the row: 0.
-    __device__ __forceinline__ void clip(int c, f32x2 (&v)[H]) const {
-#pragma unroll
-        for (int i = 0; i < H; ++i) {
-            const float2 f = split(v[i]);
-            v[i] = pair_of(has(c, i, 0) ? f.x : 0.0f, has(c, i, 1) ? f.y : 0.0f);
-        }
-    }
-    // Piece c from the slots; `row` for its alignment.  tail: columns behind the row are made 0.
-    __device__ __forceinline__ void read(const uint4* slots, const T* row, int c, bool tail, f32x2 (&v)[H]) const {
+    // Piece c from the slots; `row` for its alignment.  Columns behind the row are zeros.
+    __device__ __forceinline__ void read(const uint4* slots, const T* row, int c, f32x2 (&v)[H]) const {
         if constexpr (SHIFT) {
             const uint32_t mis = granule_offset(row);
             const uint32_t* const words = reinterpret_cast<const uint32_t*>(slots) + (mis >> 2) + t;
@@ -241,7 +241,6 @@ struct Columns {
 #pragma unroll
                 for (int i = 0; i < H; ++i) v[i] = unpack_word(words[lanes * (c * H + i)]);
             }
-            if (tail) clip(c, v);
         } else {
             Piece<T, V> a;
             a.raw = slots[t + 32 * c];
@@ -264,16 +263,20 @@ struct Columns {
         } else {
             uint16_t* const out = reinterpret_cast<uint16_t*>(row);
             const bool between = reinterpret_cast<uintptr_t>(row) & 2;  // the row starts between two words
-            if (!tail && !between) {
+            const int rest = N - first - 2 * t;
+            if (C > 1 && !between) {  // (a warp's lanes have one row: all or none of them)
 #pragma unroll
-                for (int i = 0; i < H; ++i)
-                    if (in) *reinterpret_cast<uint32_t*>(out + col(c, i)) = u[i];
+                for (int i = 0; i < H; ++i) {
+                    const int left = !in ? -1 : tail ? rest - 2 * lanes * (c * H + i) : 2;
+                    if (left >= 2) *reinterpret_cast<uint32_t*>(out + col(c, i)) = u[i];
+                    else if (left == 1) out[col(c, i)] = static_cast<uint16_t>(u[i]);
+                }
                 return;
             }
             const int lane = threadIdx.x & 31, from = (lane & ~(lanes - 1)) | ((t + lanes - 1) & (lanes - 1));
 #pragma unroll
             for (int i = 0; i < H; ++i) {
-                const int j = col(c, i), left = !in ? -1 : tail ? N - j : 2;  // columns from this pair's first on
+                const int j = col(c, i), left = !in ? -1 : tail ? rest - 2 * lanes * (c * H + i) : 2;  // columns from this pair's first on
                 const uint32_t before = __shfl_sync(0xFFFFFFFFu, u[i], from);
                 if (!between) {
                     if (left >= 2) *reinterpret_cast<uint32_t*>(out + j) = u[i];
@@ -448,7 +451,7 @@ bn_fwd_kernel(const BnFwd<T> p, int team) {
         f32x2 sq[2] = {zero2, zero2};
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            my.read(at, x_row, c, tail(c), v[c]);
+            my.read(at, x_row, c, v[c]);
 #pragma unroll
             for (int i = 0; i < H; ++i) sq[i & 1] = fma2(v[c][i], v[c][i], sq[i & 1]);
         }
@@ -468,7 +471,7 @@ bn_fwd_kernel(const BnFwd<T> p, int team) {
             for (int i = 0; i < H; ++i) v[c][i] = mul2(mul2(mul2(v[c][i], rp2), f[i]), gate2);
             if (p.res) {
                 f32x2 r[H];
-                my.read(at + kTensor, res_row, c, tail(c), r);
+                my.read(at + kTensor, res_row, c, r);
 #pragma unroll
                 for (int i = 0; i < H; ++i) v[c][i] = fma2(alpha2, r[i], v[c][i]);
             }
@@ -476,13 +479,6 @@ bn_fwd_kernel(const BnFwd<T> p, int team) {
             pack2(a, v[c]);
             if (p.r_out) my.put(p.r_out + row * p.ld_r, c, a.raw, carry, in, tail(c));
             unpack2(a, v[c]);
-            // (weights of columns behind the row are not set: 0 times them may be a NaN)
-            if constexpr (SHIFT) {
-                if (tail(c)) my.clip(c, v[c]);
-            } else if (!my.has(c)) {
-#pragma unroll
-                for (int i = 0; i < H; ++i) v[c][i] = zero2;
-            }
 #pragma unroll
             for (int i = 0; i < H; ++i) sq[i & 1] = fma2(v[c][i], v[c][i], sq[i & 1]);
         }
@@ -540,8 +536,8 @@ cudaError_t launch_bn_fwd_as(const BnFwd<T>& p, int team, unsigned block, cudaSt
 // residual is read too.
 // What bounds it: memory where the rows are on the grid and fill the lanes (bf16 65536 x 2048 239 us,
 // 1.00 of the measured copy rate; 131072 x 1600 400 us, 0.93; fp32 65536 x 1600 355 us, 1.04); off it the
-// instructions that cut words and shift them back (bf16 65536 x 1601 0.46); rows over a cluster (8192 x
-// 16384 417 us, 0.57) wait at the cluster's barriers for the stores before them.
+// instructions that cut words and shift them back (bf16 65536 x 1601 366 us, 0.51; fp32, which has none to cut,
+// 65536 x 1001 240 us, 0.97); rows over a cluster (8192 x 16384 417 us, 0.57) wait at the cluster's barriers for the stores before them.
 enum BnMode { BN_NARROW, BN_WIDE, BN_CLUSTER };
 constexpr int bn_bwd_stages(bool alpha) { return alpha ? 2 : 3; }
 enum { IN_DY, IN_R, IN_DR, IN_X, IN_RES };
@@ -651,7 +647,7 @@ bn_bwd_kernel(const BnBwd<T> p, int team) {
                 for (int i = 0; i < H; ++i) v[i] = zero2;
                 return;
             }
-            my.read(at + which * kTensor, base_p + off, c, tail(c), v);
+            my.read(at + which * kTensor, base_p + off, c, v);
         };
         f32x2 dr[C][H];
         // the norm before the next block

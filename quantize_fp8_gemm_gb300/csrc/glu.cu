@@ -25,6 +25,16 @@
 // of g and u come by TMA into a buffer a warp, the next one asked for as soon as this one is in
 // registers (32-byte loads straight into registers, 32 sectors an instruction, took 680 us).
 //
+// What bounds it (GB300).  32768 x 1600 -> 6400 forward with h_out and both code layouts 473 us, 2.84
+// PFLOP/s (the codes alone 390 us, 3.44; the plain GEMM of the same product 423): the L1-to-L2 request
+// path (69 % busy, half of the requests one-sector stores) beside the tensor pipe (68 % of its cycles);
+// sustained for half a second the 1400 W cap holds the SMs at 1470 MHz and it takes 555.  Backward with
+// both code layouts 387 us, 4.5 TB/s: the epilogue's instructions, 36 an element of dA, issue in 46 % of the
+// cycles from four warps a scheduler; DRAM at 47 % of its peak.  A few tokens (1 to 128 x 1600 -> 6400, 20.5 MB of
+// weights): 7.5 us with the clearing launch, the 100 CTAs' first bytes and the 13 k-blocks' way through the ring.
+// Not kept: h_out through shared memory in 64-column boxes (508 us: two ring stages less), adjacent instead of
+// alternate chunks a warp (backward 417), a kernel of dot products for one or two rows (7.5 and 9.7 us).
+//
 // Every wait is bounded as in gemm.cu: on time-out the CTA sets FP8Q_DEV_TIMEOUT, lets its
 // copies and MMAs land (bounded), frees TMEM and exits.
 #include "common.cuh"
