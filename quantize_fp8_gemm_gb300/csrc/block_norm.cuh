@@ -220,6 +220,14 @@ struct Columns {
             return pair_of(bf16lo_to_f32(u), bf16hi_to_f32(u));
         }
     }
+    // Columns behind the row: 0.
+    __device__ __forceinline__ void clip(int c, f32x2 (&v)[H]) const {
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            const float2 f = split(v[i]);
+            v[i] = pair_of(has(c, i, 0) ? f.x : 0.0f, has(c, i, 1) ? f.y : 0.0f);
+        }
+    }
     // Piece c from the slots; `row` for its alignment.  Columns behind the row are zeros.
     __device__ __forceinline__ void read(const uint4* slots, const T* row, int c, f32x2 (&v)[H]) const {
         if constexpr (SHIFT) {
@@ -479,6 +487,13 @@ bn_fwd_kernel(const BnFwd<T> p, int team) {
             pack2(a, v[c]);
             if (p.r_out) my.put(p.r_out + row * p.ld_r, c, a.raw, carry, in, tail(c));
             unpack2(a, v[c]);
+            // (behind the row an infinite gate or alpha times the zeros there is NaN)
+            if constexpr (SHIFT) {
+                if (tail(c)) my.clip(c, v[c]);
+            } else if (!my.has(c)) {
+#pragma unroll
+                for (int i = 0; i < H; ++i) v[c][i] = zero2;
+            }
 #pragma unroll
             for (int i = 0; i < H; ++i) sq[i & 1] = fma2(v[c][i], v[c][i], sq[i & 1]);
         }
@@ -537,7 +552,8 @@ cudaError_t launch_bn_fwd_as(const BnFwd<T>& p, int team, unsigned block, cudaSt
 // What bounds it: memory where the rows are on the grid and fill the lanes (bf16 65536 x 2048 239 us,
 // 1.00 of the measured copy rate; 131072 x 1600 400 us, 0.93; fp32 65536 x 1600 355 us, 1.04); off it the
 // instructions that cut words and shift them back (bf16 65536 x 1601 366 us, 0.51; fp32, which has none to cut,
-// 65536 x 1001 240 us, 0.97); rows over a cluster (8192 x 16384 417 us, 0.57) wait at the cluster's barriers for the stores before them.
+// 65536 x 1001 240 us, 0.97); rows over a cluster (8192 x 16384 417 us, 0.57) wait at the cluster's barriers
+// for the stores before them.
 enum BnMode { BN_NARROW, BN_WIDE, BN_CLUSTER };
 constexpr int bn_bwd_stages(bool alpha) { return alpha ? 2 : 3; }
 enum { IN_DY, IN_R, IN_DR, IN_X, IN_RES };

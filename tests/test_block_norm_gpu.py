@@ -330,3 +330,29 @@ def test_rows_over_a_cluster(B, N, T):
     """Rows that two, four and eight CTAs share, several a cluster."""
     check_bwd(B, 400, N, T, gate=True, alpha=True)
     check_bwd(B, 400, N, T)
+
+
+@pytest.mark.parametrize("T", [BF, HF, FP], ids=["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("N", [8, 99, 333, 768, 1001, 1600, 1601, 5001])
+def test_infinite_scales_leave_the_statistic_zero(B, N, T):
+    """A row under an infinite gate, and every row under an infinite alpha, is infinite, so its statistic is
+    exactly 0: columns that lanes have behind the row (0 times an infinity) must not reach its sum."""
+    M = 37
+    s = make(M, N, T, 1234 + N, gate=True)
+    for k in ("x", "residual", "wp"):  # no zeros: 0 times an infinity is NaN in the row itself
+        s[k] = torch.where(s[k] == 0, torch.ones_like(s[k]), s[k])
+    s["gate"][5] = float("inf")
+    y, r = torch.empty(M, N, dtype=T, device="cuda"), torch.empty(M, N, dtype=T, device="cuda")
+    rstd = torch.full((M,), 5.0, device="cuda")
+
+    def run(alpha):
+        B.block_norm_fwd(s["x"], s["w"], y, eps=EPS, rstd=rstd, residual=s["residual"], alpha=alpha, gate=s["gate"],
+                         post_weight=s["wp"], post_norm=True, rstd_post=torch.empty(M, device="cuda"), r_out=r)
+
+    run(None)
+    others = [i for i in range(M) if i != 5]
+    assert bool(torch.isinf(r[5]).all()) and float(rstd[5]) == 0.0
+    assert bool(torch.isfinite(y[others]).all()) and bool((rstd[others] > 0).all())
+    s["gate"][5] = 0.5
+    run(torch.full((1,), float("inf"), device="cuda"))
+    assert bool(torch.isinf(r).all()) and bool((rstd == 0).all())
