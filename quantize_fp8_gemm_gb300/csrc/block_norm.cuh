@@ -118,9 +118,9 @@ __device__ __forceinline__ void cp_async16_part(uint32_t smem_addr, const void* 
 // through the neighbouring lane where the row starts between two words.  The row's last granule is copied
 // in part and the rest zero-filled, so that nothing read needs a check.  (Cutting whole pieces from two
 // granules each, and joining them for the stores: forward bf16 65536 x 1601 315 us, backward 451;
-// now 219 and 366.)
+// now 222 and 366.)
 // BRANCH: rows that start on a word are told from the others by a branch (forward bf16 65536 x 1601
-// 277 us without, 219 with; the backward, short of registers, 389 without and 437 with).
+// 277 us without, 222 with; the backward, short of registers, 389 without and 437 with).
 template <typename T, int C, bool SHIFT, bool BRANCH>
 struct Columns {
     static constexpr int V = 16 / sizeof(T), H = V / 2;
@@ -348,6 +348,10 @@ __host__ __device__ constexpr int bn_slots(int C, bool shift, bool rows) { retur
 // The row stays in registers from its one read to its one write; its two sums of squares (of
 // the block's output, and of the stored stream) are team shuffles, or an exchange each.
 // Weights: in registers up to 32 columns a lane, in shared memory above.
+// What bounds it: memory on the 16-byte grid (bf16 131072 x 1600 with codes 302 to 316 us, 0.92 to 0.88 of the
+// measured copy rate; 65536 x 768 69 us, 0.86; 8192 x 16384 160 to 180 us, 0.99 to 0.88); off it memory for
+// float32 (65536 x 1001 175 us, 0.88) and the words' instructions for bf16 (65536 x 1601 222 us, 0.56); for one
+// row the launch.
 template <typename T, int C, bool CTA, bool SHIFT, int S>
 __global__ void __launch_bounds__(CTA ? 512 : 128)
 bn_fwd_kernel(const BnFwd<T> p, int team) {
@@ -897,7 +901,7 @@ cudaError_t launch_bn_bwd(const BnBwd<T>& p, int most, int* parts, cudaStream_t 
     // Two-byte types: a warp a row up to 24 columns a lane (65536 x 768: 93 us, 111 in two warps of 16), and 32
     // columns a lane where 16 would leave a seventh of the lanes idle (131072 x 1600: 400 us, 433) or make a whole
     // CTA one group (8192 x 8192: 129, 142); where they fill the lanes 16 are better (65536 x 2048: 239, 252), and
-    // off the grid (65536 x 1601: 401, 457).
+    // off the grid (65536 x 1601: 401, 457 before last granules were copied in part).
     if constexpr (V == 8) {
         if (pieces <= 96) return launch_bn_bwd_as<T, 3, BN_NARROW, ALPHA, SHIFT>(p, 32, 256, 1, most, parts, stream);
         if constexpr (!SHIFT) {
