@@ -31,7 +31,7 @@
 // sustained for half a second the 1400 W cap holds the SMs at 1470 MHz and it takes 555.  Backward with
 // both code layouts 387 us, 4.5 TB/s: neither memory (DRAM at 47 % of its peak at 8192 rows) nor the tensor pipe
 // (37 %); instructions, 18 an element of dA, issue in 46 % of the cycles from at most 4.5 warps a scheduler, and
-// the 96 registers that 18 warps leave a thread spill 68 bytes.  A few tokens (1 to 128 x 1600 -> 6400, 20.5 MB of
+// the 96 registers that 18 warps leave a thread spill 48 bytes.  A few tokens (1 to 128 x 1600 -> 6400, 20.5 MB of
 // weights): 7.5 us with the clearing launch, 13 k-blocks one after another in each of 100 CTAs.
 // Not kept: h_out through shared memory in 64-column boxes (508 us: two ring stages less), adjacent instead of
 // alternate chunks a warp (backward 417), a kernel of dot products for one or two rows (7.6 and 9.8).
@@ -146,6 +146,13 @@ __device__ __forceinline__ void glu_codes(const uint32_t (&v)[8], float s, uint3
         for (int g = 0; g < 2; ++g)
             nsat += sat_count8<FMT>(make_uint4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]), s);
     }
+}
+
+// Values of rows behind M or columns behind F, whatever an accumulator holds there (other rows' sums, or an
+// infinity times the zeros that fill a box): nothing for the maximum and the count.
+__device__ __forceinline__ void none(uint32_t (&v)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = 0;
 }
 
 // The magnitudes alone (a call that wants a maximum but no codes).
@@ -460,10 +467,6 @@ glu_kernel(const __grid_constant__ GluMaps maps, const GluArgs p) {
                         uint32_t g[16], u[16], a[8];
                         tmem_ld_2x16_sync(taddr + c * 32 + half * 16, taddr + C::OUT + c * 32 + half * 16, g, u);
                         if (half == 1 && last) release();
-                        if ((half == 1 && !whole) || !in) {  // (not the gate's columns; no rows of x)
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) g[j] = u[j] = 0;
-                        }
                         switch (p.act) {
                             case FP8Q_ACT_IDENTITY: glu_products<FP8Q_ACT_IDENTITY>(g, u, inv, a); break;
                             case FP8Q_ACT_RELU: glu_products<FP8Q_ACT_RELU>(g, u, inv, a); break;
@@ -471,6 +474,7 @@ glu_kernel(const __grid_constant__ GluMaps maps, const GluArgs p) {
                             case FP8Q_ACT_SILU: glu_products<FP8Q_ACT_SILU>(g, u, inv, a); break;
                             default: glu_products<FP8Q_ACT_GELU>(g, u, inv, a); break;
                         }
+                        if (!ok) none(a);
                         if (p.o) {
                             uint32_t hv[8];
                             uint16_t* at = p.o + row * 2 * p.F + col;
@@ -486,10 +490,6 @@ glu_kernel(const __grid_constant__ GluMaps maps, const GluArgs p) {
                         uint32_t r[16], g[8], u[8], dg[8], du[8];
                         tmem_ld_x16_sync(taddr + c * 32 + half * 16, r);
                         if (half == 1 && last) release();
-                        if (!in) {  // (no rows of dY: g and u are zeros, but NaN times zero is none)
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) r[j] = 0;
-                        }
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
                             const int at = ((2 * half + k) ^ ((lane >> 1) & 3)) << 4;
@@ -507,6 +507,10 @@ glu_kernel(const __grid_constant__ GluMaps maps, const GluArgs p) {
                             case FP8Q_ACT_RELU2: glu_gradients<FP8Q_ACT_RELU2>(r, inv, g, u, dg, du); break;
                             case FP8Q_ACT_SILU: glu_gradients<FP8Q_ACT_SILU>(r, inv, g, u, dg, du); break;
                             default: glu_gradients<FP8Q_ACT_GELU>(r, inv, g, u, dg, du); break;
+                        }
+                        if (!ok) {
+                            none(dg);
+                            none(du);
                         }
                         if (p.o && ok) {
                             uint16_t* at = p.o + row * 2 * p.F + col;
