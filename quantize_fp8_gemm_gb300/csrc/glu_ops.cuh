@@ -76,7 +76,11 @@ __device__ __forceinline__ void glu_act_grad(f32x2 g, f32x2& f, f32x2& d) {
         const f32x2 s = sigma2<ACT>(g);
         f = mul2(g, s);
         f32x2 rest = fma2(s, twice(-1.0f), twice(1.0f));
-        if constexpr (ACT == FP8Q_ACT_GELU) rest = mul2(rest, fma2(mul2(g, g), twice(3.0f * kGelu2CB), twice(kGelu2C)));
+        if constexpr (ACT == FP8Q_ACT_GELU) {
+            // (g^2 held at 2^100: of larger gates, whose squares leave float32, 1 - sigma or f is 0, and 0 times z' has to be)
+            const float2 gg = split(mul2(g, g));
+            rest = mul2(rest, fma2(pair_of(fminf(gg.x, 0x1p100f), fminf(gg.y, 0x1p100f)), twice(3.0f * kGelu2CB), twice(kGelu2C)));
+        }
         d = fma2(f, rest, s);
     }
 }

@@ -60,3 +60,26 @@ def test_scales_whose_product_underflows(B, M, F, K):
     h, dh = torch.ones(M, 2 * F, dtype=BF, device="cuda"), torch.empty(M, 2 * F, dtype=BF, device="cuda")
     B.fp8_gemm_dgrad_glu(x, w[:F], tiny, tiny, h, act=R.ACTS["identity"], dh=dh, amax_out=amax)
     assert bool((dh == float("inf")).all()) and float(amax) == float("inf")
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_the_derivative_far_from_zero_is_one_or_zero(B, act):
+    """Finite gates up to BF16's end, past where their squares leave float32: act(g) = g and act'(g) = 1 above,
+    0 and 0 below, so the gradient has the bits of the identity's, or is zero."""
+    M, F, N = 40, 80, 64
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    dy, w = positive(gen, M, N, 0x30), positive(gen, F, N, 0x30)
+    h = torch.randn(M, 2 * F, generator=gen, device="cuda").to(BF)
+    far = torch.tensor([1e4, 1e10, 1.8e19, 1.9e19, 1e20, 1e30, 3.38e38], device="cuda")
+    g = torch.cat([far, -far]).repeat(6)[:F].to(BF)
+    assert bool(torch.isfinite(g).all())
+    h[:, :F] = g
+    dh, same = torch.empty(M, 2 * F, dtype=BF, device="cuda"), torch.empty(M, 2 * F, dtype=BF, device="cuda")
+    amax, scale = cell(0), cell(1e3)
+    B.fp8_gemm_dgrad_glu(dy, w, scale, scale, h, act=R.ACTS[act], dh=dh, amax_out=amax)
+    B.fp8_gemm_dgrad_glu(dy, w, scale, scale, h, act=R.ACTS["identity"], dh=same)
+    up = (g > 0).repeat(2)
+    assert bool(torch.isfinite(same).all())
+    assert torch.equal(dh[:, up], same[:, up])
+    assert bool((dh[:, ~up] == 0).all())
+    assert float(amax) == float(dh.abs().max())
