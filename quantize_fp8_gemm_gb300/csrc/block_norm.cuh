@@ -567,6 +567,10 @@ __global__ void __launch_bounds__(C >= 3 ? 256 : 512, 1)
 bn_bwd_kernel(const BnBwd<T> p, int team) {
     extern __shared__ uint4 s_ring[];
     __shared__ float s_sum[2][2][16];
+    // dalpha's by warp: cells of their own, since a CTA of the cluster that is late may still read its last row's
+    // sum from s_sum (nothing orders that before this CTA's end where a row has one sum).  32 of them, so that the
+    // ring behind starts on a 128-byte line (off one, 8192 x 16384 499 us, on it 459).
+    __shared__ float s_alpha[ALPHA ? 32 : 1];
     constexpr int V = 16 / sizeof(T), H = V / 2, S = bn_bwd_stages(ALPHA), TENSORS = ALPHA ? 5 : 4;
     constexpr bool kWarp = MODE == BN_NARROW;
     constexpr int kTensor = bn_slots(C, SHIFT, kWarp && C == 1), kStage = TENSORS * kTensor;
@@ -798,14 +802,14 @@ bn_bwd_kernel(const BnBwd<T> p, int team) {
         }
         if constexpr (ALPHA) {
             float a = team_sum<false>(fold(dalpha2), 32);
-            if (lane == 0) s_sum[0][0][warp] = a;
+            if (lane == 0) s_alpha[warp] = a;
             if constexpr (MODE == BN_CLUSTER) cluster_sync_all();
             else __syncthreads();
             if (threadIdx.x == 0 && rank == 0) {
                 a = 0.0f;
                 for (uint32_t r = 0; r < ctas; ++r)
                     for (int k = 0; k < nw; ++k)
-                        a += MODE == BN_CLUSTER ? ld_cluster_f32(mapa_shared(smem_u32(&s_sum[0][0][k]), r)) : s_sum[0][0][k];
+                        a += MODE == BN_CLUSTER ? ld_cluster_f32(mapa_shared(smem_u32(&s_alpha[k]), r)) : s_alpha[k];
                 p.part[int64_t(p.parts) * 2 * p.N + block] = a;
             }
         }
