@@ -517,14 +517,23 @@ def _dtype_code(t, name: str) -> int:
 
 
 # The checks below ask a good tensor as little as they can (an attribute is 70 to 100 ns on the Grace host, and a
-# call has a dozen tensors); what is wrong with a bad one is found out afterwards.
-def _rows(t, M: int, N: int, dtype, name: str):
+# call has a dozen tensors); what is wrong with a bad one is found out afterwards.  `dev`: the device that the call
+# runs on, for calls that ask for all their tensors to be there.
+def _placed(t, name: str, dev) -> None:
+    """Refuse what is no CUDA tensor, or one of another device than `dev`."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if dev is not None and t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+
+
+def _rows(t, M: int, N: int, dtype, name: str, dev=None):
     """(device pointer, row stride) of an optional [M,N] CUDA tensor of one type whose rows are N
     adjacent elements."""
     if t is None:
         return None, 0
     try:
-        if t.is_cuda and t.dtype is dtype and t.shape == (M, N):
+        if (t.is_cuda if dev is None else t.get_device() == dev) and t.dtype is dtype and t.shape == (M, N):
             ld, inner = t.stride()
             if M <= 1:
                 ld = N
@@ -533,24 +542,22 @@ def _rows(t, M: int, N: int, dtype, name: str):
             raise ValueError(f"{name} needs rows of adjacent elements that do not overlap (strides {(ld, inner)})")
     except AttributeError:
         pass
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
+    _placed(t, name, dev)
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
     raise ValueError(f"{name} is {list(t.shape)}, the call needs {[M, N]}")
 
 
-def _vec(t, n: int, dtype, name: str):
+def _vec(t, n: int, dtype, name: str, dev=None):
     """Device pointer of an optional packed CUDA vector of n elements of one type."""
     if t is None:
         return None
     try:
-        if t.is_cuda and t.dtype is dtype and t.numel() == n and t.is_contiguous():
+        if (t.is_cuda if dev is None else t.get_device() == dev) and t.dtype is dtype and t.numel() == n and t.is_contiguous():
             return t.data_ptr()
     except AttributeError:
         pass
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
+    _placed(t, name, dev)
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
     raise ValueError(f"{name} must hold {n} packed elements")
@@ -561,66 +568,62 @@ def _rng(t):
     return _vec(t, 2, torch.int64, "rng")
 
 
-def _cell(t, dtype, name: str):
+def _cell(t, dtype, name: str, dev=None):
     """Device pointer of an optional CUDA tensor whose first element a call uses."""
     if t is None:
         return None
     try:
-        if t.is_cuda and t.dtype is dtype and t.numel():
+        if (t.is_cuda if dev is None else t.get_device() == dev) and t.dtype is dtype and t.numel():
             return t.data_ptr()
     except AttributeError:
         pass
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
+    _placed(t, name, dev)
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
     raise ValueError(f"{name} is empty")
 
 
-def _codes(t, n: int):
+def _codes(t, n: int, dev=None):
     """Device pointer of an optional packed CUDA tensor of n one-byte codes."""
     if t is None:
         return None
     try:
-        if t.is_cuda and t.nbytes == n == t.numel() and t.is_contiguous():
+        if (t.is_cuda if dev is None else t.get_device() == dev) and t.nbytes == n == t.numel() and t.is_contiguous():
             return t.data_ptr()
     except AttributeError:
         pass
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError("q_out must be a CUDA tensor")
+    _placed(t, "q_out", dev)
     raise ValueError(f"q_out must hold {n} packed one-byte codes")
 
 
-def _buffer(t):
+def _buffer(t, dev):
     """Device pointer of a packed CUDA workspace."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError("workspace must be a CUDA tensor")
+    _placed(t, "workspace", dev)
     if not t.is_contiguous():
         raise ValueError("workspace must be contiguous")
     return t.data_ptr()
 
 
-def _packed(t, rows: int, cols: int, dtype, name: str):
+def _packed(t, rows: int, cols: int, dtype, name: str, dev):
     """Device pointer of an optional packed [rows, cols] CUDA tensor of a type (None: one-byte codes)."""
     if t is None:
         return None
     try:
-        if t.is_cuda and (t.dtype is dtype or dtype is None and t.element_size() == 1) and t.shape == (rows, cols) \
+        if t.get_device() == dev and (t.dtype is dtype or dtype is None and t.element_size() == 1) and t.shape == (rows, cols) \
                 and t.is_contiguous():
             return t.data_ptr()
     except AttributeError:
         pass
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
+    _placed(t, name, dev)
     if t.element_size() != 1 if dtype is None else t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype or 'one-byte codes'}, not {t.dtype}")
     raise ValueError(f"{name} must be packed {[rows, cols]}, not {list(t.shape)} with strides {t.stride()}")
 
 
-def _here(t, name: str) -> None:
-    """The call runs on the current device: its tensors have to be there."""
-    if isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() != torch._C._cuda_getDevice():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch._C._cuda_getDevice()}")
+def _device(t, name: str) -> int:
+    """The device that a call on the CUDA tensor t runs on: the current one."""
+    _placed(t, name, None)
+    return torch._C._cuda_getDevice()
 
 
 def _param_code(x, weight, bias, code: int):
@@ -743,22 +746,22 @@ def block_norm_fwd(x: torch.Tensor, weight, y, *, eps: float = 1e-5, rstd=None, 
     gate [M] and alpha [1]: float32, or None.  y None without codes: r_out alone."""
     code, dtype = _dtype_code(x, "x"), x.dtype
     M, N = x.shape
-    _here(x, "x")
-    px, ldx = _rows(x, M, N, dtype, "x")
-    pres, ldres = _rows(residual, M, N, dtype, "residual")
-    pr, ldr = _rows(r_out, M, N, dtype, "r_out")
-    py, ldy = _rows(y, M, N, dtype, "y")
+    dev = _device(x, "x")
+    px, ldx = _rows(x, M, N, dtype, "x", dev)
+    pres, ldres = _rows(residual, M, N, dtype, "residual", dev)
+    pr, ldr = _rows(r_out, M, N, dtype, "r_out", dev)
+    py, ldy = _rows(y, M, N, dtype, "y", dev)
     pcode, ptype = _param_code(x, weight, post_weight, code)
     f32 = torch.float32
     args = _block_norm.pack(
         M, N, code, pcode, px or 0, ldx, pres or 0, ldres, pr or 0, ldr, py or 0, ldy,
-        0 if weight is None else _vec(weight, N, ptype, "weight"),
-        0 if post_weight is None else _vec(post_weight, N, ptype, "post_weight"),
-        0 if gate is None else _vec(gate, M, f32, "gate"), 0 if alpha is None else _cell(alpha, f32, "alpha"),
-        0 if rstd is None else _vec(rstd, M, f32, "rstd"), 0 if rstd_post is None else _vec(rstd_post, M, f32, "rstd_post"),
-        0 if scale is None else _cell(scale, f32, "scale"), 0 if q_out is None else _codes(q_out, M * N),
-        0 if amax_out is None else _cell(amax_out, f32, "amax_out"),
-        0 if sat_count is None else _cell(sat_count, torch.int64, "sat_count"), eps, fmt, bool(post_norm), flags)
+        0 if weight is None else _vec(weight, N, ptype, "weight", dev),
+        0 if post_weight is None else _vec(post_weight, N, ptype, "post_weight", dev),
+        0 if gate is None else _vec(gate, M, f32, "gate", dev), 0 if alpha is None else _cell(alpha, f32, "alpha", dev),
+        0 if rstd is None else _vec(rstd, M, f32, "rstd", dev), 0 if rstd_post is None else _vec(rstd_post, M, f32, "rstd_post", dev),
+        0 if scale is None else _cell(scale, f32, "scale", dev), 0 if q_out is None else _codes(q_out, M * N, dev),
+        0 if amax_out is None else _cell(amax_out, f32, "amax_out", dev),
+        0 if sat_count is None else _cell(sat_count, torch.int64, "sat_count", dev), eps, fmt, bool(post_norm), flags)
     _check("block_norm_fwd", lib().block_norm_fwd(args, _stream(stream)))
 
 
@@ -776,26 +779,26 @@ def block_norm_bwd(dy, r, rstd, weight, *, dr=None, x=None, residual=None, alpha
     first, name = (dy, "dy") if dy is not None else (dr, "dr")
     code, dtype = _dtype_code(first, name), first.dtype
     M, N = first.shape
-    _here(first, name)
-    pdy, lddy = _rows(dy, M, N, dtype, "dy")
-    pr, ldr = _rows(r, M, N, dtype, "r")
-    pdr, lddr = _rows(dr, M, N, dtype, "dr")
-    px, ldx = _rows(x, M, N, dtype, "x")
-    pres, ldres = _rows(residual, M, N, dtype, "residual")
-    pdres, lddres = _rows(dresidual, M, N, dtype, "dresidual")
-    pdx, lddx = _rows(dx, M, N, dtype, "dx")
+    dev = _device(first, name)
+    pdy, lddy = _rows(dy, M, N, dtype, "dy", dev)
+    pr, ldr = _rows(r, M, N, dtype, "r", dev)
+    pdr, lddr = _rows(dr, M, N, dtype, "dr", dev)
+    px, ldx = _rows(x, M, N, dtype, "x", dev)
+    pres, ldres = _rows(residual, M, N, dtype, "residual", dev)
+    pdres, lddres = _rows(dresidual, M, N, dtype, "dresidual", dev)
+    pdx, lddx = _rows(dx, M, N, dtype, "dx", dev)
     pcode, ptype = _param_code(first, weight, post_weight, code)
     f32 = torch.float32
     args = _block_norm_bwd.pack(
         M, N, code, pcode, pdy or 0, lddy, pr or 0, ldr, pdr or 0, lddr, px or 0, ldx, pres or 0, ldres, pdres or 0, lddres,
-        pdx or 0, lddx, 0 if weight is None else _vec(weight, N, ptype, "weight"),
-        0 if post_weight is None else _vec(post_weight, N, ptype, "post_weight"),
-        0 if gate is None else _vec(gate, M, f32, "gate"), 0 if alpha is None else _cell(alpha, f32, "alpha"),
-        0 if rstd is None else _vec(rstd, M, f32, "rstd"), 0 if rstd_post is None else _vec(rstd_post, M, f32, "rstd_post"),
-        0 if dweight is None else _vec(dweight, N, f32, "dweight"),
-        0 if dpost_weight is None else _vec(dpost_weight, N, f32, "dpost_weight"),
-        0 if dgate is None else _vec(dgate, M, f32, "dgate"), 0 if dalpha is None else _cell(dalpha, f32, "dalpha"),
-        0 if workspace is None else _buffer(workspace), 0 if workspace is None else workspace.nbytes, bool(post_norm), flags)
+        pdx or 0, lddx, 0 if weight is None else _vec(weight, N, ptype, "weight", dev),
+        0 if post_weight is None else _vec(post_weight, N, ptype, "post_weight", dev),
+        0 if gate is None else _vec(gate, M, f32, "gate", dev), 0 if alpha is None else _cell(alpha, f32, "alpha", dev),
+        0 if rstd is None else _vec(rstd, M, f32, "rstd", dev), 0 if rstd_post is None else _vec(rstd_post, M, f32, "rstd_post", dev),
+        0 if dweight is None else _vec(dweight, N, f32, "dweight", dev),
+        0 if dpost_weight is None else _vec(dpost_weight, N, f32, "dpost_weight", dev),
+        0 if dgate is None else _vec(dgate, M, f32, "dgate", dev), 0 if dalpha is None else _cell(dalpha, f32, "dalpha", dev),
+        0 if workspace is None else _buffer(workspace, dev), 0 if workspace is None else workspace.nbytes, bool(post_norm), flags)
     _check("block_norm_bwd", lib().block_norm_bwd(args, _stream(stream)))
 
 
@@ -833,17 +836,17 @@ def fp8_glu_fwd(x_q: torch.Tensor, w1t_q: torch.Tensor, scale_x: torch.Tensor, s
     F = rows // 2
     if rows != 2 * F:
         raise ValueError(f"w1t_q has {rows} rows: the gate's and as many of the up-projection")
-    _here(x_q, "x_q")
+    dev = _device(x_q, "x_q")
     bf, f32 = torch.bfloat16, torch.float32
     args = _glu.pack(
-        _packed(x_q, M, K, None, "x_q"), _packed(w1t_q, rows, K, None, "w1t_q"), _cell(scale_x, f32, "scale_x") or 0,
-        _cell(scale_w, f32, "scale_w") or 0, 0 if h_out is None else _packed(h_out, M, rows, bf, "h_out"),
-        0 if act_out is None else _packed(act_out, M, F, bf, "act_out"),
-        0 if scale_a is None else _cell(scale_a, f32, "scale_a"), 0 if a_q is None else _packed(a_q, M, F, None, "a_q"),
-        0 if a_q_t is None else _packed(a_q_t, F, M, None, "a_q_t"),
-        0 if amax_out is None else _cell(amax_out, f32, "amax_out"),
-        0 if sat_count is None else _cell(sat_count, torch.int64, "sat_count"), M, F, K, act, flags,
-        0 if status is None else _cell(status, torch.int32, "status"))
+        _packed(x_q, M, K, None, "x_q", dev), _packed(w1t_q, rows, K, None, "w1t_q", dev), _cell(scale_x, f32, "scale_x", dev) or 0,
+        _cell(scale_w, f32, "scale_w", dev) or 0, 0 if h_out is None else _packed(h_out, M, rows, bf, "h_out", dev),
+        0 if act_out is None else _packed(act_out, M, F, bf, "act_out", dev),
+        0 if scale_a is None else _cell(scale_a, f32, "scale_a", dev), 0 if a_q is None else _packed(a_q, M, F, None, "a_q", dev),
+        0 if a_q_t is None else _packed(a_q_t, F, M, None, "a_q_t", dev),
+        0 if amax_out is None else _cell(amax_out, f32, "amax_out", dev),
+        0 if sat_count is None else _cell(sat_count, torch.int64, "sat_count", dev), M, F, K, act, flags,
+        0 if status is None else _cell(status, torch.int32, "status", dev))
     _check("fp8_glu_fwd", lib().fp8_glu_fwd(args, _stream(stream)))
 
 
@@ -857,17 +860,17 @@ def fp8_gemm_dgrad_glu(dy_q: torch.Tensor, w2_q: torch.Tensor, scale_dy: torch.T
         raise TypeError("dy_q and w2_q must be 2-dimensional CUDA tensors")
     M, N = dy_q.shape
     F = w2_q.shape[0]
-    _here(dy_q, "dy_q")
+    dev = _device(dy_q, "dy_q")
     bf, f32 = torch.bfloat16, torch.float32
     args = _glu.pack(
-        _packed(dy_q, M, N, None, "dy_q"), _packed(w2_q, F, N, None, "w2_q"), _cell(scale_dy, f32, "scale_dy") or 0,
-        _cell(scale_w, f32, "scale_w") or 0, _packed(h, M, 2 * F, bf, "h") or 0,
-        0 if dh is None else _packed(dh, M, 2 * F, bf, "dh"), 0 if scale_dh is None else _cell(scale_dh, f32, "scale_dh"),
-        0 if dh_q is None else _packed(dh_q, M, 2 * F, None, "dh_q"),
-        0 if dh_q_t is None else _packed(dh_q_t, 2 * F, M, None, "dh_q_t"),
-        0 if amax_out is None else _cell(amax_out, f32, "amax_out"),
-        0 if sat_count is None else _cell(sat_count, torch.int64, "sat_count"), M, N, F, act, flags,
-        0 if status is None else _cell(status, torch.int32, "status"))
+        _packed(dy_q, M, N, None, "dy_q", dev), _packed(w2_q, F, N, None, "w2_q", dev), _cell(scale_dy, f32, "scale_dy", dev) or 0,
+        _cell(scale_w, f32, "scale_w", dev) or 0, _packed(h, M, 2 * F, bf, "h", dev) or 0,
+        0 if dh is None else _packed(dh, M, 2 * F, bf, "dh", dev), 0 if scale_dh is None else _cell(scale_dh, f32, "scale_dh", dev),
+        0 if dh_q is None else _packed(dh_q, M, 2 * F, None, "dh_q", dev),
+        0 if dh_q_t is None else _packed(dh_q_t, 2 * F, M, None, "dh_q_t", dev),
+        0 if amax_out is None else _cell(amax_out, f32, "amax_out", dev),
+        0 if sat_count is None else _cell(sat_count, torch.int64, "sat_count", dev), M, N, F, act, flags,
+        0 if status is None else _cell(status, torch.int32, "status", dev))
     _check("fp8_gemm_dgrad_glu", lib().fp8_gemm_dgrad_glu(args, _stream(stream)))
 
 
