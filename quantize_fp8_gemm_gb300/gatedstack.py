@@ -4,7 +4,7 @@
 
 Norms are root-mean-square ones; W1 = [Wg | Wu] is one matrix, so its gradient and its input's are
 those of a linear layer.  Products run on the FP8 GEMMs with delayed per-tensor scales as in
-``Fp8MlpStack``, and between two of them the data is passed over once:
+``Fp8MlpStack``; in the forward pass the data is passed over once between two of them:
 
     block_norm_fwd      the sub-layer's end below (norm, gate, residual), the norm before this
                         block, and the E4M3 codes that the projections read
@@ -14,8 +14,10 @@ those of a linear layer.  Products run on the FP8 GEMMs with delayed per-tensor 
 
 and back: block_norm_bwd, the branch gradient's cast, fp8_gemm_dgrad_glu (whose epilogue writes the
 projections' gradients as E5M2 codes in both layouts: they never exist in BF16), the weight
-gradients, fp8_gemm_dgrad, block_norm_bwd.  Nothing of a step's state is on the host: a CUDA graph may
-hold any number of steps, and its replays may mix with eager ones.
+gradients, fp8_gemm_dgrad, block_norm_bwd.  Two passes there stand by themselves: the cast of the branch
+gradient, which block_norm_bwd writes in BF16, and that of the norm's output into the transposed codes that
+W1's gradient reads, for which the forward keeps it in BF16.  Nothing of a step's state is on the host: a
+CUDA graph may hold any number of steps, and its replays may mix with eager ones.
 """
 from __future__ import annotations
 
