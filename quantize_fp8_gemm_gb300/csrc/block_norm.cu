@@ -40,7 +40,10 @@ namespace {
 
 // Rows wider than the one-pass kernels take: one CTA a row, in passes over it (the later ones
 // from L1 / L2).  The row is formed again in every pass and written in the last, element by
-// element by the thread that read it, so an output may replace an input.
+// element by the thread that read it, so an output may replace an input.  Far from any bound of the hardware (of
+// the copy rate: forward bf16 4096 x 20001 542 us, 0.18, 1024 x 65536 638, 0.12; float32 688, 0.28, and 665, 0.24;
+// backward, which comes here past 65536 two-byte or 32768 four-byte columns, bf16 1024 x 100000 3.2 ms, 0.06, float32
+// 2.6 ms, 0.14); no counters were taken, the code loads single elements and keeps its column sums in memory.
 template <typename T>
 __device__ __forceinline__ float bn_stream(const BnFwd<T>& p, int64_t row, int64_t j, float rp, float gate, float alpha) {
     float v = __fmul_rn(__fmul_rn(__fmul_rn(to_f32(p.x[row * p.ldx + j]), rp), p.wp.at(j)), gate);

@@ -350,8 +350,9 @@ __host__ __device__ constexpr int bn_slots(int C, bool shift, bool rows) { retur
 // Weights: in registers up to 32 columns a lane, in shared memory above.
 // What bounds it: memory on the 16-byte grid (bf16 131072 x 1600 with codes 302 to 316 us, 0.92 to 0.88 of the
 // measured copy rate; 65536 x 768 69 us, 0.86; 8192 x 16384 160 to 180 us, 0.99 to 0.88); off it memory for
-// float32 (65536 x 1001 175 us, 0.88) and the words' instructions for bf16 (65536 x 1601 222 us, 0.56); for one
-// row the launch.
+// float32 (65536 x 1001 175 us, 0.88) and the words' instructions for bf16 (65536 x 1601 222 us, 0.56; narrow rows
+// also leave lanes of their last piece idle, and codes go byte by byte: 333 columns 55 us, 0.47, with codes 70,
+// 0.42, 99 columns 24 us, 0.32); for one row the launch.
 template <typename T, int C, bool CTA, bool SHIFT, int S>
 __global__ void __launch_bounds__(CTA ? 512 : 128)
 bn_fwd_kernel(const BnFwd<T> p, int team) {
@@ -556,8 +557,9 @@ cudaError_t launch_bn_fwd_as(const BnFwd<T>& p, int team, unsigned block, cudaSt
 // What bounds it: memory where the rows are on the grid and fill the lanes (bf16 65536 x 2048 239 us,
 // 1.00 of the measured copy rate; 131072 x 1600 400 us, 0.93; fp32 65536 x 1600 355 us, 1.04); off it the
 // instructions that cut words and shift them back (bf16 65536 x 1601 366 us, 0.51; fp32, which has none to cut,
-// 65536 x 1001 240 us, 0.97); rows over a cluster (8192 x 16384 417 us, 0.57) wait at the cluster's barriers
-// for the stores before them.
+// 65536 x 1001 240 us, 0.97; bf16 333 columns 79 us, 0.49, 99 columns 39 us, 0.30); rows over a cluster (8192 x 16384
+// 419 us, 0.57; 12288 columns 383, 0.46; float32 8192 columns 382, 0.62, off the grid 16384 x 5001 738, 0.39) wait
+// at the cluster's barriers for the stores before them.
 enum BnMode { BN_NARROW, BN_WIDE, BN_CLUSTER };
 constexpr int bn_bwd_stages(bool alpha) { return alpha ? 2 : 3; }
 enum { IN_DY, IN_R, IN_DR, IN_X, IN_RES };

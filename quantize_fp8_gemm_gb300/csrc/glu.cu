@@ -25,13 +25,13 @@
 // of g and u come by TMA into a buffer a warp, the next one asked for as soon as this one is in
 // registers (32-byte loads straight into registers, 32 sectors an instruction, took 680 us).
 //
-// What bounds it (GB300).  32768 x 1600 -> 6400 forward with h_out and both code layouts 473 us, 2.84
-// PFLOP/s (one code layout alone 400 us, 3.36; the plain GEMM of the same product 423): the L1-to-L2 request
-// path (69 % busy at 8192 rows) beside the tensor pipe (68 % of its cycles);
-// sustained for half a second the 1400 W cap holds the SMs at 1470 MHz and it takes 555.  Backward with
-// both code layouts 387 us, 4.5 TB/s: neither memory (DRAM at 47 % of its peak at 8192 rows) nor the tensor pipe
-// (37 %); instructions, 18 an element of dA, issue in 46 % of the cycles from at most 4.5 warps a scheduler, and
-// the 96 registers that 18 warps leave a thread spill 48 bytes.  A few tokens (1 to 128 x 1600 -> 6400, 20.5 MB of
+// What bounds it (GB300).  32768 x 1600 -> 6400 forward with h_out and both code layouts 471 to 490 us, 2.8
+// PFLOP/s (one code layout alone 400 us, 3.36; the plain GEMM of the same product 423): busiest are the L1-to-L2
+// request path (69 % at 8192 rows) and the tensor pipe (68 % of its cycles), so neither is a limit yet;
+// sustained for half a second the 1400 W cap holds the SMs at 1470 MHz and it takes 540 to 566.  Backward with
+// both code layouts 389 to 393 us (GELU 415), 4.4 TB/s: neither memory (DRAM at 44 % of its peak at 8192 rows) nor
+// the tensor pipe (37 %); instructions, 18 an element of dA, issue in 46 % of the cycles from at most 4.5 warps a
+// scheduler, and the 96 registers that 18 warps leave a thread spill 48 bytes.  A few tokens (1 to 128 x 1600 -> 6400, 20.5 MB of
 // weights): 7.5 us with the clearing launch, 13 k-blocks one after another in each of 100 CTAs.
 // Not kept: h_out through shared memory in 64-column boxes (508 us: two ring stages less), adjacent instead of
 // alternate chunks a warp (backward 417), a kernel of dot products for one or two rows (7.6 and 9.8).
