@@ -30,7 +30,10 @@ case for counter captures); `--profile` runs a few eager steps only, without
 timing, for `ncu` (with `--mx` the MXFP8 path, with `--group` the 1x128 /
 128x128 group-scaled path, with `--unfused` the two-launch path).
 
-Prints one JSON line on rank 0.
+Prints one JSON line on rank 0: the metric, its configuration, the dominant kernel's
+roofline, clocks, `e2e` and the CPU baseline, short enough for a log that keeps the
+last 3000 characters.  The same with everything else (each kernel's time and
+roofline, `extras`) goes to standard error as one line after "details: ".
 """
 from __future__ import annotations
 
@@ -441,6 +444,18 @@ def rooflines(w, kern_ms: dict, peaks: dict, fp8: dict, workload_key: str, step_
     return out
 
 
+# what of a run's record is printed on standard output
+PRINTED = ("metric", "value", "unit", "n_gpus", "steps", "warmup", "ms_per_step", "higher_is_better", "scaling", "vs_baseline",
+           "dtype", "data", "config", "quant_hbm_gbs", "gemm_tflops", "roofline", "cpu_baseline", "e2e", "gpu_launches", "clocks")
+
+
+def printed_line(line: dict) -> dict:
+    """The part of a run's record that fits one short line; where times and peaks come from is in the details."""
+    out = {k: line[k] for k in PRINTED}
+    out["roofline"] = {k: v for k, v in line["roofline"].items() if k not in ("duration_source", "peak_source")}
+    return out
+
+
 def measure_step(w, dev, steps: int, warmup: int, flush, eager: bool = False, group: bool = False):
     """Build the step's state for workload w, calibrate, capture the step as CUDA
     graphs, run `warmup` untimed steps and time `steps` steps (L2 flushed before
@@ -624,7 +639,8 @@ def run_ours(args, world, rank, local):
         "wall_s_timed_loop": wall,
         "extras": extras,
     }
-    print(json.dumps(line), flush=True)
+    print("details: " + json.dumps(line), file=sys.stderr, flush=True)
+    print(json.dumps(printed_line(line)), flush=True)
 
 
 def measure_other_config(name: str, dev, flush, fp8: dict, peaks: dict, steps: int, group: bool = False) -> dict:
