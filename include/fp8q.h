@@ -903,7 +903,8 @@ int fp8_gemm_dgrad_glu(const fp8q_dgrad_glu_args* args, cudaStream_t stream);
  * The norm before the next block is that of the stored r (rounded to T).  Without
  * residual, gate, post_weight and post_norm r is x itself: the norm before the
  * first block; without y, q_out, rstd, amax_out and sat_count only r is formed:
- * the end of the last.  Sums are float32: a row whose squares add up past its
+ * the end of the last.  Sums are float32, in a fixed order that depends on N, the
+ * types and the tensors' alignment: a row whose squares add up past float32's
  * largest value (3.4e38) gets a statistic of 0; with eps = 0 a row of zeros gives
  * NaNs.  An infinity or NaN stays in its row (and makes amax a NaN or infinite).
  *   dtype, param_dtype   x, residual, r_out, y; weight and post_weight: FP8Q_FP32 or
